@@ -514,6 +514,120 @@ int ffn24_step(const p24_ffn_args* a, void* workspace, size_t ws_bytes, void* st
 int ffn24_step_traced(const p24_ffn_args* a, void* workspace, size_t ws_bytes, void* stream,
                       void* const* events, int n_events);
 
+/*
+ * The language-model head's row operators. Logits z are a matrix [T, V] (T token
+ * positions, V vocabulary entries), bf16 or fp32, row stride ldz >= V in elements. Unlike
+ * the GEMMs' matrices they need no 16-byte alignment: any vocabulary size and any stride
+ * that is a multiple of the element will do (rows are read in aligned 16-byte pieces and
+ * their ends element by element). Sums and statistics are fp32 and are added in a fixed
+ * order: repeated calls are bit-identical.
+ *
+ * A logit of -inf is masked: probability 0, gradient 0. A row of nothing else has no
+ * distribution: log probabilities -inf, entropy 0, losses +inf, gradients 0. A row with a
+ * NaN or +inf gives NaN. Logits of the type's lowest finite value are ordinary numbers.
+ */
+typedef enum { P24_BF16 = 0, P24_F32 = 1 } p24_dtype;
+
+#define P24_TOPK_MAX 128 /* longest list of alternatives or of teacher entries per row */
+
+/*
+ * p24_token_logprobs -- for each row, at a temperature tau, with
+ * p = softmax(z / tau), m = max z and s = sum exp((z - m) / tau):
+ *   logp    : fp32 [T], ln p[tokens[t]] = (z - m) / tau - ln s; 0 where the token is outside
+ *             0..V-1 (padding).
+ *   entropy : fp32 [T], -sum p ln p.
+ *   stats   : fp32 [T, 2], m and ln s (what the backward reads; m / tau + ln s is the
+ *             log-sum-exp).
+ *   top_logp, top_idx : fp32 and int32 [T, k], the k most probable entries in falling
+ *             order, ties to the lower index, NaN above +inf, -0 equal to +0; the places
+ *             past V hold -inf and -1. As a teacher's list these go to p24_distill_topk.
+ * Each output may be NULL (top_logp and top_idx go together, with k = 0); logp needs tokens.
+ *
+ * p24_token_logprobs_bwd -- the gradient of logp and entropy, from the forward's stats:
+ *   dlogits = ( dlogp (delta - p) - dentropy p (ln p + entropy) ) / tau
+ *   dlogp, dentropy : fp32 [T] upstream gradients; either may be NULL (then not part of
+ *             it). dlogp needs tokens, dentropy the forward's entropy.
+ *   dlogits : the logits' type, [T, V], row stride ldd >= V; it may be the logits
+ *             themselves (in place, ldd == ldz). The alternatives carry no gradient.
+ *
+ * tokens: int32 [T]. 1e-4 <= temperature <= 1e4. 0 <= k <= P24_TOPK_MAX and
+ * 1 <= V <= 2^30 (P24_EUNSUPPORTED beyond). Pointers are aligned to their element.
+ */
+typedef struct {
+  int64_t T, V, k;
+  int32_t dtype;
+  float temperature;
+  const void* logits;
+  int64_t ldz;
+  const int32_t* tokens;
+  float* logp;
+  float* entropy; /* written by the forward, read by the backward */
+  float* stats;   /* written by the forward, read by the backward */
+  float* top_logp;
+  int32_t* top_idx;
+  const float* dlogp;
+  const float* dentropy;
+  void* dlogits;
+  int64_t ldd;
+} p24_logprobs_args;
+
+int p24_token_logprobs(const p24_logprobs_args* a, void* stream);
+int p24_token_logprobs_bwd(const p24_logprobs_args* a, void* stream);
+
+/*
+ * p24_distill_topk -- the loss of a student's rows of logits against a teacher's top-K
+ * list (a pruned model recovering from its dense teacher), beside the label's cross
+ * entropy. The list of row t: columns top_idx[t, 0..K) (int32; one outside 0..V-1 is
+ * absent, the others of a row are distinct) with values top_val[t, 0..K) (fp32).
+ *   Without P24_DISTILL_TAIL the list is renormalised: q = softmax(top_val / tau) over it.
+ *     kl = sum_list q (ln q - ln p),            p = softmax(z / tau)
+ *   With P24_DISTILL_TAIL top_val are log probabilities at the temperature in use, and the
+ *   rest of the vocabulary is one bucket: q = exp(top_val), q_r = max(0, 1 - sum q),
+ *   p_r = the sum of p off the list.
+ *     kl = sum_list q (ln q - ln p) + q_r (ln q_r - ln p_r)
+ *   (0 ln 0 = 0; an empty list gives kl = 0; the bucket is dropped, q_r = 0, where every
+ *   logit off the list is -inf, as 1 - sum q would be a rounding residue there.)
+ *     ce = -ln softmax(z)[labels[t]], at temperature 1; 0 where the label is outside 0..V-1.
+ *   kl, ce : fp32 [T]; ce and labels may be NULL.
+ *   stats  : fp32 [T, 4], may be NULL: m = max z, and ln of the sums of exp((z - m) / tau)
+ *            over all, of the same off the list (tail; else 0), and of exp(z - m) (with
+ *            labels; else 0). The backward reads them.
+ * With dlogits the same call also writes the gradient, reading the logits once:
+ *   dlogits = dkl d(kl)/dz + dce d(ce)/dz
+ *   dkl, dce : fp32 [T], each row's weight in the loss (its upstream gradient); either may
+ *            be NULL (not part of it). dce needs labels.
+ *   dlogits  : the logits' type, row stride ldd >= V; it may be the logits (in place, ldd == ldz).
+ *
+ * p24_distill_topk_bwd -- that gradient alone, from the forward's stats (the list, labels,
+ * temperature and flags as there), where the weights are known only after the loss.
+ *
+ * 0 <= K <= P24_TOPK_MAX and 1 <= V <= 2^30, with P24_DISTILL_TAIL V <= 2^19
+ * (P24_EUNSUPPORTED beyond); 1e-4 <= temperature <= 1e4.
+ */
+#define P24_DISTILL_TAIL 0x1u
+
+typedef struct {
+  int64_t T, V, K;
+  int32_t dtype;
+  float temperature;
+  uint32_t flags;
+  const void* logits;
+  int64_t ldz;
+  const int32_t* top_idx;
+  const float* top_val;
+  const int32_t* labels;
+  float* kl;
+  float* ce;
+  float* stats;
+  const float* dkl;
+  const float* dce;
+  void* dlogits;
+  int64_t ldd;
+} p24_distill_args;
+
+int p24_distill_topk(const p24_distill_args* a, void* stream);
+int p24_distill_topk_bwd(const p24_distill_args* a, void* stream);
+
 /* Number of kernels this library has launched in this process (all devices). */
 uint64_t p24_launch_count(void);
 

@@ -24,6 +24,9 @@ P24_STEP_ACT24 = 0x1
 P24_STEP_KEEP_MASKS = 0x2
 P24_STEP_ADAPTERS = 0x4
 P24_STEP_VNM = 0x8
+P24_BF16, P24_F32 = 0, 1
+P24_TOPK_MAX = 128
+P24_DISTILL_TAIL = 0x1
 
 
 class P24Error(RuntimeError):
@@ -54,6 +57,22 @@ class p24_hybrid(C.Structure):
     _fields_ = [("rows", C.c_int64), ("cols", C.c_int64), ("E", C.c_int64), ("cap", C.c_int64),
                 ("nnz", C.c_void_p), ("ell_cols", C.c_void_p), ("ell_vals", C.c_void_p), ("slot", C.c_void_p),
                 ("ovf_rows", C.c_void_p), ("n_ovf", C.c_void_p), ("ovf", C.c_void_p), ("ldo", C.c_int64)]
+
+
+class p24_logprobs_args(C.Structure):
+    _fields_ = [("T", C.c_int64), ("V", C.c_int64), ("k", C.c_int64), ("dtype", C.c_int32),
+                ("temperature", C.c_float), ("logits", C.c_void_p), ("ldz", C.c_int64), ("tokens", C.c_void_p),
+                ("logp", C.c_void_p), ("entropy", C.c_void_p), ("stats", C.c_void_p), ("top_logp", C.c_void_p),
+                ("top_idx", C.c_void_p), ("dlogp", C.c_void_p), ("dentropy", C.c_void_p), ("dlogits", C.c_void_p),
+                ("ldd", C.c_int64)]
+
+
+class p24_distill_args(C.Structure):
+    _fields_ = [("T", C.c_int64), ("V", C.c_int64), ("K", C.c_int64), ("dtype", C.c_int32),
+                ("temperature", C.c_float), ("flags", C.c_uint32), ("logits", C.c_void_p), ("ldz", C.c_int64),
+                ("top_idx", C.c_void_p), ("top_val", C.c_void_p), ("labels", C.c_void_p), ("kl", C.c_void_p),
+                ("ce", C.c_void_p), ("stats", C.c_void_p), ("dkl", C.c_void_p), ("dce", C.c_void_p),
+                ("dlogits", C.c_void_p), ("ldd", C.c_int64)]
 
 
 def _load() -> C.CDLL:
@@ -91,6 +110,10 @@ def _load() -> C.CDLL:
         "hyb_compress": (i32, [vp, i64, C.POINTER(p24_hybrid), vp]),
         "hyb_spmm": (i32, [C.POINTER(p24_hybrid), vp, i64, i64, vp, i64, vp]),
         "hyb_sddmm": (i32, [C.POINTER(p24_hybrid), vp, i64, i64, vp, i64, vp, vp, i64, vp]),
+        "p24_token_logprobs": (i32, [C.POINTER(p24_logprobs_args), vp]),
+        "p24_token_logprobs_bwd": (i32, [C.POINTER(p24_logprobs_args), vp]),
+        "p24_distill_topk": (i32, [C.POINTER(p24_distill_args), vp]),
+        "p24_distill_topk_bwd": (i32, [C.POINTER(p24_distill_args), vp]),
         "p24_launch_count": (C.c_uint64, []),
         "p24_query_status": (i32, [vp]),
         "p24_query_timeout": (i32, [vp, C.POINTER(i64), C.POINTER(i64)]),
@@ -598,3 +621,123 @@ def hyb_sddmm(h: Hybrid, G: torch.Tensor, B: torch.Tensor, S_ell: torch.Tensor |
     _check(lib.hyb_sddmm(C.byref(hc), G.data_ptr(), N, ldg, B.data_ptr(), ldb, S_ell.data_ptr(), S_ovf.data_ptr(),
                          S_ovf.stride(0), _stream(stream)), "hyb_sddmm")
     return S_ell, S_ovf
+
+
+# ------------------------------------------------------------------ the language-model head's row operators
+_LOGIT_TYPES = {torch.bfloat16: P24_BF16, torch.float32: P24_F32}
+
+
+def _logits(t: torch.Tensor, name: str, like: torch.Tensor | None = None) -> tuple[int, int, int, int]:
+    """(T, V, row stride, dtype code) of a matrix of logits or of their gradient."""
+    if t.dtype not in _LOGIT_TYPES:
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    T, V, ld = _mat(t, t.dtype, name)
+    if like is not None and (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must have the logits' shape, type and device")
+    return T, V, ld, _LOGIT_TYPES[t.dtype]
+
+
+def _per_row(t: torch.Tensor | None, shape: tuple, dtype, name: str, device) -> int | None:
+    """Pointer of a contiguous per-row tensor (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {shape} tensor on the logits' device")
+    return t.data_ptr()
+
+
+def p24_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, k: int = 0,
+                       temperature: float = 1.0, entropy: bool = True, out: dict | None = None,
+                       stream=None) -> dict:
+    """Per row of logits [T, V] (bf16 or fp32), of softmax(logits / temperature): logp [T] of
+    tokens (int32 [T]; one outside 0..V-1 gives 0), entropy [T] (if asked for), the k most
+    probable entries top_logp, top_idx [T, k], and stats [T, 2] for the backward, as a dict.
+    out: tensors to write to, under those names. See include/prune24.h."""
+    T, V, ldz, dt = _logits(logits, "logits")
+    dev, f32 = logits.device, torch.float32
+    o = {} if out is None else dict(out)
+    want = [("stats", (T, 2), f32)]
+    if tokens is not None:
+        want.append(("logp", (T,), f32))
+    if entropy:
+        want.append(("entropy", (T,), f32))
+    if k > 0:
+        want += [("top_logp", (T, k), f32), ("top_idx", (T, k), torch.int32)]
+    a = p24_logprobs_args(T, V, k, dt, temperature, logits.data_ptr(), ldz,
+                          _per_row(tokens, (T,), torch.int32, "tokens", dev))
+    for name, shape, dtype in want:
+        if o.get(name) is None:
+            o[name] = torch.empty(shape, dtype=dtype, device=dev)
+        setattr(a, name, _per_row(o[name], shape, dtype, name, dev))
+    _check(lib.p24_token_logprobs(C.byref(a), _stream(stream)), "p24_token_logprobs")
+    return o
+
+
+def p24_token_logprobs_bwd(logits: torch.Tensor, tokens: torch.Tensor | None, stats: torch.Tensor,
+                           dlogp: torch.Tensor | None = None, entropy: torch.Tensor | None = None,
+                           dentropy: torch.Tensor | None = None, temperature: float = 1.0,
+                           dlogits: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The gradient of p24_token_logprobs' logp and entropy for the upstream gradients dlogp and
+    dentropy (fp32 [T], either may be None): dlogits [T, V], which may be the logits themselves."""
+    T, V, ldz, dt = _logits(logits, "logits")
+    dev, f32 = logits.device, torch.float32
+    dlogits = torch.empty((T, V), dtype=logits.dtype, device=dev) if dlogits is None else dlogits
+    ldd = _logits(dlogits, "dlogits", logits)[2]
+    a = p24_logprobs_args(T, V, 0, dt, temperature, logits.data_ptr(), ldz,
+                          _per_row(tokens, (T,), torch.int32, "tokens", dev), None,
+                          _per_row(entropy, (T,), f32, "entropy", dev), _per_row(stats, (T, 2), f32, "stats", dev),
+                          None, None, _per_row(dlogp, (T,), f32, "dlogp", dev),
+                          _per_row(dentropy, (T,), f32, "dentropy", dev), dlogits.data_ptr(), ldd)
+    _check(lib.p24_token_logprobs_bwd(C.byref(a), _stream(stream)), "p24_token_logprobs_bwd")
+    return dlogits
+
+
+def _distill_args(logits, top_idx, top_val, labels, temperature, tail, dkl, dce, dlogits) -> p24_distill_args:
+    T, V, ldz, dt = _logits(logits, "logits")
+    if top_idx.dim() != 2:
+        raise ValueError("top_idx must be 2-D [T, K]")
+    dev, f32, i32, K = logits.device, torch.float32, torch.int32, top_idx.shape[1]
+    return p24_distill_args(T, V, K, dt, temperature, P24_DISTILL_TAIL if tail else 0, logits.data_ptr(), ldz,
+                            _per_row(top_idx, (T, K), i32, "top_idx", dev),
+                            _per_row(top_val, (T, K), f32, "top_val", dev),
+                            _per_row(labels, (T,), i32, "labels", dev), None, None, None,
+                            _per_row(dkl, (T,), f32, "dkl", dev), _per_row(dce, (T,), f32, "dce", dev),
+                            _ptr(dlogits), 0 if dlogits is None else _logits(dlogits, "dlogits", logits)[2])
+
+
+def p24_distill_topk(logits: torch.Tensor, top_idx: torch.Tensor, top_val: torch.Tensor,
+                     labels: torch.Tensor | None = None, temperature: float = 1.0, tail: bool = False,
+                     dkl: torch.Tensor | None = None, dce: torch.Tensor | None = None, out: dict | None = None,
+                     stream=None) -> dict:
+    """Distillation of rows of student logits [T, V] from a teacher's list top_idx (int32 [T, K],
+    -1 for an absent entry), top_val (fp32 [T, K]): kl [T], with labels (int32 [T]) also the cross
+    entropy ce [T], and stats [T, 4] for the backward, as a dict. tail: the teacher's remaining
+    probability is one bucket (else the list is renormalised). With the rows' weights dkl and/or dce
+    (fp32 [T]), or a tensor under out["dlogits"], the same call also gives the gradient dlogits
+    (out["dlogits"] may be the logits themselves). See include/prune24.h."""
+    o = {} if out is None else dict(out)
+    T, dev, f32 = logits.shape[0], logits.device, torch.float32
+    if (dkl is not None or dce is not None) and o.get("dlogits") is None:
+        o["dlogits"] = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+    a = _distill_args(logits, top_idx, top_val, labels, temperature, tail, dkl, dce, o.get("dlogits"))
+    for name, shape in (("kl", (T,)), ("stats", (T, 4))) + ((("ce", (T,)),) if labels is not None else ()):
+        if o.get(name) is None:
+            o[name] = torch.empty(shape, dtype=f32, device=dev)
+        setattr(a, name, _per_row(o[name], shape, f32, name, dev))
+    _check(lib.p24_distill_topk(C.byref(a), _stream(stream)), "p24_distill_topk")
+    return o
+
+
+def p24_distill_topk_bwd(logits: torch.Tensor, top_idx: torch.Tensor, top_val: torch.Tensor, stats: torch.Tensor,
+                         dkl: torch.Tensor | None = None, labels: torch.Tensor | None = None,
+                         dce: torch.Tensor | None = None, temperature: float = 1.0, tail: bool = False,
+                         dlogits: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The gradient of p24_distill_topk's kl and ce for the rows' weights dkl and dce (fp32 [T],
+    either may be None), from its stats: dlogits [T, V], which may be the logits themselves."""
+    dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device) if dlogits is None else dlogits
+    a = _distill_args(logits, top_idx, top_val, labels, temperature, tail, dkl, dce, dlogits)
+    a.stats = _per_row(stats, (a.T, 4), torch.float32, "stats", logits.device)
+    _check(lib.p24_distill_topk_bwd(C.byref(a), _stream(stream)), "p24_distill_topk_bwd")
+    return dlogits

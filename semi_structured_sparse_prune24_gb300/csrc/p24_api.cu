@@ -7,6 +7,7 @@
 #include <mutex>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 
 #include "p24_internal.h"
 
@@ -710,6 +711,89 @@ int hyb_sddmm(const p24_hybrid* h, const void* G, int64_t N, int64_t ldg, const 
   if (h->cap > 0) P24_TRY(check_dense(S_ovf, h->cap, h->cols, lds));
   if (h->rows == 0) return P24_OK;
   return cuda_status(launch_hyb_sddmm(*h, G, N, ldg, B, ldb, S_ell, S_ovf, lds, as_stream(stream)));
+}
+
+namespace {
+constexpr int64_t kMaxVocab = int64_t(1) << 30;      // positions in a row are 32-bit
+constexpr int64_t kMaxVocabTail = int64_t(1) << 19;  // the listed columns' mask is in shared memory
+
+// [T, V] logits or their gradient: any row stride, aligned to the element
+int check_logits(const void* p, int32_t dtype, int64_t T, int64_t V, int64_t ld) {
+  if (dtype != P24_BF16 && dtype != P24_F32) return P24_EINVAL;
+  if (T < 0 || T > kMaxDim || V < 1) return P24_EINVAL;
+  if (V > kMaxVocab) return P24_EUNSUPPORTED;
+  if (T == 0) return P24_OK;
+  if (!p || ld < V) return P24_EINVAL;
+  return (reinterpret_cast<uintptr_t>(p) & (dtype == P24_BF16 ? 1u : 3u)) ? P24_EALIGN : P24_OK;
+}
+
+bool good_temperature(float t) { return t >= 1e-4f && t <= 1e4f; }  // false for NaN
+
+bool all_aligned4(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (!aligned4(p)) return false;
+  return true;
+}
+}  // namespace
+
+int p24_token_logprobs(const p24_logprobs_args* a, void* stream) {
+  if (!a) return P24_EINVAL;
+  P24_TRY(check_logits(a->logits, a->dtype, a->T, a->V, a->ldz));
+  if (!good_temperature(a->temperature) || a->k < 0) return P24_EINVAL;
+  if (a->k > P24_TOPK_MAX) return P24_EUNSUPPORTED;
+  if (a->T == 0) return P24_OK;
+  if (a->logp && !a->tokens) return P24_EINVAL;
+  if (a->k > 0 ? !(a->top_logp && a->top_idx) : (a->top_logp || a->top_idx)) return P24_EINVAL;
+  if (!a->logp && !a->entropy && !a->stats && a->k == 0) return P24_EINVAL;
+  if (!all_aligned4({a->tokens, a->logp, a->entropy, a->stats, a->top_logp, a->top_idx})) return P24_EALIGN;
+  return cuda_status(launch_logprobs(*a, as_stream(stream)));
+}
+
+int p24_token_logprobs_bwd(const p24_logprobs_args* a, void* stream) {
+  if (!a) return P24_EINVAL;
+  P24_TRY(check_logits(a->logits, a->dtype, a->T, a->V, a->ldz));
+  P24_TRY(check_logits(a->dlogits, a->dtype, a->T, a->V, a->ldd));
+  if (!good_temperature(a->temperature)) return P24_EINVAL;
+  if (a->T == 0) return P24_OK;
+  if (!a->stats || (a->dlogp && !a->tokens) || (a->dentropy && !a->entropy)) return P24_EINVAL;
+  if (a->dlogits == a->logits && a->ldd != a->ldz) return P24_EINVAL;
+  if (!all_aligned4({a->tokens, a->entropy, a->stats, a->dlogp, a->dentropy})) return P24_EALIGN;
+  return cuda_status(launch_logprobs_bwd(*a, as_stream(stream)));
+}
+
+namespace {
+int check_distill(const p24_distill_args* a, bool forward) {
+  if (!a) return P24_EINVAL;
+  if (a->flags & ~P24_DISTILL_TAIL) return P24_EINVAL;
+  P24_TRY(check_logits(a->logits, a->dtype, a->T, a->V, a->ldz));
+  if ((a->flags & P24_DISTILL_TAIL) && a->V > kMaxVocabTail) return P24_EUNSUPPORTED;
+  if (!good_temperature(a->temperature) || a->K < 0) return P24_EINVAL;
+  if (a->K > P24_TOPK_MAX) return P24_EUNSUPPORTED;
+  if (a->T == 0) return P24_OK;
+  if (a->K > 0 && (!a->top_idx || !a->top_val)) return P24_EINVAL;
+  if ((a->dce || a->ce) && !a->labels) return P24_EINVAL;
+  if (forward ? !a->kl : !a->stats) return P24_EINVAL;
+  if (a->dlogits || !forward) {
+    P24_TRY(check_logits(a->dlogits, a->dtype, a->T, a->V, a->ldd));
+    if (a->dlogits == a->logits && a->ldd != a->ldz) return P24_EINVAL;
+  } else if (a->dkl || a->dce) {
+    return P24_EINVAL;  // weights, but nowhere to put the gradient
+  }
+  if (!all_aligned4({a->top_idx, a->top_val, a->labels, a->kl, a->ce, a->stats, a->dkl, a->dce})) return P24_EALIGN;
+  return P24_OK;
+}
+}  // namespace
+
+int p24_distill_topk(const p24_distill_args* a, void* stream) {
+  P24_TRY(check_distill(a, true));
+  if (a->T == 0) return P24_OK;
+  return cuda_status(launch_distill(*a, as_stream(stream)));
+}
+
+int p24_distill_topk_bwd(const p24_distill_args* a, void* stream) {
+  P24_TRY(check_distill(a, false));
+  if (a->T == 0) return P24_OK;
+  return cuda_status(launch_distill_bwd(*a, as_stream(stream)));
 }
 
 int p24_selftest_timeout(int64_t limit_ns, void* stream) {
