@@ -1,0 +1,583 @@
+// head_rows.cuh -- what the language-model head's row kernels share: how a row of logits is
+// split over threads and CTAs, its softmax sums, and how they are joined.
+//
+// A row of V elements at any element alignment is its interior, nint aligned 16-byte vectors
+// of N elements starting `head` elements in, and at most 2 (N - 1) edge elements before and
+// after it. A cluster of C CTAs takes a row together: rank r the interior vectors
+// from r ceil(nint / C) on, rank 0 the edges too (one per thread).
+//
+// A CTA's share of its rows comes through a ring of stages in shared memory, filled by bulk
+// copies (cp.async.bulk) that run ahead of the threads by the ring's length, over row ends too:
+// loads are under way while the CTA reduces, waits and stores. Measured against loads into
+// registers one stage ahead (16-byte loads, 64 registers): see the kernels' comments.
+#pragma once
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include <cstdint>
+
+#include "p24_internal.h"
+#include "p24_ptx.cuh"
+
+namespace p24 {
+namespace {
+
+// How a kernel is laid out on an SM: kCtas CTAs of NT threads, each with a ring of S stages of SV
+// vectors per thread.
+template <int NT_, int kCtas_, int SV_, int S_>
+struct Layout {
+  static constexpr int NT = NT_, kCtas = kCtas_, SV = SV_, S = S_, kWarps = NT_ / 32;
+  static constexpr int kStage = NT * SV;          // vectors of a stage
+  static constexpr int kRing = S * kStage * 16;   // bytes
+};
+
+constexpr int kTopMax = P24_TOPK_MAX;
+constexpr int kMaxRanks = 8;                  // the portable cluster size
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ninf() { return __int_as_float(0xff800000); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// max(x, -1e30) that keeps a NaN: a difference of -inf (a masked logit) becomes finite, so
+// that its product with exp = 0 is 0 and not NaN.
+__device__ __forceinline__ float floored(float x) {
+  float y;
+  asm("max.NaN.f32 %0, %1, 0fF149F2CA;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two fp32 operations in one instruction.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void split(F2 p, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p.v));
+}
+__device__ __forceinline__ F2 add2(F2 p, F2 q) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(p.v), "l"(q.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 p, F2 q) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(p.v), "l"(q.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 p, F2 q, F2 s) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(p.v), "l"(q.v), "l"(s.v));
+  return r;
+}
+__device__ __forceinline__ F2 ex2x2(F2 p) {
+  float x, y;
+  split(p, x, y);
+  return f2(ex2(x), ex2(y));
+}
+
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f32(float x) { return x; }
+
+// ---------------------------------------------------------------- vectors of 16 bytes
+template <typename T>
+struct Vec {
+  static constexpr int N = 16 / sizeof(T);
+  static constexpr uint32_t kFill = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;  // -inf
+};
+
+template <typename T>
+__device__ __forceinline__ uint4 fill_vec() {
+  return make_uint4(Vec<T>::kFill, Vec<T>::kFill, Vec<T>::kFill, Vec<T>::kFill);
+}
+
+// The vector with the elements whose bits are set replaced by -inf.
+template <typename T>
+__device__ __forceinline__ uint4 without(uint4 r, uint32_t bits) {
+  uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t b = bits >> (2 * i);
+      const uint32_t m = ((b & 1u) ? 0xffffu : 0u) | ((b & 2u) ? 0xffff0000u : 0u);
+      w[i] = (w[i] & ~m) | (Vec<T>::kFill & m);
+    } else {
+      if ((bits >> i) & 1u) w[i] = Vec<T>::kFill;
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Element pairs j of a vector as fp32: j < N / 2.
+template <typename T>
+__device__ __forceinline__ F2 pair(const uint4& r, int j) {
+  if constexpr (sizeof(T) == 2) {
+    const uint32_t w = j == 0 ? r.x : j == 1 ? r.y : j == 2 ? r.z : r.w;
+    return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  } else {
+    return j == 0 ? f2(__uint_as_float(r.x), __uint_as_float(r.y)) : f2(__uint_as_float(r.z), __uint_as_float(r.w));
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ float elem_of(const uint4& r, int j) {
+  float x, y;
+  split(pair<T>(r, j >> 1), x, y);
+  return (j & 1) ? y : x;
+}
+
+// The larger elements of two registers of a vector, NaN dropped; and the largest element of one.
+template <typename T>
+__device__ __forceinline__ uint32_t max_raw(uint32_t a, uint32_t b) {
+  if constexpr (sizeof(T) == 2) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  } else {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }
+}
+// Of a vector and what was found before.
+template <typename T>
+__device__ __forceinline__ uint32_t max_vec(uint32_t a, const uint4& r) {
+  return max_raw<T>(max_raw<T>(a, max_raw<T>(r.x, r.y)), max_raw<T>(r.z, r.w));
+}
+template <typename T>
+__device__ __forceinline__ float max_of(uint32_t a) {
+  if constexpr (sizeof(T) == 2)
+    return fmaxf(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
+  else
+    return fmaxf(__uint_as_float(a), ninf());  // a NaN is dropped here too
+}
+
+// ---------------------------------------------------------------- a row's parts
+template <typename T>
+struct RowPart {
+  const T* row;
+  const uint4* body;  // the interior's first vector
+  int head, tail0;    // the interior covers elements [head, tail0)
+  int lo, hi;         // this CTA's interior vectors
+  int edges;          // this CTA's edge elements (rank 0: all of the row's)
+
+  // ranks: a power of two
+  __device__ __forceinline__ RowPart(const T* r, int V, int rank, int ranks) {
+    constexpr int N = Vec<T>::N;
+    const int a = static_cast<int>((reinterpret_cast<uintptr_t>(r) & 15u) / sizeof(T));
+    head = min(a ? N - a : 0, V);
+    const int nint = (V - head) / N;
+    tail0 = head + nint * N;
+    row = r;
+    body = reinterpret_cast<const uint4*>(r + head);
+    const int each = (nint + ranks - 1) >> (31 - __clz(ranks));
+    lo = min(nint, rank * each);
+    hi = min(nint, lo + each);
+    edges = rank == 0 ? head + V - tail0 : 0;
+  }
+  __device__ __forceinline__ int edge_pos(int e) const { return e < head ? e : tail0 + e - head; }
+  __device__ __forceinline__ int vec_pos(int v) const { return head + v * Vec<T>::N; }
+  // whether element i of the row is this CTA's
+  __device__ __forceinline__ bool owns(int i) const {
+    if (i < head || i >= tail0) return edges > 0;
+    const int v = (i - head) / Vec<T>::N;
+    return v >= lo && v < hi;
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ float load_edge(const RowPart<T>& p, bool on) {
+  const int e = static_cast<int>(threadIdx.x);
+  return on && e < p.edges ? to_f32(p.row[p.edge_pos(e)]) : ninf();
+}
+
+// ---------------------------------------------------------------- softmax sums
+// Sums over part of a row relative to its maximum m: s = sum exp((z - m)/tau) and
+// a = sum exp((z - m)/tau) (z - m). s == 0: nothing above -inf yet. c = log2(e) / tau below.
+struct Sums {
+  float m, s, a;
+};
+
+// The factor that takes sums at m to the reference `to` >= m; d becomes m - to.
+__device__ __forceinline__ float rebase_factor(float m, float to, float c, float& d) {
+  d = floored(m - to);
+  return ex2(d * c);
+}
+
+// A thread's sums while it walks its vectors; two halves that are added at the end.
+template <bool kEntropy>
+struct Walk {
+  float m;
+  F2 s, a;
+
+  __device__ __forceinline__ Walk() : m(ninf()), s(f2(0.f, 0.f)), a(f2(0.f, 0.f)) {}
+
+  __device__ __forceinline__ void raise(float vm, float c) {  // the running maximum becomes at least vm
+    if (vm > m) {
+      if (m > ninf()) {
+        float d;
+        const float r = rebase_factor(m, vm, c, d);
+        if constexpr (kEntropy) a = mul2(fma2(s, f2(d, d), a), f2(r, r));
+        s = mul2(s, f2(r, r));
+      }
+      m = vm;
+    }
+  }
+  __device__ __forceinline__ float ref() const { return m > ninf() ? m : 0.f; }
+
+  // The elements of a vector, of which none is above m.
+  template <typename T>
+  __device__ __forceinline__ void add(const uint4& r, float c) {
+    const float ref_ = -ref();
+    const F2 off = f2(ref_, ref_), c2 = f2(c, c);
+    F2 av = f2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < Vec<T>::N / 2; ++j) {
+      const F2 t = add2(pair<T>(r, j), off);
+      const F2 e = ex2x2(mul2(t, c2));
+      s = add2(s, e);
+      if constexpr (kEntropy) av = j == 0 ? mul2(e, t) : fma2(e, t, av);
+    }
+    if constexpr (kEntropy) {
+      float x, y;
+      split(av, x, y);
+      if (x + y != x + y) {  // an element of -inf (0 times -inf), or a NaN: once more with the difference floored
+        av = f2(0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < Vec<T>::N / 2; ++j) {
+          split(add2(pair<T>(r, j), off), x, y);
+          const F2 t = f2(floored(x), floored(y));
+          av = fma2(ex2x2(mul2(t, c2)), t, av);
+        }
+      }
+      a = add2(a, av);
+    }
+  }
+  __device__ __forceinline__ void add_one(float x, float c) {
+    raise(x, c);
+    const float t = floored(x - ref());
+    const float e = ex2(t * c);
+    s = add2(s, f2(e, 0.f));
+    if constexpr (kEntropy) a = add2(a, f2(e * t, 0.f));
+  }
+  __device__ __forceinline__ Sums sums() const {
+    Sums u{m, 0.f, 0.f};
+    float x, y;
+    split(s, x, y);
+    u.s = x + y;
+    split(a, x, y);
+    u.a = x + y;
+    return u;
+  }
+};
+
+// The larger of two maxima ignores a NaN, as the running maximum does.
+__device__ __forceinline__ float warp_max(float m) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(m));
+  return r;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(~0u, x, d);
+  return x;
+}
+
+// The sums of kParts parts, one per lane (and again from lane kParts on), in every lane. The
+// order of the additions is fixed.
+template <bool kEntropy, int kParts = 32>
+__device__ __forceinline__ Sums warp_join(Sums u, float c) {
+  const float m = warp_max(u.m);
+  float d, r = rebase_factor(u.m, m, c, d);
+  if (u.s == 0.f) r = 0.f, d = 0.f;
+  float a = (u.a + u.s * d) * r, s = u.s * r;
+#pragma unroll
+  for (int i = kParts / 2; i; i >>= 1) {
+    s += __shfl_xor_sync(~0u, s, i);
+    if constexpr (kEntropy) a += __shfl_xor_sync(~0u, a, i);
+  }
+  return Sums{m, s, a};
+}
+
+__device__ __forceinline__ Sums join(Sums u, Sums v, float c) {
+  const float m = fmaxf(u.m, v.m);
+  float d;
+  const float ru = rebase_factor(u.m, m, c, d), rv = rebase_factor(v.m, m, c, d);
+  return Sums{m, (u.s == 0.f ? 0.f : u.s * ru) + (v.s == 0.f ? 0.f : v.s * rv), 0.f};
+}
+
+// ---------------------------------------------------------------- clusters
+__device__ __forceinline__ int cluster_ranks() {
+  uint32_t n;
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+  return static_cast<int>(n);
+}
+// The address of `p` (shared memory of this CTA) in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t remote(const void* p, int rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void store_remote(uint32_t a, float x) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(x) : "memory");
+}
+__device__ __forceinline__ void store_remote(uint32_t a, uint64_t x) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(x) : "memory");
+}
+
+// Whole-cluster barrier that threads of a warp may reach apart.
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+struct JoinShared {
+  Sums warp[2][16];           // by row parity: the warps' sums
+  Sums rank[2][kMaxRanks];    // and the cluster's CTAs'
+};
+
+// The row's sums, in every thread of every CTA of its cluster; also a barrier of all of them.
+// `par` alternates from call to call, which keeps one row's reads apart from the next one's
+// writes: a CTA writes parity p again only two barriers later.
+template <bool kEntropy, int NT>
+__device__ __forceinline__ Sums row_join(Sums u, float c, JoinShared& sh, int par, int rank, int ranks) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  u = warp_join<kEntropy>(u, c);
+  if (lane == 0) sh.warp[par][warp] = u;
+  __syncthreads();
+  u = warp_join<kEntropy, NT / 32>(sh.warp[par][lane % (NT / 32)], c);
+  if (ranks > 1) {
+    if (warp == 0 && lane < ranks) {
+      const uint32_t to = remote(&sh.rank[par][rank], lane);
+      store_remote(to, u.m);
+      store_remote(to + 4, u.s);
+      if constexpr (kEntropy) store_remote(to + 8, u.a);
+    }
+    cluster_barrier();
+    u = lane % kMaxRanks < ranks ? sh.rank[par][lane % kMaxRanks] : Sums{ninf(), 0.f, 0.f};
+    u = warp_join<kEntropy, kMaxRanks>(u, c);
+  }
+  return u;
+}
+
+// ---------------------------------------------------------------- the ring
+template <int S>
+struct RingShared {
+  uint64_t full[S];    // a stage's data has arrived
+  int done[S];         // warps that have finished reading it
+  int fills[S];        // times it was filled
+  int abort;           // a wait ran out (the device status word says so)
+};
+
+// The stages a CTA walks: for each of its rows (row r of it is row first + r step), `visits`
+// times the `stages` parts of L::kStage vectors of its share. Stage q of that sequence
+// sits in slot q % S; the last warp to finish a slot refills it with stage q + S.
+template <typename T, typename L>
+struct Ring {
+  static constexpr int S = L::S, kStage = L::kStage, kThreads = L::NT;
+  const T* logits;
+  int64_t ld, first, step, rows;
+  int V, rank, ranks, stages, visits;
+  uint4* data;
+  RingShared<S>* sh;
+  int* status;
+  int slot;            // of the next stage to read
+  uint32_t parity;
+
+  __device__ __forceinline__ void fill(int to, int64_t r, int at) const {
+    const int64_t t = first + r * step;
+    if (t >= rows || *reinterpret_cast<volatile int*>(&sh->abort)) return;
+    const RowPart<T> p(logits + t * ld, V, rank, ranks);
+    const int v = p.lo + (at < stages ? at : at - stages) * L::kStage;
+    const int n = min(p.hi - v, L::kStage);
+    ++sh->fills[to];
+    if (n <= 0) {  // rows of one matrix can differ by a vector: nothing to copy for this one
+      mbar_arrive(&sh->full[to]);
+      return;
+    }
+    mbar_arrive_expect_tx(&sh->full[to], n * 16u);
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(data + to * L::kStage)),
+                 "l"(p.body + v), "r"(n * 16u), "r"(smem_u32(&sh->full[to]))
+                 : "memory");
+  }
+
+  // All threads; ends with a barrier.
+  __device__ __forceinline__ void start() {
+    slot = 0;
+    parity = 0;
+    if (threadIdx.x == 0) {
+      sh->abort = 0;
+      for (int i = 0; i < S; ++i) {
+        mbar_init(&sh->full[i], 1);
+        sh->done[i] = 0;
+        sh->fills[i] = 0;
+      }
+      fence_barrier_init();
+      fence_proxy_async_smem();
+    }
+    __syncthreads();
+    if (threadIdx.x == 0)
+      for (int i = 0; i < S; ++i) fill(i, i / (stages * visits), i % (stages * visits));
+  }
+
+  // The next stage's data, once it is there: vector u of this thread is at u * L::NT.
+  __device__ __forceinline__ const uint4* wait() {
+    p24_wait(&sh->full[slot], parity, &sh->abort, status);
+    return data + slot * L::kStage + threadIdx.x;
+  }
+  // f(vector, u) for this thread's vectors of a stage that holds n (or, past the ring's stage
+  // size, all of them).
+  template <typename F>
+  __device__ __forceinline__ static void each(const uint4* at, int n, F&& f) {
+    if (n >= L::kStage) {
+#pragma unroll
+      for (int u = 0; u < L::SV; ++u) f(at[u * L::NT], u);
+    } else {
+#pragma unroll 1
+      for (int u = 0; u * L::NT + static_cast<int>(threadIdx.x) < n; ++u) f(at[u * L::NT], u);
+    }
+  }
+  // This warp has read the current stage, stage `at` of row r: on to the next.
+  __device__ __forceinline__ void release(int64_t r, int at) {
+    const int of = slot;
+    if (++slot == S) {
+      slot = 0;
+      parity ^= 1;
+    }
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+      int before;
+      asm volatile("atom.acq_rel.cta.shared::cta.add.s32 %0, [%1], 1;" : "=r"(before) : "r"(smem_u32(&sh->done[of])) : "memory");
+      if (before == L::kWarps - 1) {
+        sh->done[of] = 0;
+        int next = at + S;
+        while (next >= stages * visits) {
+          next -= stages * visits;
+          ++r;
+        }
+        fill(of, r, next);
+      }
+    }
+  }
+  // After an expired wait, copies may still be on their way into this CTA's shared memory.
+  __device__ __forceinline__ void finish() const {
+    __syncthreads();  // no wait begins after this
+    if (threadIdx.x == 0 && *reinterpret_cast<volatile int*>(&sh->abort))
+      for (int i = 0; i < S; ++i)
+        if (sh->fills[i] > 0) p24_wait_quiet(&sh->full[i], (sh->fills[i] - 1) & 1);
+  }
+};
+
+// Elements w exp((z - m)/tau - l) (+ w1 exp(z - m - l1)): a gradient's terms in p, with off =
+// -l log2(e) and off1 = -l1 log2(e).
+struct Terms {
+  float m, c, off, w, off1, w1;
+
+  template <bool kTwo>
+  __device__ __forceinline__ float one(float z) const {
+    const float d = z - m;
+    float y = w * ex2(fmaf(d, c, off));
+    if constexpr (kTwo) y = fmaf(w1, ex2(fmaf(d, kLog2e, off1)), y);
+    return y;
+  }
+  template <bool kTwo>
+  __device__ __forceinline__ F2 two(F2 z) const {
+    const F2 d = add2(z, f2(-m, -m));
+    F2 y = mul2(f2(w, w), ex2x2(fma2(d, f2(c, c), f2(off, off))));
+    if constexpr (kTwo) y = fma2(f2(w1, w1), ex2x2(fma2(d, f2(kLog2e, kLog2e), f2(off1, off1))), y);
+    return y;
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ uint4 pack_vec(const F2 (&y)[Vec<T>::N / 2]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < Vec<T>::N / 2; ++j) {
+    float a, b;
+    split(y[j], a, b);
+    if constexpr (sizeof(T) == 2) {
+      w[j] = pack_bf16x2(a, b);
+    } else {
+      w[2 * j] = __float_as_uint(a);
+      w[2 * j + 1] = __float_as_uint(b);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Store a vector at element i0 of an output row; `aligned`: the row has the logits' alignment.
+template <typename T>
+__device__ __forceinline__ void store_vec(T* row, int i0, bool aligned, const uint4& r) {
+  if (aligned) {
+    *reinterpret_cast<uint4*>(row + i0) = r;
+  } else {
+#pragma unroll
+    for (int j = 0; j < Vec<T>::N; ++j) row[i0 + j] = static_cast<T>(elem_of<T>(r, j));
+  }
+}
+
+// ---------------------------------------------------------------- launch
+// A persistent grid of clusters of `ranks` CTAs of NT threads over `rows` items.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_rows(void (*kern)(KArgs...), int NT, int64_t rows, int ranks, size_t smem, cudaStream_t s,
+                        Args&&... args) {
+  int slots = 0;
+  cudaError_t e = row_kernel_slots(reinterpret_cast<const void*>(kern), NT, ranks, smem, &slots);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(rows, slots) * ranks));
+  cfg.blockDim = dim3(NT);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(ranks);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = ranks > 1 ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+  if (e == cudaSuccess) count_launch();
+  return e;
+}
+
+// An elementwise kernel's CTAs take parts of rows: enough of them that every SM has its CTAs.
+template <typename L>
+int row_parts(int64_t T, int64_t vecs) {
+  int parts = 1;
+  while (T * parts < sm_count() * L::kCtas && vecs >= 2 * L::NT * parts) parts *= 2;
+  return parts;
+}
+// The CTAs of a row whose loss is wanted: more than one only where rows are few.
+template <typename L>
+int row_ranks(int ranks, int64_t T, int64_t vecs) {
+  while (ranks < kMaxRanks && T * ranks * 2 <= sm_count() * L::kCtas && vecs >= L::NT * ranks) ranks *= 2;
+  return ranks;
+}
+// As launch_rows, over T rows in `parts` parts: CTA b takes part b % parts of rows.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_parts(void (*kern)(KArgs...), int NT, int64_t T, int parts, size_t smem, cudaStream_t s, Args&&... args) {
+  int slots = 0;
+  cudaError_t e = row_kernel_slots(reinterpret_cast<const void*>(kern), NT, 1, smem, &slots);
+  if (e != cudaSuccess) return e;
+  const int64_t rows = std::min<int64_t>(T, std::max(1, slots / parts));
+  e = launch_plain(kern, dim3(static_cast<unsigned>(rows * parts)), dim3(NT), smem, s, std::forward<Args>(args)...);
+  if (e == cudaSuccess) count_launch();
+  return e;
+}
+
+// Stages that the longest share of a row of `vecs` vectors takes.
+__host__ __device__ constexpr int row_stages(int64_t vecs, int ranks, int per_stage) {
+  const int64_t n = (vecs + ranks - 1) / ranks;
+  return n > per_stage ? static_cast<int>((n + per_stage - 1) / per_stage) : 1;
+}
+
+}  // namespace
+}  // namespace p24

@@ -1,0 +1,562 @@
+// logprobs_kernels.cu -- log probabilities of given tokens, entropy and top alternatives of
+// rows of logits, and the gradient of the first two.
+//
+//   x = (z - m) / tau,  m = max z,  s = sum exp(x),  p = exp(x) / s
+//   logp = x[token] - ln s        H = ln s - (1/s) sum exp(x) x
+//   dz = (1/tau) [ dlogp (delta - p) - dentropy p (ln p + H) ]
+//
+//  logprobs_kernel      a cluster per row (head_rows.cuh): one pass with a running maximum and
+//                       sums per thread, joined over the CTA and the cluster. The alternatives
+//                       come from a second look at few vectors: the k-th largest of the threads'
+//                       maxima is a lower bound of the k-th largest logit, so only parts whose
+//                       maximum reaches it can hold alternatives. Those parts (a thread's share
+//                       of one stage or a few) are read again, from L2, the elements that reach
+//                       the bound are listed, and each one's place is the number of listed ones
+//                       before it. Where the list overflows because many logits tie at the bound
+//                       (masked rows, constant rows) the ones above it are listed and the rest
+//                       taken in order of position; what is left goes through an exact selection.
+//  logprobs_bwd_kernel  elementwise from the saved statistics.
+//
+// Bound: HBM, one read of the logits (and one write of the gradient).
+#include <algorithm>
+#include <type_traits>
+
+#include "head_rows.cuh"
+
+namespace p24 {
+namespace {
+
+// ---------------------------------------------------------------- top k
+// Order of the logits as an unsigned key: larger key first; NaN above +inf, -0 equal to +0.
+// Every key is above 0.
+__device__ __forceinline__ uint32_t order_key(float x) {
+  if (x != x) return 0xffffffffu;
+  const uint32_t u = __float_as_uint(x + 0.f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t key) {
+  return __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
+}
+// Key and position in one number that orders both: ties go to the lower position.
+__device__ __forceinline__ uint64_t entry(uint32_t key, int i) {
+  return (static_cast<uint64_t>(key) << 32) | (0xffffffffu - static_cast<uint32_t>(i));
+}
+__device__ __forceinline__ int entry_pos(uint64_t e) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(e)); }
+__device__ __forceinline__ uint32_t entry_key(uint64_t e) { return static_cast<uint32_t>(e >> 32); }
+
+using Long = Layout<256, 4, 4, 2>;       // with alternatives (17 KB for them)
+using LongPlain = Layout<256, 4, 4, 3>;  // without
+using LongGrad = Layout<256, 4, 4, 3>;
+using Short = Layout<128, 8, 2, 4>;      // rows of up to kShortRow vectors
+constexpr int kShortRow = 1024;
+
+constexpr int kList = 1024;  // candidates listed before something else has to be done
+constexpr int kParts = 16;   // parts a thread's share of a row has for the second look
+constexpr int kItems = 1024; // parts looked at a second time before something else has to be done
+
+template <int NT>
+struct TopShared {
+  uint64_t list[kList];       // candidates
+  uint16_t part[kParts][NT];  // upper half of the largest element of each thread's parts
+  uint16_t item[kItems];      // parts to look at: part * NT + thread
+  uint32_t hist[256];
+  int warp[16];
+  uint32_t low[16], high[16];
+  uint32_t prefix;
+  int left;                   // how many of the elements equal to the prefix are still to be taken
+  int n, items;               // entries listed, parts to look at
+};
+
+// Step `i` of a walk over a row part in order of position: step 0 the elements before the
+// interior, then tiles of NT interior vectors, last the elements after it. Gives a thread's
+// elements of the step (the rest -inf), their number and the first one's position.
+template <typename T, int NT>
+__device__ __forceinline__ int walk_step(const RowPart<T>& p, int i, int steps, float (&x)[Vec<T>::N], int& pos) {
+  constexpr int N = Vec<T>::N;
+  const int tid = threadIdx.x;
+  if (i > 0 && i < steps - 1) {
+    const int v = p.lo + (i - 1) * NT + tid;
+    if (v >= p.hi) return 0;
+    const uint4 r = p.body[v];
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[j] = elem_of<T>(r, j);
+    pos = p.vec_pos(v);
+    return N;
+  }
+  const int e = i == 0 ? tid : p.head + tid;
+  if (e >= (i == 0 ? min(p.head, p.edges) : p.edges)) return 0;
+  pos = p.edge_pos(e);
+  x[0] = to_f32(p.row[pos]);
+  return 1;
+}
+
+// The first k elements of a row part that has at least k, unordered, into sh.list[0, k):
+// a radix selection of the k-th key, 8 bits a pass, then the elements above it and, in
+// order of position, as many equal to it as are needed. All threads; ends with a barrier.
+template <typename T, int NT>
+__device__ __noinline__ void select_exact(const RowPart<T>& p, int k, TopShared<NT>& sh) {
+  constexpr int N = Vec<T>::N;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int steps = 2 + (p.hi - p.lo + NT - 1) / NT;
+  __syncthreads();
+  if (tid == 0) {
+    sh.prefix = 0;
+    sh.left = k;
+    sh.n = 0;
+  }
+  uint32_t mask = 0;
+  for (int shift = 24; shift >= 32 - 8 * static_cast<int>(sizeof(T)); shift -= 8) {
+    for (int i = tid; i < 256; i += NT) sh.hist[i] = 0;
+    __syncthreads();
+    const uint32_t prefix = sh.prefix;
+    // a thread adds equal digits up before it touches their counter: rows that come here have many
+    uint32_t digit = 0, run = 0;
+    for (int i = 0; i < steps; ++i) {
+      float x[N];
+      int pos;
+      const int n = walk_step<T, NT>(p, i, steps, x, pos);
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        if (j >= n) continue;
+        const uint32_t key = order_key(x[j]), d = (key >> shift) & 255u;
+        if ((key & mask) != prefix) continue;
+        if (d != digit) {
+          if (run) atomicAdd(&sh.hist[digit], run);
+          digit = d;
+          run = 0;
+        }
+        ++run;
+      }
+    }
+    if (run) atomicAdd(&sh.hist[digit], run);
+    __syncthreads();
+    if (warp == 0) {
+      // lane l holds the counters of digits 255 - 8 l down to 248 - 8 l
+      int own = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) own += static_cast<int>(sh.hist[255 - 8 * lane - i]);
+      int before = own;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(~0u, before, d);
+        if (lane >= d) before += y;
+      }
+      before -= own;
+      const int left = sh.left;
+      __syncwarp();
+      if (before < left && left <= before + own) {
+        int i = 0, here = left - before;
+        for (; static_cast<int>(sh.hist[255 - 8 * lane - i]) < here; ++i) here -= static_cast<int>(sh.hist[255 - 8 * lane - i]);
+        sh.left = here;
+        sh.prefix = prefix | (static_cast<uint32_t>(255 - 8 * lane - i) << shift);
+      }
+    }
+    mask |= 255u << shift;
+    __syncthreads();
+  }
+  const uint32_t kth = sh.prefix;
+  const int left = sh.left;
+  int equal_before = 0;
+  for (int i = 0; i < steps; ++i) {
+    float x[N];
+    int pos = 0;
+    const int n = walk_step<T, NT>(p, i, steps, x, pos);
+    uint32_t eq = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if (j >= n) continue;
+      const uint32_t key = order_key(x[j]);
+      if ((key & mask) > kth) sh.list[atomicAdd(&sh.n, 1)] = entry(key, pos + j);  // fewer than k of them
+      if ((key & mask) == kth) eq |= 1u << j;
+    }
+    // the place of this thread's equal elements among all of the part's
+    const int mine = __popc(eq);
+    int incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(~0u, incl, d);
+      if (lane >= d) incl += y;
+    }
+    if (lane == 31) sh.warp[warp] = incl;
+    __syncthreads();
+    int before = equal_before + incl - mine;
+    for (int w = 0; w < NT / 32; ++w) {
+      if (w < warp) before += sh.warp[w];
+      equal_before += sh.warp[w];
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if ((eq >> j) & 1u) {
+        if (before < left) sh.list[k - left + before] = entry(order_key(x[j]), pos + j);
+        ++before;
+      }
+    __syncthreads();
+  }
+}
+
+// Element i of a row part, counted in order of position.
+template <typename T>
+__device__ __forceinline__ int nth_pos(const RowPart<T>& p, int i) {
+  const int head = p.edges > 0 ? p.head : 0, inner = (p.hi - p.lo) * Vec<T>::N;
+  return i < head ? i : i - head < inner ? p.vec_pos(p.lo) + i - head : p.tail0 + i - head - inner;
+}
+
+// List the elements of this CTA whose key is at least `from`: from the threads' parts that can
+// hold any, whose vectors all threads read together. own16: the upper half of the key of the
+// thread's largest element. Returns the number found; more than kList if there is no room. All
+// threads; sh.n and sh.items are 0 and a barrier lies behind that; ends with a barrier.
+template <typename T, typename L>
+__device__ __forceinline__ int list_from(const RowPart<T>& p, uint32_t from, uint32_t own16, int stages, int shift,
+                                         TopShared<L::NT>& sh) {
+  constexpr int N = Vec<T>::N, NT = L::NT;
+  static_assert(kParts * NT <= 65536, "an item is 16 bits");
+  const int tid = threadIdx.x;
+  auto list = [&](float x, int pos) {
+    const uint32_t key = order_key(x);
+    if (key >= from) {
+      const int at = atomicAdd(&sh.n, 1);
+      if (at < kList) sh.list[at] = entry(key, pos);
+    }
+  };
+  if (own16 >= (from >> 16) && own16 > 0) {
+    for (int i = 0; i << shift < stages; ++i)
+      if (order_key(__uint_as_float(static_cast<uint32_t>(sh.part[i][tid]) << 16)) >> 16 >= (from >> 16)) {
+        const int at = atomicAdd(&sh.items, 1);
+        if (at < kItems) sh.item[at] = static_cast<uint16_t>(i * NT + tid);
+      }
+    if (tid < p.edges) {
+      const int pos = p.edge_pos(tid);
+      list(to_f32(p.row[pos]), pos);
+    }
+  }
+  __syncthreads();
+  const int items = sh.items;
+  if (items > kItems) return kList + 1;
+  const int lg = shift + 31 - __clz(L::SV);  // log2 of a part's vectors
+  for (int i = tid; i < items << lg; i += NT) {
+    const int item = sh.item[i >> lg], v = p.lo + (((item / NT) << lg) + (i & ((1 << lg) - 1))) * NT + item % NT;
+    if (v >= p.hi) continue;
+    const uint4 r = p.body[v];
+#pragma unroll
+    for (int j = 0; j < N; ++j) list(elem_of<T>(r, j), p.vec_pos(v) + j);
+  }
+  __syncthreads();
+  return sh.n;
+}
+
+// This CTA's first min(k, its elements) elements, unordered, into sh.list; returns how many are
+// listed there (at least those). own16: the upper half of the order key of the thread's largest
+// element (0: it has none); odd: the row holds a NaN or +inf, which the maxima do not show. All
+// threads; ends with a barrier.
+template <typename T, typename L>
+__device__ __forceinline__ int top_of_part(const RowPart<T>& p, int k, uint32_t own16, bool odd, int stages, int shift,
+                                           TopShared<L::NT>& sh) {
+  constexpr int NT = L::NT;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int have = (p.hi - p.lo) * Vec<T>::N + p.edges;
+  if (k > have) k = have;
+  if (k == 0) return 0;
+  if (odd) {
+    select_exact<T, NT>(p, k, sh);
+    return k;
+  }
+  // the largest bound that k threads' maxima reach; 0 where fewer than k threads have elements
+  const uint32_t low = __reduce_min_sync(~0u, own16), high = __reduce_max_sync(~0u, own16);
+  if (lane == 0) sh.low[tid >> 5] = low, sh.high[tid >> 5] = high;
+  if (tid == 0) sh.n = sh.items = 0;
+  __syncthreads();
+  uint32_t lo = __reduce_min_sync(~0u, sh.low[lane % (NT / 32)]), hi = __reduce_max_sync(~0u, sh.high[lane % (NT / 32)]);
+  while (lo < hi) {
+    const uint32_t mid = (lo + hi + 1) / 2;
+    if (__syncthreads_count(own16 >= mid) >= k) lo = mid;
+    else hi = mid - 1;
+  }
+  int n = 0;
+  const bool masked = lo == 0x7fu || lo == 0x80u;  // a bound of -inf or of the lowest finite values
+  if (!masked) {
+    n = list_from<T, L>(p, lo << 16, own16, stages, shift, sh);
+    if (n <= kList) return n;
+  }
+  // Many ties at the bound: in bf16 the bound is one value; in fp32 two masking values are looked
+  // for, -inf and the lowest finite one. List what is above, then take ties from the front.
+  const uint32_t tie = sizeof(T) == 2 ? ((lo & 0x8000u) ? lo << 16 : lo << 16 | 0xffffu) : lo == 0x7fu ? 0x7fffffu : lo << 16;
+  if (sizeof(T) == 2 || masked) {
+    __syncthreads();
+    if (tid == 0) sh.n = sh.items = 0;
+    __syncthreads();
+    n = list_from<T, L>(p, tie + 1, own16, stages, shift, sh);
+    if (n >= k && n <= kList) return n;
+    __syncthreads();
+    if (n < k && tid < 32) {
+      constexpr int kEach = 4, kSteps = 32;
+      for (int step = 0; step < kSteps && n < k; ++step) {
+        const int i0 = step * 32 * kEach + lane;
+        float x[kEach];
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) x[j] = i0 + 32 * j < have ? to_f32(p.row[nth_pos(p, i0 + 32 * j)]) : 0.f;
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+          const uint32_t same = __ballot_sync(~0u, i0 + 32 * j < have && order_key(x[j]) == tie);
+          const int at = n + __popc(same & ((1u << lane) - 1));
+          if (((same >> lane) & 1u) && at < k) sh.list[at] = entry(tie, nth_pos(p, i0 + 32 * j));
+          n += __popc(same);
+        }
+      }
+      if (lane == 0) sh.n = min(n, k);
+    }
+    __syncthreads();
+    n = sh.n;
+    if (n == k) return n;
+  }
+  select_exact<T, NT>(p, k, sh);
+  return k;
+}
+
+// kTop: with alternatives.
+template <typename T, bool kEntropy, bool kTop, typename L>
+__global__ void __launch_bounds__(L::NT, L::kCtas) logprobs_kernel(const p24_logprobs_args g, int* status) {
+  using R = Ring<T, L>;
+  constexpr int NT = L::NT;
+  extern __shared__ __align__(128) uint4 ring_data[];
+  __shared__ RingShared<L::S> ring_sh;
+  __shared__ JoinShared joins;
+  TopShared<NT>& top = *reinterpret_cast<TopShared<NT>*>(reinterpret_cast<char*>(ring_data) + L::kRing);  // kTop
+  uint64_t* best = reinterpret_cast<uint64_t*>(&top + 1);  // kTop and more ranks than one: [rank][k], in order
+  const int tid = threadIdx.x, V = static_cast<int>(g.V), k = static_cast<int>(g.k);
+  const int ranks = cluster_ranks(), rank = ranks > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const float tau = g.temperature, c = kLog2e / tau;
+  const T* logits = static_cast<const T*>(g.logits);
+  const int stages = row_stages(V / Vec<T>::N, ranks, L::kStage);
+  int shift = 0;  // stages to a part of the second look, a power of two
+  while (kTop && (stages - 1) >> shift >= kParts) ++shift;
+  R ring{logits, g.ldz, blockIdx.x / ranks, gridDim.x / ranks, g.T, V, rank, ranks, stages, 1, ring_data, &ring_sh, status};
+  ring.start();
+  if (ranks > 1) cluster_barrier();  // every CTA runs before another writes to its shared memory
+
+  float edge = load_edge(RowPart<T>(logits + ring.first * g.ldz, V, rank, ranks), true);
+  int64_t r = 0;
+  for (int64_t t = ring.first; t < g.T; t += ring.step, ++r) {
+    const int par = r & 1;
+    const RowPart<T> p(logits + t * g.ldz, V, rank, ranks);
+    float z_tok = 0.f;
+    bool has_tok = false;
+    if (g.logp && tid == 0 && rank == 0) {
+      const int tok = g.tokens[t];
+      has_tok = tok >= 0 && tok < V;
+      if (has_tok) z_tok = to_f32(p.row[tok]);
+    }
+    Walk<kEntropy> w;
+    float part_max = ninf();
+    if (tid < p.edges) w.add_one(edge, c);
+    if (t + ring.step < g.T) edge = load_edge(RowPart<T>(logits + (t + ring.step) * g.ldz, V, rank, ranks), true);
+    for (int at = 0; at < stages; ++at) {
+      const uint4* data = ring.wait();
+      const int n = p.hi - p.lo - at * L::kStage;
+      uint32_t mr = Vec<T>::kFill;
+      R::each(data, n, [&](const uint4& x, int) { mr = max_vec<T>(mr, x); });
+      const float vm = max_of<T>(mr);
+      w.raise(vm, c);
+      if constexpr (kTop) {
+        part_max = fmaxf(part_max, vm);
+        if (((at + 1) & ((1 << shift) - 1)) == 0 || at + 1 == stages) {
+          top.part[at >> shift][tid] = static_cast<uint16_t>(__float_as_uint(part_max) >> 16);
+          part_max = ninf();
+        }
+      }
+      R::each(data, n, [&](const uint4& x, int) { w.template add<T>(x, c); });
+      ring.release(r, at);
+    }
+    const float own_max = w.m;
+    const bool own = p.lo + tid < p.hi || tid < p.edges;
+    const Sums u = row_join<kEntropy, NT>(w.sums(), c, joins, par, rank, ranks);
+    const float ls = u.s == 0.f ? ninf() : logf(u.s);
+    // ln of the probability of a logit; a row with nothing above -inf has none
+    auto logp = [&](float z) { return u.s == 0.f ? ninf() : (z - u.m) / tau - ls; };
+    if (tid == 0 && rank == 0) {
+      if (g.stats) {
+        g.stats[2 * t] = u.m;
+        g.stats[2 * t + 1] = ls;
+      }
+      if (g.logp) g.logp[t] = has_tok ? logp(z_tok) : 0.f;
+      if (kEntropy) g.entropy[t] = u.s == 0.f ? 0.f : ls - u.a / (u.s * tau);
+    }
+    if constexpr (kTop) {
+      auto put = [&](uint64_t e, int place) {
+        g.top_idx[t * k + place] = entry_pos(e);
+        g.top_logp[t * k + place] = logp(key_value(entry_key(e)));
+      };
+      const int n = top_of_part<T, L>(p, k, own ? order_key(own_max) >> 16 : 0u, !(u.s == u.s), stages, shift, top);
+      // each entry's place among them; of several ranks, rank 0 gets every list, filled up with
+      // entries that come after all others
+      // (four lanes to an entry)
+      const int all = ranks > 1 ? max(n, k) : n, sub = tid & 3;
+      for (int i0 = 0; i0 < all; i0 += NT / 4) {
+        const int i = i0 + (tid >> 2);
+        const uint64_t e = i < n ? top.list[i] : 0;
+        int place = 0;
+#pragma unroll 4
+        for (int j = sub; j < n; j += 4) place += top.list[j] > e;
+        place += __shfl_xor_sync(~0u, place, 1);
+        place += __shfl_xor_sync(~0u, place, 2);
+        if (i >= n) place = i;
+        if (sub != 0 || place >= k || i >= all) continue;
+        if (ranks > 1) store_remote(remote(best + rank * kTopMax + place, 0), e);
+        else put(e, place);
+      }
+      if (ranks > 1) {
+        cluster_barrier();
+        for (int i = rank == 0 ? tid : ranks * k; i < ranks * k; i += NT) {
+          const int from = i / k, at = i % k;
+          const uint64_t e = best[from * kTopMax + at];
+          if (e == 0) continue;
+          int place = at;  // and the entries of the other lists that come before it
+          for (int r2 = 0; r2 < ranks; ++r2) {
+            if (r2 == from) continue;
+            int lo = 0, hi = k;
+            while (lo < hi) {
+              const int mid = (lo + hi) / 2;
+              if (best[r2 * kTopMax + mid] > e) lo = mid + 1;
+              else hi = mid;
+            }
+            place += lo;
+          }
+          if (place < k) put(e, place);
+        }
+        cluster_barrier();  // rank 0 has read the lists before the next row's are written
+      } else {
+        __syncthreads();  // the list and the parts' maxima are free for the next row
+      }
+      for (int i = V + tid; rank == 0 && i < k; i += NT) {  // fewer entries than alternatives asked for
+        g.top_idx[t * k + i] = -1;
+        g.top_logp[t * k + i] = ninf();
+      }
+    }
+  }
+  ring.finish();
+}
+
+// The gradient, elementwise: a CTA takes parts of rows.
+template <typename T, bool kEntropy, typename L>
+__global__ void __launch_bounds__(L::NT, L::kCtas) logprobs_bwd_kernel(const p24_logprobs_args g, int parts, int* status) {
+  using R = Ring<T, L>;
+  constexpr int NT = L::NT;
+  constexpr int N = Vec<T>::N;
+  extern __shared__ __align__(128) uint4 ring_data[];
+  __shared__ RingShared<L::S> ring_sh;
+  const int tid = threadIdx.x, V = static_cast<int>(g.V), part = blockIdx.x % parts;
+  const float tau = g.temperature, c1 = 1.f / tau;
+  const T* logits = static_cast<const T*>(g.logits);
+  struct Row {
+    int tok;
+    float m, ls, dl, dh, H, edge;
+  };
+  const int stages = row_stages(V / N, parts, L::kStage);
+  R ring{logits, g.ldz, blockIdx.x / parts, gridDim.x / parts, g.T, V, part, parts, stages, 1, ring_data, &ring_sh, status};
+  ring.start();
+  auto row_of = [&](int64_t t) {
+    Row r;
+    r.tok = g.tokens ? g.tokens[t] : -1;
+    if (r.tok >= V) r.tok = -1;
+    r.m = g.stats[2 * t];
+    r.ls = g.stats[2 * t + 1];
+    r.dl = g.dlogp ? g.dlogp[t] : 0.f;
+    r.dh = kEntropy ? g.dentropy[t] : 0.f;
+    r.H = kEntropy ? g.entropy[t] : 0.f;
+    r.edge = load_edge(RowPart<T>(logits + t * g.ldz, V, part, parts), true);
+    return r;
+  };
+  Row row = row_of(ring.first);
+  int64_t r = 0;
+  for (int64_t t = ring.first; t < g.T; t += ring.step, ++r) {
+    const RowPart<T> p(logits + t * g.ldz, V, part, parts);
+    const Row now = row;
+    if (t + ring.step < g.T) row = row_of(t + ring.step);
+    T* out = static_cast<T*>(g.dlogits) + t * g.ldd;
+    const bool aligned = (reinterpret_cast<uintptr_t>(out) & 15u) == (reinterpret_cast<uintptr_t>(p.row) & 15u);
+    const bool none = now.ls == ninf();  // a row with nothing above -inf
+    const float m = none ? 0.f : now.m, ls = none ? 0.f : now.ls;
+    const float dl = (!none && now.tok >= 0) ? now.dl * c1 : 0.f;
+    const float dh = (kEntropy && !none) ? now.dh * c1 : 0.f;
+    const float k0 = kEntropy ? -(dl + dh * now.H) : -dl;  // dz = p (k0 - dh ln p) + dl delta
+    const F2 m2 = f2(-m, -m), c2 = f2(c1, c1), ls2 = f2(-ls, -ls), e2 = f2(kLog2e, kLog2e);
+    auto grad = [&](F2 z) {
+      F2 lp = fma2(add2(z, m2), c2, ls2);
+      if constexpr (kEntropy) {
+        float a, b;
+        split(lp, a, b);
+        lp = f2(floored(a), floored(b));
+      }
+      const F2 q = ex2x2(mul2(lp, e2));
+      return mul2(q, kEntropy ? fma2(f2(-dh, -dh), lp, f2(k0, k0)) : f2(k0, k0));
+    };
+    if (tid < p.edges) {
+      const int pos = p.edge_pos(tid);
+      float y, unused;
+      split(grad(f2(now.edge, now.edge)), y, unused);
+      out[pos] = static_cast<T>(y + (pos == now.tok ? dl : 0.f));
+    }
+    for (int at = 0; at < stages; ++at) {
+      const uint4* data = ring.wait();
+      const int n = p.hi - p.lo - at * L::kStage;
+      R::each(data, n, [&](const uint4& x, int u) {
+        F2 y[N / 2];
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) y[j] = grad(pair<T>(x, j));
+        const int i0 = p.vec_pos(p.lo + at * L::kStage + u * NT + tid);
+        if (now.tok >= i0 && now.tok < i0 + N) {
+#pragma unroll
+          for (int j = 0; j < N / 2; ++j)
+            y[j] = add2(y[j], f2(now.tok == i0 + 2 * j ? dl : 0.f, now.tok == i0 + 2 * j + 1 ? dl : 0.f));
+        }
+        store_vec(out, i0, aligned, pack_vec<T>(y));
+      });
+      ring.release(r, at);
+    }
+  }
+  ring.finish();
+}
+
+template <typename T, bool kEntropy, bool kTop>
+cudaError_t launch_logprobs_as(const p24_logprobs_args& g, int* status, cudaStream_t s) {
+  using L = std::conditional_t<kTop, Long, LongPlain>;
+  const int64_t vecs = g.V / Vec<T>::N;
+  auto smem = [&](auto layout, int ranks) {
+    using M = decltype(layout);
+    return M::kRing + (kTop ? sizeof(TopShared<M::NT>) + (ranks > 1 ? ranks * kTopMax * sizeof(uint64_t) : 0) : 0);
+  };
+  if (vecs <= kShortRow && g.T > sm_count())
+    return launch_rows(logprobs_kernel<T, kEntropy, kTop, Short>, Short::NT, g.T, 1, smem(Short(), 1), s, g, status);
+  const int ranks = row_ranks<L>(1, g.T, vecs);
+  return launch_rows(logprobs_kernel<T, kEntropy, kTop, L>, L::NT, g.T, ranks, smem(L(), ranks), s, g, status);
+}
+
+template <typename T, bool kEntropy>
+cudaError_t launch_logprobs_bwd_as(const p24_logprobs_args& g, int* status, cudaStream_t s) {
+  const int64_t vecs = g.V / Vec<T>::N;
+  if (vecs <= kShortRow)
+    return launch_parts(logprobs_bwd_kernel<T, kEntropy, Short>, Short::NT, g.T, 1, Short::kRing, s, g, 1, status);
+  const int parts = row_parts<LongGrad>(g.T, vecs);
+  return launch_parts(logprobs_bwd_kernel<T, kEntropy, LongGrad>, LongGrad::NT, g.T, parts, LongGrad::kRing, s, g, parts,
+                      status);
+}
+
+template <typename T>
+cudaError_t launch_logprobs_type(const p24_logprobs_args& g, int* st, cudaStream_t s) {
+  if (g.k > 0) return g.entropy ? launch_logprobs_as<T, true, true>(g, st, s) : launch_logprobs_as<T, false, true>(g, st, s);
+  return g.entropy ? launch_logprobs_as<T, true, false>(g, st, s) : launch_logprobs_as<T, false, false>(g, st, s);
+}
+
+}  // namespace
+
+cudaError_t launch_logprobs(const p24_logprobs_args& g, int* status, cudaStream_t s) {
+  return g.dtype == P24_BF16 ? launch_logprobs_type<__nv_bfloat16>(g, status, s) : launch_logprobs_type<float>(g, status, s);
+}
+
+cudaError_t launch_logprobs_bwd(const p24_logprobs_args& g, int* status, cudaStream_t s) {
+  if (g.dtype == P24_BF16)
+    return g.dentropy ? launch_logprobs_bwd_as<__nv_bfloat16, true>(g, status, s)
+                      : launch_logprobs_bwd_as<__nv_bfloat16, false>(g, status, s);
+  return g.dentropy ? launch_logprobs_bwd_as<float, true>(g, status, s) : launch_logprobs_bwd_as<float, false>(g, status, s);
+}
+
+}  // namespace p24

@@ -123,6 +123,67 @@ void step_layout(int64_t M, int64_t d, int64_t ffn, uint32_t flags, int64_t r, c
 std::atomic<uint64_t> g_launches{0};
 void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 
+int sm_count() {
+  static const int n = [] {
+    int dev = 0, v = 0;
+    return cudaGetDevice(&dev) == cudaSuccess &&
+                   cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess
+               ? v
+               : 152;
+  }();
+  return n;
+}
+
+cudaError_t row_kernel_slots(const void* kern, int NT, int ranks, size_t smem, int* slots) {
+  struct Known {
+    const void* kern;
+    size_t smem;
+    int dev, ranks, slots;
+  };
+  constexpr int kKnown = 256;  // more than that are looked up every time
+  static std::mutex lock;
+  static Known known[kKnown];
+  static int n = 0;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const std::lock_guard<std::mutex> hold(lock);
+  for (int i = 0; i < n; ++i)
+    if (known[i].kern == kern && known[i].ranks == ranks && known[i].smem == smem && known[i].dev == dev) {
+      *slots = known[i].slots;
+      return cudaSuccess;
+    }
+  cudaFuncAttributes fa;
+  int most = 0;
+  if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           most - static_cast<int>(fa.sharedSizeBytes));
+  if (e != cudaSuccess) return e;
+  int found = 0;
+  if (ranks == 1) {
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&found, kern, NT, smem);
+    found *= sm_count();
+  } else {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ranks));
+    cfg.blockDim = dim3(static_cast<unsigned>(NT));
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(ranks);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&found, kern, &cfg);
+  }
+  if (e != cudaSuccess) return e;
+  if (found < 1) return cudaErrorInvalidConfiguration;
+  if (n < kKnown) known[n++] = Known{kern, smem, dev, ranks, found};
+  *slots = found;
+  return cudaSuccess;
+}
+
 int* device_status_ptr() {
   // the status word's device address, looked up once per device
   constexpr int kDevs = 64;
@@ -746,7 +807,9 @@ int p24_token_logprobs(const p24_logprobs_args* a, void* stream) {
   if (a->k > 0 ? !(a->top_logp && a->top_idx) : (a->top_logp || a->top_idx)) return P24_EINVAL;
   if (!a->logp && !a->entropy && !a->stats && a->k == 0) return P24_EINVAL;
   if (!all_aligned4({a->tokens, a->logp, a->entropy, a->stats, a->top_logp, a->top_idx})) return P24_EALIGN;
-  return cuda_status(launch_logprobs(*a, as_stream(stream)));
+  int* st = device_status_ptr();
+  if (!st) return P24_ECUDA;
+  return cuda_status(launch_logprobs(*a, st, as_stream(stream)));
 }
 
 int p24_token_logprobs_bwd(const p24_logprobs_args* a, void* stream) {
@@ -758,7 +821,9 @@ int p24_token_logprobs_bwd(const p24_logprobs_args* a, void* stream) {
   if (!a->stats || (a->dlogp && !a->tokens) || (a->dentropy && !a->entropy)) return P24_EINVAL;
   if (a->dlogits == a->logits && a->ldd != a->ldz) return P24_EINVAL;
   if (!all_aligned4({a->tokens, a->entropy, a->stats, a->dlogp, a->dentropy})) return P24_EALIGN;
-  return cuda_status(launch_logprobs_bwd(*a, as_stream(stream)));
+  int* st = device_status_ptr();
+  if (!st) return P24_ECUDA;
+  return cuda_status(launch_logprobs_bwd(*a, st, as_stream(stream)));
 }
 
 namespace {
@@ -787,13 +852,17 @@ int check_distill(const p24_distill_args* a, bool forward) {
 int p24_distill_topk(const p24_distill_args* a, void* stream) {
   P24_TRY(check_distill(a, true));
   if (a->T == 0) return P24_OK;
-  return cuda_status(launch_distill(*a, as_stream(stream)));
+  int* st = device_status_ptr();
+  if (!st) return P24_ECUDA;
+  return cuda_status(launch_distill(*a, st, as_stream(stream)));
 }
 
 int p24_distill_topk_bwd(const p24_distill_args* a, void* stream) {
   P24_TRY(check_distill(a, false));
   if (a->T == 0) return P24_OK;
-  return cuda_status(launch_distill_bwd(*a, as_stream(stream)));
+  int* st = device_status_ptr();
+  if (!st) return P24_ECUDA;
+  return cuda_status(launch_distill_bwd(*a, st, as_stream(stream)));
 }
 
 int p24_selftest_timeout(int64_t limit_ns, void* stream) {

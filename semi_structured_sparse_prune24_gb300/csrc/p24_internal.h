@@ -101,17 +101,24 @@ cudaError_t launch_hyb_spmm(const p24_hybrid& h, const void* B, int64_t N, int64
 cudaError_t launch_hyb_sddmm(const p24_hybrid& h, const void* G, int64_t N, int64_t ldg, const void* B, int64_t ldb,
                              void* S_ell, void* S_ovf, int64_t lds, cudaStream_t s);
 
-// ---- the language-model head's row operators (head_kernels.cu); arguments checked by the caller, T > 0
-cudaError_t launch_logprobs(const p24_logprobs_args& g, cudaStream_t s);
-cudaError_t launch_logprobs_bwd(const p24_logprobs_args& g, cudaStream_t s);
-cudaError_t launch_distill(const p24_distill_args& g, cudaStream_t s);      // loss; with dlogits also the gradient
-cudaError_t launch_distill_bwd(const p24_distill_args& g, cudaStream_t s);
+// ---- the language-model head's row operators (logprobs_kernels.cu, distill_kernels.cu); arguments
+// checked by the caller, T > 0
+cudaError_t launch_logprobs(const p24_logprobs_args& g, int* status, cudaStream_t s);
+cudaError_t launch_logprobs_bwd(const p24_logprobs_args& g, int* status, cudaStream_t s);
+cudaError_t launch_distill(const p24_distill_args& g, int* status, cudaStream_t s);  // loss; with dlogits also the gradient
+cudaError_t launch_distill_bwd(const p24_distill_args& g, int* status, cudaStream_t s);
 
 // A 2-D tensor map over a row-major matrix, for the HBM-bound kernels' TMA staging:
 // `inner` columns of `outer` rows, boxes of box_inner x box_outer; swizzle128 lays each
 // 128-byte box row out with the 128B swizzle (box_inner x element size must be 128).
 bool make_tensor_map_2d(CUtensorMap* m, bool bf16, const void* base, uint64_t inner, uint64_t outer,
                         uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, bool swizzle128 = false);
+
+int sm_count();  // SMs of the current device (of the first one asked about)
+// How many clusters of `ranks` CTAs of NT threads and `smem` dynamic bytes of a kernel run at once
+// on the current device. Also lets the kernel take that much shared memory. Looked up once for
+// each kernel, cluster size and amount.
+cudaError_t row_kernel_slots(const void* kern, int NT, int ranks, size_t smem, int* slots);
 
 int* device_status_ptr();  // the status word of the current device
 

@@ -308,6 +308,41 @@ def test_distill(P, dtype, T, V, K, pad, tail, mode):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,V,K,pad", [(2, 300001, 40, 0), (170, 40003, 12, 0), (30, 80000, 24, 5), (400, 1000, 128, 0)])
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("mode", ["step", "bwd"])
+def test_distill_long_rows_and_many_rows(P, dtype, T, V, K, pad, tail, mode):
+    """Rows longer than a cluster's registers, rows split over CTAs, more rows than fit at once."""
+    z, rng = logits(T, V, dtype, T + V, pad=pad)
+    idx, val = teacher_list(rng, T, V, K)
+    labels = rng.integers(0, V, T)
+    w = f64(dev(rng.random(T), F32))
+    check_distill(P, z, idx, val, labels, [1.0, 1.5][T % 4 == 2], tail, w, w[::-1].copy(), mode, inplace=tail)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,V,k", [(2, 300001, 100), (400, 40003, 64), (500, 1000, 128), (160, 70000, 7)])
+def test_score_long_rows_and_many_rows(P, dtype, T, V, k):
+    z, rng = logits(T, V, dtype, T + V)
+    check_score(P, z, rng.integers(0, V, T), k, 1.0)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("gap", [60.0, 300.0])
+@pytest.mark.parametrize("mode", ["step", "bwd"])
+def test_distill_bucket_far_below_the_list(P, dtype, gap, mode):
+    """The list holds all but exp(-gap) of the student: p_r underflows, q_r / p_r would overflow,
+    and the bucket's loss and gradient are still finite and right."""
+    z, rng = logits(3, 5000, dtype, 33, peak=False)
+    idx, val = teacher_list(rng, 3, 5000, 4)
+    idx[:] = np.array([7, 100, 2500, 4999])
+    z[:, torch.as_tensor(idx[0], device="cuda")] += gap
+    w = np.ones(3)
+    o, ref = check_distill(P, z, idx, val, None, 1.0, True, w, None, mode)
+    assert np.all(np.isfinite(ref["kl"])) and np.abs(ref["dlogits"]).max() > 0.01
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("tau", [1.0, 2.0])
 @pytest.mark.parametrize("tail", [False, True])
 def test_distill_without_a_list_is_cross_entropy(P, dtype, tau, tail):
