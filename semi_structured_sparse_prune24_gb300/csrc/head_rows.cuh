@@ -100,23 +100,6 @@ __device__ __forceinline__ uint4 fill_vec() {
   return make_uint4(Vec<T>::kFill, Vec<T>::kFill, Vec<T>::kFill, Vec<T>::kFill);
 }
 
-// The vector with the elements whose bits are set replaced by -inf.
-template <typename T>
-__device__ __forceinline__ uint4 without(uint4 r, uint32_t bits) {
-  uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (sizeof(T) == 2) {
-      const uint32_t b = bits >> (2 * i);
-      const uint32_t m = ((b & 1u) ? 0xffffu : 0u) | ((b & 2u) ? 0xffff0000u : 0u);
-      w[i] = (w[i] & ~m) | (Vec<T>::kFill & m);
-    } else {
-      if ((bits >> i) & 1u) w[i] = Vec<T>::kFill;
-    }
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 // Element pairs j of a vector as fp32: j < N / 2.
 template <typename T>
 __device__ __forceinline__ F2 pair(const uint4& r, int j) {
@@ -338,32 +321,80 @@ __device__ __forceinline__ void cluster_barrier() {
 }
 
 struct JoinShared {
-  Sums warp[2][16];           // by row parity: the warps' sums
-  Sums rank[2][kMaxRanks];    // and the cluster's CTAs'
+  Sums warp[2][2][16];         // by row parity and sum: the warps'
+  Sums rank[2][2][kMaxRanks];  // and the cluster's CTAs'
+  uint64_t arrived[2];         // a row's CTAs have written theirs
 };
 
-// The row's sums, in every thread of every CTA of its cluster; also a barrier of all of them.
-// `par` alternates from call to call, which keeps one row's reads apart from the next one's
-// writes: a CTA writes parity p again only two barriers later.
-template <bool kEntropy, int NT>
-__device__ __forceinline__ Sums row_join(Sums u, float c, JoinShared& sh, int par, int rank, int ranks) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// One thread, before the CTA's (or the cluster's) first barrier.
+__device__ __forceinline__ void join_init(JoinShared& sh, int ranks) {
+  for (int i = 0; i < 2; ++i) mbar_init(&sh.arrived[i], ranks);
+}
+
+// Bounded wait for a phase that threads of other CTAs of the cluster complete.
+__device__ __forceinline__ void wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
+  const uint32_t a = smem_u32(bar);
+  uint64_t t0 = 0;
+  for (uint32_t i = 0;; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(a), "r"(parity)
+        : "memory");
+    if (ok) return;
+    if (i == 0) t0 = global_ns();
+    if ((i & 255u) == 255u) {
+      if (*abort) return;
+      if (global_ns() - t0 > P24_WAIT_NS) {
+        *abort = 1;
+        p24_record_timeout(status, bar);
+        return;
+      }
+    }
+  }
+}
+
+// The sums of row r of a CTA, in each of its NT threads that call it (barrier 1 is theirs), and
+// over all CTAs of its cluster. kTwo: of two kinds at once. Buffers and barriers take turns from
+// row to row: a CTA writes to one of them again only when every CTA is past the row between.
+template <bool kEntropy, bool kTwo, int NT>
+__device__ __forceinline__ void row_join(Sums& u, float c, Sums& v, float cv, JoinShared& sh, int64_t r, int rank, int ranks,
+                                         volatile int* abort, int* status) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, par = r & 1;
   u = warp_join<kEntropy>(u, c);
-  if (lane == 0) sh.warp[par][warp] = u;
-  __syncthreads();
-  u = warp_join<kEntropy, NT / 32>(sh.warp[par][lane % (NT / 32)], c);
+  if (kTwo) v = warp_join<false>(v, cv);
+  if (lane == 0) {
+    sh.warp[par][0][warp] = u;
+    if (kTwo) sh.warp[par][1][warp] = v;
+  }
+  named_bar_sync(1, NT);
+  // NT / 32 parts, or the next power of two with empty ones
+  constexpr int kWarps = NT / 32, kParts = kWarps <= 4 ? 4 : kWarps <= 8 ? 8 : 16;
+  const Sums none{ninf(), 0.f, 0.f};
+  const int from = lane % kParts;
+  u = warp_join<kEntropy, kParts>(from < kWarps ? sh.warp[par][0][from] : none, c);
+  if (kTwo) v = warp_join<false, kParts>(from < kWarps ? sh.warp[par][1][from] : none, cv);
   if (ranks > 1) {
     if (warp == 0 && lane < ranks) {
-      const uint32_t to = remote(&sh.rank[par][rank], lane);
+      const uint32_t to = remote(&sh.rank[par][0][rank], lane);
       store_remote(to, u.m);
       store_remote(to + 4, u.s);
       if constexpr (kEntropy) store_remote(to + 8, u.a);
+      if (kTwo) {
+        const uint32_t to1 = remote(&sh.rank[par][1][rank], lane);
+        store_remote(to1, v.m);
+        store_remote(to1 + 4, v.s);
+      }
+      asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote(&sh.arrived[par], lane)) : "memory");
     }
-    cluster_barrier();
-    u = lane % kMaxRanks < ranks ? sh.rank[par][lane % kMaxRanks] : Sums{ninf(), 0.f, 0.f};
-    u = warp_join<kEntropy, kMaxRanks>(u, c);
+    wait_cluster(&sh.arrived[par], (r >> 1) & 1, abort, status);
+    const int i = lane % kMaxRanks;
+    u = warp_join<kEntropy, kMaxRanks>(i < ranks ? sh.rank[par][0][i] : none, c);
+    if (kTwo) v = warp_join<false, kMaxRanks>(i < ranks ? sh.rank[par][1][i] : none, cv);
   }
-  return u;
 }
 
 // ---------------------------------------------------------------- the ring
@@ -402,10 +433,17 @@ struct Ring {
       return;
     }
     mbar_arrive_expect_tx(&sh->full[to], n * 16u);
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                     smem_u32(data + to * L::kStage)),
-                 "l"(p.body + v), "r"(n * 16u), "r"(smem_u32(&sh->full[to]))
-                 : "memory");
+    // what is read for the last time need not stay in L2, what comes again should
+    uint64_t policy;
+    if (at + stages < stages * visits)
+      asm("createpolicy.fractional.L2::evict_last.b64 %0;" : "=l"(policy));
+    else
+      asm("createpolicy.fractional.L2::evict_first.b64 %0;" : "=l"(policy));
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+            smem_u32(data + to * L::kStage)),
+        "l"(p.body + v), "r"(n * 16u), "r"(smem_u32(&sh->full[to])), "l"(policy)
+        : "memory");
   }
 
   // All threads; ends with a barrier.
@@ -428,7 +466,7 @@ struct Ring {
   }
 
   // The next stage's data, once it is there: vector u of this thread is at u * L::NT.
-  __device__ __forceinline__ const uint4* wait() {
+  __device__ __forceinline__ uint4* wait() {
     p24_wait(&sh->full[slot], parity, &sh->abort, status);
     return data + slot * L::kStage + threadIdx.x;
   }
@@ -548,18 +586,17 @@ cudaError_t launch_rows(void (*kern)(KArgs...), int NT, int64_t rows, int ranks,
   return e;
 }
 
-// An elementwise kernel's CTAs take parts of rows: enough of them that every SM has its CTAs.
-template <typename L>
-int row_parts(int64_t T, int64_t vecs) {
-  int parts = 1;
-  while (T * parts < sm_count() * L::kCtas && vecs >= 2 * L::NT * parts) parts *= 2;
-  return parts;
-}
-// The CTAs of a row whose loss is wanted: more than one only where rows are few.
-template <typename L>
-int row_ranks(int ranks, int64_t T, int64_t vecs) {
-  while (ranks < kMaxRanks && T * ranks * 2 <= sm_count() * L::kCtas && vecs >= L::NT * ranks) ranks *= 2;
-  return ranks;
+// Over how many CTAs (a power of two up to `most`) to split rows of `vecs` vectors, T of them on
+// `slots` CTAs at a time: the rows of the last round leave CTAs idle, and each share costs as much
+// as `fixed` vectors beside its own.
+inline int row_split(int64_t T, int64_t vecs, int64_t slots, int most, int64_t fixed) {
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int n = 1; n <= most && (n == 1 || vecs >= n * int64_t(128)); n *= 2) {
+    const int64_t cost = (T * n + slots - 1) / slots * (vecs / n + fixed);
+    if (cost < least) least = cost, best = n;
+  }
+  return best;
 }
 // As launch_rows, over T rows in `parts` parts: CTA b takes part b % parts of rows.
 template <typename... KArgs, typename... Args>

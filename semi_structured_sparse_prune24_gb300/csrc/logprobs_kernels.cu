@@ -330,13 +330,13 @@ __global__ void __launch_bounds__(L::NT, L::kCtas) logprobs_kernel(const p24_log
   int shift = 0;  // stages to a part of the second look, a power of two
   while (kTop && (stages - 1) >> shift >= kParts) ++shift;
   R ring{logits, g.ldz, blockIdx.x / ranks, gridDim.x / ranks, g.T, V, rank, ranks, stages, 1, ring_data, &ring_sh, status};
+  if (tid == 0) join_init(joins, ranks);
   ring.start();
   if (ranks > 1) cluster_barrier();  // every CTA runs before another writes to its shared memory
 
   float edge = load_edge(RowPart<T>(logits + ring.first * g.ldz, V, rank, ranks), true);
   int64_t r = 0;
   for (int64_t t = ring.first; t < g.T; t += ring.step, ++r) {
-    const int par = r & 1;
     const RowPart<T> p(logits + t * g.ldz, V, rank, ranks);
     float z_tok = 0.f;
     bool has_tok = false;
@@ -368,7 +368,8 @@ __global__ void __launch_bounds__(L::NT, L::kCtas) logprobs_kernel(const p24_log
     }
     const float own_max = w.m;
     const bool own = p.lo + tid < p.hi || tid < p.edges;
-    const Sums u = row_join<kEntropy, NT>(w.sums(), c, joins, par, rank, ranks);
+    Sums u = w.sums(), unused{0.f, 0.f, 0.f};
+    row_join<kEntropy, false, NT>(u, c, unused, c, joins, r, rank, ranks, &ring_sh.abort, status);
     const float ls = u.s == 0.f ? ninf() : logf(u.s);
     // ln of the probability of a logit; a row with nothing above -inf has none
     auto logp = [&](float z) { return u.s == 0.f ? ninf() : (z - u.m) / tau - ls; };
@@ -526,7 +527,7 @@ cudaError_t launch_logprobs_as(const p24_logprobs_args& g, int* status, cudaStre
   };
   if (vecs <= kShortRow && g.T > sm_count())
     return launch_rows(logprobs_kernel<T, kEntropy, kTop, Short>, Short::NT, g.T, 1, smem(Short(), 1), s, g, status);
-  const int ranks = row_ranks<L>(1, g.T, vecs);
+  const int ranks = row_split(g.T, vecs, sm_count() * L::kCtas, kMaxRanks, 1024);
   return launch_rows(logprobs_kernel<T, kEntropy, kTop, L>, L::NT, g.T, ranks, smem(L(), ranks), s, g, status);
 }
 
@@ -535,7 +536,7 @@ cudaError_t launch_logprobs_bwd_as(const p24_logprobs_args& g, int* status, cuda
   const int64_t vecs = g.V / Vec<T>::N;
   if (vecs <= kShortRow)
     return launch_parts(logprobs_bwd_kernel<T, kEntropy, Short>, Short::NT, g.T, 1, Short::kRing, s, g, 1, status);
-  const int parts = row_parts<LongGrad>(g.T, vecs);
+  const int parts = row_split(g.T, vecs, sm_count() * LongGrad::kCtas, 64, 256);
   return launch_parts(logprobs_bwd_kernel<T, kEntropy, LongGrad>, LongGrad::NT, g.T, parts, LongGrad::kRing, s, g, parts,
                       status);
 }
