@@ -81,9 +81,10 @@ __device__ __forceinline__ void list_row(const p24_distill_args& g, int64_t t, c
     z[i] = on && (!own || p.owns(r.idx[i])) ? to_f32(p.row[r.idx[i]]) : ninf();
     q[i] = on ? r.val[i] : ninf();
     vtop = fmaxf(vtop, q[i]);
-    ztop = fmaxf(ztop, z[i]);
     listed |= on && r.idx[i] == label;
   }
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) ztop = fmaxf(ztop, z[i]);
   vtop = warp_max(vtop);
   ztop = warp_max(ztop);
   float sum = 0.f, s = 0.f;
@@ -153,9 +154,9 @@ __device__ __forceinline__ RowGrad row_grad(const ListShared& sh, bool two, floa
   return r;
 }
 
-// The gradient's terms off the list over the stages of a row, whose first is stage `from` of the row's sequence.
+// The gradient's terms off the list, over the next stages of the ring: those of a row.
 template <typename T, bool kTwo, typename R>
-__device__ __forceinline__ void store_row(R& ring, int64_t r, int from, T* out, bool aligned, const RowPart<T>& p, int stages,
+__device__ __forceinline__ void store_row(R& ring, T* out, bool aligned, const RowPart<T>& p, int stages,
                                           const Terms& terms) {
   constexpr int N = Vec<T>::N, NT = R::kThreads;
   for (int at = 0; at < stages; ++at) {
@@ -167,7 +168,7 @@ __device__ __forceinline__ void store_row(R& ring, int64_t r, int from, T* out, 
       for (int j = 0; j < N / 2; ++j) y[j] = terms.template two<kTwo>(pair<T>(x, j));
       store_vec(out, p.vec_pos(v0 + u * NT), aligned, pack_vec<T>(y));
     });
-    ring.release(r, from + at);
+    ring.release();
   }
 }
 
@@ -184,8 +185,8 @@ __device__ __forceinline__ void store_listed(T* out, const RowPart<T>& p, const 
   }
 }
 
-using Loss = Layout<256, 4, 4, 2>;
-using Step = Layout<384, 2, 4, 3>;
+using Loss = Layout<192, 4, 4, 4>;
+using Step = Layout<256, 3, 4, 4>;
 using Grad = Layout<256, 4, 4, 3>;
 using Short = Layout<128, 6, 2, 4>;  // rows of up to kShortRow vectors
 constexpr int kShortRow = 1024;
@@ -258,9 +259,10 @@ __device__ __forceinline__ void store_loss(const p24_distill_args& g, int64_t t,
 }
 
 // kGrad: with the gradient. kTwo: the label's softmax (temperature 1) differs from the list's.
-// The CTA's last warp prepares the lists and stores the losses, the others walk the rows.
+// The CTA's last warp prepares the lists and stores the losses, the one before it fills the ring,
+// the others walk the rows.
 template <typename T, bool kTwo, bool kGrad, typename L>
-__global__ void __launch_bounds__(L::NT + 32, L::kCtas) distill_kernel(const p24_distill_args g, int* status) {
+__global__ void __launch_bounds__(L::kThreads + 32, L::kCtas) distill_kernel(const p24_distill_args g, int* status) {
   using R = Ring<T, L>;
   constexpr int NT = L::NT, N = Vec<T>::N;
   extern __shared__ __align__(128) uint4 ring_data[];
@@ -287,11 +289,13 @@ __global__ void __launch_bounds__(L::NT + 32, L::kCtas) distill_kernel(const p24
     }
   }
   if (tail)
-    for (int i = tid; i < 2 * stages * L::kWarps; i += NT + 32) heads[i] = -1;
+    for (int i = tid; i < 2 * stages * L::kWarps; i += L::kThreads + 32) heads[i] = -1;
   ring.start();
   if (ranks > 1) cluster_barrier();  // every CTA runs before another writes to its shared memory
 
   if (warp == L::kWarps) {
+    if (tid == NT) ring.run();
+  } else if (warp == L::kWarps + 1) {
     auto prepare = [&](int64_t r) {
       const int64_t t = ring.first + r * ring.step;
       if (t >= g.T) return;
@@ -362,7 +366,7 @@ __global__ void __launch_bounds__(L::NT + 32, L::kCtas) distill_kernel(const p24
         if (!kTwo || tail) R::each(data, n, [&](const uint4& x, int) { mr = max_vec<T>(mr, x); });
         w.raise(max_of<T>(mr), c);
         R::each(data, n, [&](const uint4& x, int) { w.template add<T>(x, c); });
-        ring.release(r, at);
+        ring.release();
       }
 
       Sums rest = w.sums(), one = w1.sums();
@@ -382,19 +386,19 @@ __global__ void __launch_bounds__(L::NT + 32, L::kCtas) distill_kernel(const p24
         const bool aligned = (reinterpret_cast<uintptr_t>(out) & 15u) == (reinterpret_cast<uintptr_t>(p.row) & 15u);
         const RowGrad rg = row_grad(sh, kTwo, tau, st.m, st.ls, st.lr, st.l1);
         if (tid < p.edges) out[p.edge_pos(tid)] = static_cast<T>(rg.off.template one<kTwo>(edge_here));
-        store_row<T, kTwo, R>(ring, r, stages, out, aligned, p, stages, rg.off);
-        named_bar_sync(1, NT);
+        store_row<T, kTwo, R>(ring, out, aligned, p, stages, rg.off);
+        walk_sync<NT>();
         store_listed<T, kTwo, NT>(out, p, sh, K, rg);
       }
       __syncwarp();
       if ((tid & 31) == 0) mbar_arrive(&hand.freed[par]);
     }
   }
-  ring.finish();
 }
 
+// The gradient from saved statistics. The CTA's last warp fills the ring, the others walk the rows.
 template <typename T, bool kTwo, typename L>
-__global__ void __launch_bounds__(L::NT, L::kCtas) distill_bwd_kernel(const p24_distill_args g, int parts, int* status) {
+__global__ void __launch_bounds__(L::kThreads, L::kCtas) distill_bwd_kernel(const p24_distill_args g, int parts, int* status) {
   using R = Ring<T, L>;
   constexpr int NT = L::NT, N = Vec<T>::N;
   extern __shared__ __align__(128) uint4 ring_data[];
@@ -407,6 +411,10 @@ __global__ void __launch_bounds__(L::NT, L::kCtas) distill_bwd_kernel(const p24_
   const int stages = row_stages(V / N, parts, L::kStage);
   R ring{logits, g.ldz, blockIdx.x / parts, gridDim.x / parts, g.T, V, part, parts, stages, 1, ring_data, &ring_sh, status};
   ring.start();
+  if (tid >= NT) {
+    if (tid == NT) ring.run();
+    return;
+  }
   float edge = load_edge(RowPart<T>(logits + ring.first * g.ldz, V, part, parts), true);
   int64_t r = 0;
   for (int64_t t = ring.first; t < g.T; t += ring.step, ++r) {
@@ -417,17 +425,16 @@ __global__ void __launch_bounds__(L::NT, L::kCtas) distill_bwd_kernel(const p24_
       ListRegs list;
       list_row(g, t, p, true, sh, list);  // another part's logits are being overwritten, in place
     }
-    __syncthreads();
+    walk_sync<NT>();
     T* out = static_cast<T*>(g.dlogits) + t * g.ldd;
     const bool aligned = (reinterpret_cast<uintptr_t>(out) & 15u) == (reinterpret_cast<uintptr_t>(p.row) & 15u);
     const RowGrad rg = row_grad(sh, kTwo, tau, st.m, st.ls, st.lr, st.l1);
     if (tid < p.edges) out[p.edge_pos(tid)] = static_cast<T>(rg.off.template one<kTwo>(edge));
     if (t + ring.step < g.T) edge = load_edge(RowPart<T>(logits + (t + ring.step) * g.ldz, V, part, parts), true);
-    store_row<T, kTwo, R>(ring, r, 0, out, aligned, p, stages, rg.off);
-    __syncthreads();
+    store_row<T, kTwo, R>(ring, out, aligned, p, stages, rg.off);
+    walk_sync<NT>();
     store_listed<T, kTwo, NT>(out, p, sh, K, rg);
   }
-  ring.finish();
 }
 
 template <typename T, bool kTwo, bool kGrad>
@@ -440,22 +447,22 @@ cudaError_t launch_distill_as(const p24_distill_args& g, int* status, cudaStream
     return static_cast<size_t>(M::kRing + (tail ? 2 * row_stages(vecs, ranks, M::kStage) * M::kWarps * 4 : 0));
   };
   if (vecs <= kShortRow && g.T > sm_count())
-    return launch_rows(distill_kernel<T, kTwo, kGrad, Short>, Short::NT + 32, g.T, 1, smem(Short(), 1), s, g, status);
+    return launch_rows(distill_kernel<T, kTwo, kGrad, Short>, Short::kThreads + 32, g.T, 1, smem(Short(), 1), s, g, status);
   int ranks = 1;
   // the rows in flight stay in L2 until they come the second time
   constexpr int64_t kL2Rows = 64 << 20;
   while (kGrad && ranks < kMaxRanks && std::min<int64_t>(g.T, sm_count() * L::kCtas / ranks) * vecs * 16 > kL2Rows) ranks *= 2;
   ranks = std::max(ranks, row_split(g.T, vecs, sm_count() * L::kCtas, kMaxRanks, 1024));
-  return launch_rows(distill_kernel<T, kTwo, kGrad, L>, L::NT + 32, g.T, ranks, smem(L(), ranks), s, g, status);
+  return launch_rows(distill_kernel<T, kTwo, kGrad, L>, L::kThreads + 32, g.T, ranks, smem(L(), ranks), s, g, status);
 }
 
 template <typename T, bool kTwo>
 cudaError_t launch_distill_bwd_as(const p24_distill_args& g, int* status, cudaStream_t s) {
   const int64_t vecs = g.V / Vec<T>::N;
   if (vecs <= kShortRow)
-    return launch_parts(distill_bwd_kernel<T, kTwo, Short>, Short::NT, g.T, 1, Short::kRing, s, g, 1, status);
+    return launch_parts(distill_bwd_kernel<T, kTwo, Short>, Short::kThreads, g.T, 1, Short::kRing, s, g, 1, status);
   const int parts = row_split(g.T, vecs, sm_count() * Grad::kCtas, 64, 512);
-  return launch_parts(distill_bwd_kernel<T, kTwo, Grad>, Grad::NT, g.T, parts, Grad::kRing, s, g, parts, status);
+  return launch_parts(distill_bwd_kernel<T, kTwo, Grad>, Grad::kThreads, g.T, parts, Grad::kRing, s, g, parts, status);
 }
 
 template <typename T>

@@ -8,8 +8,7 @@
 //
 // A CTA's share of its rows comes through a ring of stages in shared memory, filled by bulk
 // copies (cp.async.bulk) that run ahead of the threads by the ring's length, over row ends too:
-// loads are under way while the CTA reduces, waits and stores. Measured against loads into
-// registers one stage ahead (16-byte loads, 64 registers): see the kernels' comments.
+// loads are under way while the CTA reduces, waits and stores.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -23,11 +22,12 @@
 namespace p24 {
 namespace {
 
-// How a kernel is laid out on an SM: kCtas CTAs of NT threads, each with a ring of S stages of SV
-// vectors per thread.
+// How a kernel is laid out on an SM: kCtas CTAs of NT threads that walk the rows and a warp that
+// fills their ring, of S stages of SV vectors per thread.
 template <int NT_, int kCtas_, int SV_, int S_>
 struct Layout {
   static constexpr int NT = NT_, kCtas = kCtas_, SV = SV_, S = S_, kWarps = NT_ / 32;
+  static constexpr int kThreads = NT + 32;
   static constexpr int kStage = NT * SV;          // vectors of a stage
   static constexpr int kRing = S * kStage * 16;   // bytes
 };
@@ -315,6 +315,11 @@ __device__ __forceinline__ void store_remote(uint32_t a, uint64_t x) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(x) : "memory");
 }
 
+// Arrive at the barrier `bar` of CTA `rank` of the cluster.
+__device__ __forceinline__ void arrive_remote(const uint64_t* bar, int rank) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote(bar, rank)) : "memory");
+}
+
 // Whole-cluster barrier that threads of a warp may reach apart.
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
@@ -357,7 +362,24 @@ __device__ __forceinline__ void wait_cluster(uint64_t* bar, uint32_t parity, vol
   }
 }
 
-// The sums of row r of a CTA, in each of its NT threads that call it (barrier 1 is theirs), and
+// Barrier of the NT threads of a CTA that walk its rows; and how many of them `on` holds for.
+template <int NT>
+__device__ __forceinline__ void walk_sync() {
+  named_bar_sync(1, NT);
+}
+template <int NT>
+__device__ __forceinline__ int walk_count(bool on) {
+  int n;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %1, 0;\n\t"
+      "bar.red.popc.u32 %0, 1, %2, p;\n\t}"
+      : "=r"(n)
+      : "r"(static_cast<int>(on)), "r"(NT)
+      : "memory");
+  return n;
+}
+
+// The sums of row r of a CTA, in each of the NT threads that walk it, and
 // over all CTAs of its cluster. kTwo: of two kinds at once. Buffers and barriers take turns from
 // row to row: a CTA writes to one of them again only when every CTA is past the row between.
 template <bool kEntropy, bool kTwo, int NT>
@@ -370,7 +392,7 @@ __device__ __forceinline__ void row_join(Sums& u, float c, Sums& v, float cv, Jo
     sh.warp[par][0][warp] = u;
     if (kTwo) sh.warp[par][1][warp] = v;
   }
-  named_bar_sync(1, NT);
+  walk_sync<NT>();
   // NT / 32 parts, or the next power of two with empty ones
   constexpr int kWarps = NT / 32, kParts = kWarps <= 4 ? 4 : kWarps <= 8 ? 8 : 16;
   const Sums none{ninf(), 0.f, 0.f};
@@ -388,7 +410,7 @@ __device__ __forceinline__ void row_join(Sums& u, float c, Sums& v, float cv, Jo
         store_remote(to1, v.m);
         store_remote(to1 + 4, v.s);
       }
-      asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote(&sh.arrived[par], lane)) : "memory");
+      arrive_remote(&sh.arrived[par], lane);
     }
     wait_cluster(&sh.arrived[par], (r >> 1) & 1, abort, status);
     const int i = lane % kMaxRanks;
@@ -398,17 +420,30 @@ __device__ __forceinline__ void row_join(Sums& u, float c, Sums& v, float cv, Jo
 }
 
 // ---------------------------------------------------------------- the ring
+// Whether a phase is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(const uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 template <int S>
 struct RingShared {
   uint64_t full[S];    // a stage's data has arrived
-  int done[S];         // warps that have finished reading it
-  int fills[S];        // times it was filled
+  uint64_t empty[S];   // every warp has read it
   int abort;           // a wait ran out (the device status word says so)
 };
 
 // The stages a CTA walks: for each of its rows (row r of it is row first + r step), `visits`
-// times the `stages` parts of L::kStage vectors of its share. Stage q of that sequence
-// sits in slot q % S; the last warp to finish a slot refills it with stage q + S.
+// times the `stages` parts of L::kStage vectors of its share. Stage q of that sequence sits in
+// slot q % S. A warp of its own fills the slots (one lane issues the copies), so that the others
+// only wait for data and say when they have read it.
 template <typename T, typename L>
 struct Ring {
   static constexpr int S = L::S, kStage = L::kStage, kThreads = L::NT;
@@ -418,63 +453,39 @@ struct Ring {
   uint4* data;
   RingShared<S>* sh;
   int* status;
-  int slot;            // of the next stage to read
-  uint32_t parity;
+  // the next stage: of the reading warps to read, of the filling one to fill
+  int slot = 0;
+  uint32_t parity = 0;
+  // the filling lane's: what is left of the current row's share, the visit of it, the row
+  const uint4* from = nullptr;
+  int left = 0, at = 0, visit = 0;
+  int64_t row = 0, fills = 0;
 
-  __device__ __forceinline__ void fill(int to, int64_t r, int at) const {
-    const int64_t t = first + r * step;
-    if (t >= rows || *reinterpret_cast<volatile int*>(&sh->abort)) return;
-    const RowPart<T> p(logits + t * ld, V, rank, ranks);
-    const int v = p.lo + (at < stages ? at : at - stages) * L::kStage;
-    const int n = min(p.hi - v, L::kStage);
-    ++sh->fills[to];
-    if (n <= 0) {  // rows of one matrix can differ by a vector: nothing to copy for this one
-      mbar_arrive(&sh->full[to]);
-      return;
-    }
-    mbar_arrive_expect_tx(&sh->full[to], n * 16u);
-    // what is read for the last time need not stay in L2, what comes again should
-    uint64_t policy;
-    if (at + stages < stages * visits)
-      asm("createpolicy.fractional.L2::evict_last.b64 %0;" : "=l"(policy));
-    else
-      asm("createpolicy.fractional.L2::evict_first.b64 %0;" : "=l"(policy));
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
-            smem_u32(data + to * L::kStage)),
-        "l"(p.body + v), "r"(n * 16u), "r"(smem_u32(&sh->full[to])), "l"(policy)
-        : "memory");
-  }
-
-  // All threads; ends with a barrier.
+  // All threads of the CTA; ends with a barrier.
   __device__ __forceinline__ void start() {
-    slot = 0;
-    parity = 0;
     if (threadIdx.x == 0) {
       sh->abort = 0;
       for (int i = 0; i < S; ++i) {
         mbar_init(&sh->full[i], 1);
-        sh->done[i] = 0;
-        sh->fills[i] = 0;
+        mbar_init(&sh->empty[i], L::kWarps);
       }
       fence_barrier_init();
       fence_proxy_async_smem();
     }
     __syncthreads();
-    if (threadIdx.x == 0)
-      for (int i = 0; i < S; ++i) fill(i, i / (stages * visits), i % (stages * visits));
   }
 
+  // ---- the reading warps
   // The next stage's data, once it is there: vector u of this thread is at u * L::NT.
   __device__ __forceinline__ uint4* wait() {
     p24_wait(&sh->full[slot], parity, &sh->abort, status);
-    return data + slot * L::kStage + threadIdx.x;
+    return data + slot * kStage + threadIdx.x;
   }
   // f(vector, u) for this thread's vectors of a stage that holds n (or, past the ring's stage
   // size, all of them).
   template <typename F>
   __device__ __forceinline__ static void each(const uint4* at, int n, F&& f) {
-    if (n >= L::kStage) {
+    if (n >= kStage) {
 #pragma unroll
       for (int u = 0; u < L::SV; ++u) f(at[u * L::NT], u);
     } else {
@@ -482,34 +493,74 @@ struct Ring {
       for (int u = 0; u * L::NT + static_cast<int>(threadIdx.x) < n; ++u) f(at[u * L::NT], u);
     }
   }
-  // This warp has read the current stage, stage `at` of row r: on to the next.
-  __device__ __forceinline__ void release(int64_t r, int at) {
-    const int of = slot;
+  // This warp has read the current stage: on to the next.
+  __device__ __forceinline__ void release() {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&sh->empty[slot]);
+    advance();
+  }
+  __device__ __forceinline__ void advance() {
     if (++slot == S) {
       slot = 0;
       parity ^= 1;
     }
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) {
-      int before;
-      asm volatile("atom.acq_rel.cta.shared::cta.add.s32 %0, [%1], 1;" : "=r"(before) : "r"(smem_u32(&sh->done[of])) : "memory");
-      if (before == L::kWarps - 1) {
-        sh->done[of] = 0;
-        int next = at + S;
-        while (next >= stages * visits) {
-          next -= stages * visits;
-          ++r;
-        }
-        fill(of, r, next);
+  }
+
+  // ---- the filling lane
+  __device__ __forceinline__ bool more() const { return first + row * step < rows; }
+  // Whether the next slot is free. The slots are free to begin with.
+  __device__ __forceinline__ bool free() const { return fills < S || mbar_test(&sh->empty[slot], parity ^ 1); }
+  __device__ __forceinline__ void fill() {
+    if (at == 0) {
+      const RowPart<T> p(logits + (first + row * step) * ld, V, rank, ranks);
+      from = p.body + p.lo;
+      left = p.hi - p.lo;
+    }
+    const int n = min(left, kStage);
+    if (n <= 0) {  // rows of one matrix can differ by a vector: nothing to copy for this one
+      mbar_arrive(&sh->full[slot]);
+    } else {
+      mbar_arrive_expect_tx(&sh->full[slot], n * 16u);
+      // what is read for the last time need not stay in L2, what comes again should
+      uint64_t policy;
+      if (visit + 1 < visits)
+        asm("createpolicy.fractional.L2::evict_last.b64 %0;" : "=l"(policy));
+      else
+        asm("createpolicy.fractional.L2::evict_first.b64 %0;" : "=l"(policy));
+      asm volatile(
+          "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+              smem_u32(data + slot * kStage)),
+          "l"(from), "r"(n * 16u), "r"(smem_u32(&sh->full[slot])), "l"(policy)
+          : "memory");
+    }
+    ++fills;
+    advance();
+    from += kStage;
+    left -= kStage;
+    if (++at == stages) {
+      at = 0;
+      if (++visit == visits) {
+        visit = 0;
+        ++row;
       }
     }
   }
+  // Fill what can be filled without waiting.
+  __device__ __forceinline__ void pump() {
+    while (more() && free()) fill();
+  }
+  // Fill everything; for a lane that has nothing else to do.
+  __device__ __forceinline__ void run() {
+    while (more()) {
+      if (fills >= S && !p24_wait(&sh->empty[slot], parity ^ 1, &sh->abort, status)) break;
+      fill();
+    }
+    finish();
+  }
   // After an expired wait, copies may still be on their way into this CTA's shared memory.
   __device__ __forceinline__ void finish() const {
-    __syncthreads();  // no wait begins after this
-    if (threadIdx.x == 0 && *reinterpret_cast<volatile int*>(&sh->abort))
-      for (int i = 0; i < S; ++i)
-        if (sh->fills[i] > 0) p24_wait_quiet(&sh->full[i], (sh->fills[i] - 1) & 1);
+    if (*reinterpret_cast<volatile int*>(&sh->abort) == 0) return;
+    for (int64_t i = fills > S ? fills - S : 0; i < fills; ++i) p24_wait_quiet(&sh->full[i % S], (i / S) & 1);
   }
 };
 
@@ -563,16 +614,16 @@ __device__ __forceinline__ void store_vec(T* row, int i0, bool aligned, const ui
 }
 
 // ---------------------------------------------------------------- launch
-// A persistent grid of clusters of `ranks` CTAs of NT threads over `rows` items.
+// A persistent grid of clusters of `ranks` CTAs over `rows` items.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_rows(void (*kern)(KArgs...), int NT, int64_t rows, int ranks, size_t smem, cudaStream_t s,
+cudaError_t launch_rows(void (*kern)(KArgs...), int threads, int64_t rows, int ranks, size_t smem, cudaStream_t s,
                         Args&&... args) {
   int slots = 0;
-  cudaError_t e = row_kernel_slots(reinterpret_cast<const void*>(kern), NT, ranks, smem, &slots);
+  cudaError_t e = row_kernel_slots(reinterpret_cast<const void*>(kern), threads, ranks, smem, &slots);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(rows, slots) * ranks));
-  cfg.blockDim = dim3(NT);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -600,12 +651,12 @@ inline int row_split(int64_t T, int64_t vecs, int64_t slots, int most, int64_t f
 }
 // As launch_rows, over T rows in `parts` parts: CTA b takes part b % parts of rows.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_parts(void (*kern)(KArgs...), int NT, int64_t T, int parts, size_t smem, cudaStream_t s, Args&&... args) {
+cudaError_t launch_parts(void (*kern)(KArgs...), int threads, int64_t T, int parts, size_t smem, cudaStream_t s, Args&&... args) {
   int slots = 0;
-  cudaError_t e = row_kernel_slots(reinterpret_cast<const void*>(kern), NT, 1, smem, &slots);
+  cudaError_t e = row_kernel_slots(reinterpret_cast<const void*>(kern), threads, 1, smem, &slots);
   if (e != cudaSuccess) return e;
   const int64_t rows = std::min<int64_t>(T, std::max(1, slots / parts));
-  e = launch_plain(kern, dim3(static_cast<unsigned>(rows * parts)), dim3(NT), smem, s, std::forward<Args>(args)...);
+  e = launch_plain(kern, dim3(static_cast<unsigned>(rows * parts)), dim3(threads), smem, s, std::forward<Args>(args)...);
   if (e == cudaSuccess) count_launch();
   return e;
 }

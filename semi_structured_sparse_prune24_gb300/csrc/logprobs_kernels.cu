@@ -45,7 +45,7 @@ __device__ __forceinline__ int entry_pos(uint64_t e) { return static_cast<int>(0
 __device__ __forceinline__ uint32_t entry_key(uint64_t e) { return static_cast<uint32_t>(e >> 32); }
 
 using Long = Layout<256, 4, 4, 2>;       // with alternatives (17 KB for them)
-using LongPlain = Layout<256, 4, 4, 3>;  // without
+using LongPlain = Layout<192, 5, 4, 3>;  // without
 using LongGrad = Layout<256, 4, 4, 3>;
 using Short = Layout<128, 8, 2, 4>;      // rows of up to kShortRow vectors
 constexpr int kShortRow = 1024;
@@ -98,7 +98,7 @@ __device__ __noinline__ void select_exact(const RowPart<T>& p, int k, TopShared<
   constexpr int N = Vec<T>::N;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int steps = 2 + (p.hi - p.lo + NT - 1) / NT;
-  __syncthreads();
+  walk_sync<NT>();
   if (tid == 0) {
     sh.prefix = 0;
     sh.left = k;
@@ -107,7 +107,7 @@ __device__ __noinline__ void select_exact(const RowPart<T>& p, int k, TopShared<
   uint32_t mask = 0;
   for (int shift = 24; shift >= 32 - 8 * static_cast<int>(sizeof(T)); shift -= 8) {
     for (int i = tid; i < 256; i += NT) sh.hist[i] = 0;
-    __syncthreads();
+    walk_sync<NT>();
     const uint32_t prefix = sh.prefix;
     // a thread adds equal digits up before it touches their counter: rows that come here have many
     uint32_t digit = 0, run = 0;
@@ -129,7 +129,7 @@ __device__ __noinline__ void select_exact(const RowPart<T>& p, int k, TopShared<
       }
     }
     if (run) atomicAdd(&sh.hist[digit], run);
-    __syncthreads();
+    walk_sync<NT>();
     if (warp == 0) {
       // lane l holds the counters of digits 255 - 8 l down to 248 - 8 l
       int own = 0;
@@ -152,7 +152,7 @@ __device__ __noinline__ void select_exact(const RowPart<T>& p, int k, TopShared<
       }
     }
     mask |= 255u << shift;
-    __syncthreads();
+    walk_sync<NT>();
   }
   const uint32_t kth = sh.prefix;
   const int left = sh.left;
@@ -178,7 +178,7 @@ __device__ __noinline__ void select_exact(const RowPart<T>& p, int k, TopShared<
       if (lane >= d) incl += y;
     }
     if (lane == 31) sh.warp[warp] = incl;
-    __syncthreads();
+    walk_sync<NT>();
     int before = equal_before + incl - mine;
     for (int w = 0; w < NT / 32; ++w) {
       if (w < warp) before += sh.warp[w];
@@ -190,7 +190,7 @@ __device__ __noinline__ void select_exact(const RowPart<T>& p, int k, TopShared<
         if (before < left) sh.list[k - left + before] = entry(order_key(x[j]), pos + j);
         ++before;
       }
-    __syncthreads();
+    walk_sync<NT>();
   }
 }
 
@@ -229,7 +229,7 @@ __device__ __forceinline__ int list_from(const RowPart<T>& p, uint32_t from, uin
       list(to_f32(p.row[pos]), pos);
     }
   }
-  __syncthreads();
+  walk_sync<NT>();
   const int items = sh.items;
   if (items > kItems) return kList + 1;
   const int lg = shift + 31 - __clz(L::SV);  // log2 of a part's vectors
@@ -240,7 +240,7 @@ __device__ __forceinline__ int list_from(const RowPart<T>& p, uint32_t from, uin
 #pragma unroll
     for (int j = 0; j < N; ++j) list(elem_of<T>(r, j), p.vec_pos(v) + j);
   }
-  __syncthreads();
+  walk_sync<NT>();
   return sh.n;
 }
 
@@ -264,11 +264,11 @@ __device__ __forceinline__ int top_of_part(const RowPart<T>& p, int k, uint32_t 
   const uint32_t low = __reduce_min_sync(~0u, own16), high = __reduce_max_sync(~0u, own16);
   if (lane == 0) sh.low[tid >> 5] = low, sh.high[tid >> 5] = high;
   if (tid == 0) sh.n = sh.items = 0;
-  __syncthreads();
+  walk_sync<NT>();
   uint32_t lo = __reduce_min_sync(~0u, sh.low[lane % (NT / 32)]), hi = __reduce_max_sync(~0u, sh.high[lane % (NT / 32)]);
   while (lo < hi) {
     const uint32_t mid = (lo + hi + 1) / 2;
-    if (__syncthreads_count(own16 >= mid) >= k) lo = mid;
+    if (walk_count<NT>(own16 >= mid) >= k) lo = mid;
     else hi = mid - 1;
   }
   int n = 0;
@@ -281,12 +281,12 @@ __device__ __forceinline__ int top_of_part(const RowPart<T>& p, int k, uint32_t 
   // for, -inf and the lowest finite one. List what is above, then take ties from the front.
   const uint32_t tie = sizeof(T) == 2 ? ((lo & 0x8000u) ? lo << 16 : lo << 16 | 0xffffu) : lo == 0x7fu ? 0x7fffffu : lo << 16;
   if (sizeof(T) == 2 || masked) {
-    __syncthreads();
+    walk_sync<NT>();
     if (tid == 0) sh.n = sh.items = 0;
-    __syncthreads();
+    walk_sync<NT>();
     n = list_from<T, L>(p, tie + 1, own16, stages, shift, sh);
     if (n >= k && n <= kList) return n;
-    __syncthreads();
+    walk_sync<NT>();
     if (n < k && tid < 32) {
       constexpr int kEach = 4, kSteps = 32;
       for (int step = 0; step < kSteps && n < k; ++step) {
@@ -304,7 +304,7 @@ __device__ __forceinline__ int top_of_part(const RowPart<T>& p, int k, uint32_t 
       }
       if (lane == 0) sh.n = min(n, k);
     }
-    __syncthreads();
+    walk_sync<NT>();
     n = sh.n;
     if (n == k) return n;
   }
@@ -314,14 +314,16 @@ __device__ __forceinline__ int top_of_part(const RowPart<T>& p, int k, uint32_t 
 
 // kTop: with alternatives.
 template <typename T, bool kEntropy, bool kTop, typename L>
-__global__ void __launch_bounds__(L::NT, L::kCtas) logprobs_kernel(const p24_logprobs_args g, int* status) {
+__global__ void __launch_bounds__(L::kThreads, L::kCtas) logprobs_kernel(const p24_logprobs_args g, int* status) {
   using R = Ring<T, L>;
   constexpr int NT = L::NT;
   extern __shared__ __align__(128) uint4 ring_data[];
   __shared__ RingShared<L::S> ring_sh;
   __shared__ JoinShared joins;
   TopShared<NT>& top = *reinterpret_cast<TopShared<NT>*>(reinterpret_cast<char*>(ring_data) + L::kRing);  // kTop
-  uint64_t* best = reinterpret_cast<uint64_t*>(&top + 1);  // kTop and more ranks than one: [rank][k], in order
+  // kTop and more ranks than one: the ranks' lists in rank 0, [row parity][rank][k], in order
+  uint64_t* best = reinterpret_cast<uint64_t*>(&top + 1);
+  __shared__ uint64_t best_in[2];
   const int tid = threadIdx.x, V = static_cast<int>(g.V), k = static_cast<int>(g.k);
   const int ranks = cluster_ranks(), rank = ranks > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const float tau = g.temperature, c = kLog2e / tau;
@@ -330,9 +332,16 @@ __global__ void __launch_bounds__(L::NT, L::kCtas) logprobs_kernel(const p24_log
   int shift = 0;  // stages to a part of the second look, a power of two
   while (kTop && (stages - 1) >> shift >= kParts) ++shift;
   R ring{logits, g.ldz, blockIdx.x / ranks, gridDim.x / ranks, g.T, V, rank, ranks, stages, 1, ring_data, &ring_sh, status};
-  if (tid == 0) join_init(joins, ranks);
+  if (tid == 0) {
+    join_init(joins, ranks);
+    for (int i = 0; i < 2; ++i) mbar_init(&best_in[i], ranks);
+  }
   ring.start();
   if (ranks > 1) cluster_barrier();  // every CTA runs before another writes to its shared memory
+  if (tid >= NT) {
+    if (tid == NT) ring.run();
+    return;
+  }
 
   float edge = load_edge(RowPart<T>(logits + ring.first * g.ldz, V, rank, ranks), true);
   int64_t r = 0;
@@ -364,7 +373,7 @@ __global__ void __launch_bounds__(L::NT, L::kCtas) logprobs_kernel(const p24_log
         }
       }
       R::each(data, n, [&](const uint4& x, int) { w.template add<T>(x, c); });
-      ring.release(r, at);
+      ring.release();
     }
     const float own_max = w.m;
     const bool own = p.lo + tid < p.hi || tid < p.edges;
@@ -401,14 +410,17 @@ __global__ void __launch_bounds__(L::NT, L::kCtas) logprobs_kernel(const p24_log
         place += __shfl_xor_sync(~0u, place, 2);
         if (i >= n) place = i;
         if (sub != 0 || place >= k || i >= all) continue;
-        if (ranks > 1) store_remote(remote(best + rank * kTopMax + place, 0), e);
+        if (ranks > 1) store_remote(remote(best + ((r & 1) * ranks + rank) * kTopMax + place, 0), e);
         else put(e, place);
       }
-      if (ranks > 1) {
-        cluster_barrier();
-        for (int i = rank == 0 ? tid : ranks * k; i < ranks * k; i += NT) {
+      walk_sync<NT>();  // the list and the parts' maxima are free for the next row
+      if (ranks > 1 && tid == 0) arrive_remote(&best_in[r & 1], 0);
+      if (ranks > 1 && rank == 0) {
+        wait_cluster(&best_in[r & 1], (r >> 1) & 1, &ring_sh.abort, status);
+        const uint64_t* lists = best + (r & 1) * ranks * kTopMax;
+        for (int i = tid; i < ranks * k; i += NT) {
           const int from = i / k, at = i % k;
-          const uint64_t e = best[from * kTopMax + at];
+          const uint64_t e = lists[from * kTopMax + at];
           if (e == 0) continue;
           int place = at;  // and the entries of the other lists that come before it
           for (int r2 = 0; r2 < ranks; ++r2) {
@@ -416,16 +428,13 @@ __global__ void __launch_bounds__(L::NT, L::kCtas) logprobs_kernel(const p24_log
             int lo = 0, hi = k;
             while (lo < hi) {
               const int mid = (lo + hi) / 2;
-              if (best[r2 * kTopMax + mid] > e) lo = mid + 1;
+              if (lists[r2 * kTopMax + mid] > e) lo = mid + 1;
               else hi = mid;
             }
             place += lo;
           }
           if (place < k) put(e, place);
         }
-        cluster_barrier();  // rank 0 has read the lists before the next row's are written
-      } else {
-        __syncthreads();  // the list and the parts' maxima are free for the next row
       }
       for (int i = V + tid; rank == 0 && i < k; i += NT) {  // fewer entries than alternatives asked for
         g.top_idx[t * k + i] = -1;
@@ -433,12 +442,11 @@ __global__ void __launch_bounds__(L::NT, L::kCtas) logprobs_kernel(const p24_log
       }
     }
   }
-  ring.finish();
 }
 
 // The gradient, elementwise: a CTA takes parts of rows.
 template <typename T, bool kEntropy, typename L>
-__global__ void __launch_bounds__(L::NT, L::kCtas) logprobs_bwd_kernel(const p24_logprobs_args g, int parts, int* status) {
+__global__ void __launch_bounds__(L::kThreads, L::kCtas) logprobs_bwd_kernel(const p24_logprobs_args g, int parts, int* status) {
   using R = Ring<T, L>;
   constexpr int NT = L::NT;
   constexpr int N = Vec<T>::N;
@@ -454,6 +462,10 @@ __global__ void __launch_bounds__(L::NT, L::kCtas) logprobs_bwd_kernel(const p24
   const int stages = row_stages(V / N, parts, L::kStage);
   R ring{logits, g.ldz, blockIdx.x / parts, gridDim.x / parts, g.T, V, part, parts, stages, 1, ring_data, &ring_sh, status};
   ring.start();
+  if (tid >= NT) {
+    if (tid == NT) ring.run();
+    return;
+  }
   auto row_of = [&](int64_t t) {
     Row r;
     r.tok = g.tokens ? g.tokens[t] : -1;
@@ -467,8 +479,7 @@ __global__ void __launch_bounds__(L::NT, L::kCtas) logprobs_bwd_kernel(const p24
     return r;
   };
   Row row = row_of(ring.first);
-  int64_t r = 0;
-  for (int64_t t = ring.first; t < g.T; t += ring.step, ++r) {
+  for (int64_t t = ring.first; t < g.T; t += ring.step) {
     const RowPart<T> p(logits + t * g.ldz, V, part, parts);
     const Row now = row;
     if (t + ring.step < g.T) row = row_of(t + ring.step);
@@ -511,10 +522,9 @@ __global__ void __launch_bounds__(L::NT, L::kCtas) logprobs_bwd_kernel(const p24
         }
         store_vec(out, i0, aligned, pack_vec<T>(y));
       });
-      ring.release(r, at);
+      ring.release();
     }
   }
-  ring.finish();
 }
 
 template <typename T, bool kEntropy, bool kTop>
@@ -523,21 +533,21 @@ cudaError_t launch_logprobs_as(const p24_logprobs_args& g, int* status, cudaStre
   const int64_t vecs = g.V / Vec<T>::N;
   auto smem = [&](auto layout, int ranks) {
     using M = decltype(layout);
-    return M::kRing + (kTop ? sizeof(TopShared<M::NT>) + (ranks > 1 ? ranks * kTopMax * sizeof(uint64_t) : 0) : 0);
+    return M::kRing + (kTop ? sizeof(TopShared<M::NT>) + (ranks > 1 ? 2 * ranks * kTopMax * sizeof(uint64_t) : 0) : 0);
   };
   if (vecs <= kShortRow && g.T > sm_count())
-    return launch_rows(logprobs_kernel<T, kEntropy, kTop, Short>, Short::NT, g.T, 1, smem(Short(), 1), s, g, status);
+    return launch_rows(logprobs_kernel<T, kEntropy, kTop, Short>, Short::kThreads, g.T, 1, smem(Short(), 1), s, g, status);
   const int ranks = row_split(g.T, vecs, sm_count() * L::kCtas, kMaxRanks, 1024);
-  return launch_rows(logprobs_kernel<T, kEntropy, kTop, L>, L::NT, g.T, ranks, smem(L(), ranks), s, g, status);
+  return launch_rows(logprobs_kernel<T, kEntropy, kTop, L>, L::kThreads, g.T, ranks, smem(L(), ranks), s, g, status);
 }
 
 template <typename T, bool kEntropy>
 cudaError_t launch_logprobs_bwd_as(const p24_logprobs_args& g, int* status, cudaStream_t s) {
   const int64_t vecs = g.V / Vec<T>::N;
   if (vecs <= kShortRow)
-    return launch_parts(logprobs_bwd_kernel<T, kEntropy, Short>, Short::NT, g.T, 1, Short::kRing, s, g, 1, status);
+    return launch_parts(logprobs_bwd_kernel<T, kEntropy, Short>, Short::kThreads, g.T, 1, Short::kRing, s, g, 1, status);
   const int parts = row_split(g.T, vecs, sm_count() * LongGrad::kCtas, 64, 256);
-  return launch_parts(logprobs_bwd_kernel<T, kEntropy, LongGrad>, LongGrad::NT, g.T, parts, LongGrad::kRing, s, g, parts,
+  return launch_parts(logprobs_bwd_kernel<T, kEntropy, LongGrad>, LongGrad::kThreads, g.T, parts, LongGrad::kRing, s, g, parts,
                       status);
 }
 
