@@ -185,9 +185,9 @@ __device__ __forceinline__ void store_listed(T* out, const RowPart<T>& p, const 
   }
 }
 
-using Loss = Layout<192, 4, 4, 4>;
-using Step = Layout<256, 3, 4, 4>;
-using Grad = Layout<256, 4, 4, 3>;
+using Loss = Layout<128, 6, 8, 2>;
+using Step = Layout<256, 3, 8, 2>;
+using Grad = Layout<192, 4, 8, 2>;
 using Short = Layout<128, 6, 2, 4>;  // rows of up to kShortRow vectors
 constexpr int kShortRow = 1024;
 

@@ -46,7 +46,7 @@ __device__ __forceinline__ uint32_t entry_key(uint64_t e) { return static_cast<u
 
 using Long = Layout<256, 4, 4, 2>;       // with alternatives (17 KB for them)
 using LongPlain = Layout<192, 5, 4, 3>;  // without
-using LongGrad = Layout<256, 4, 4, 3>;
+using LongGrad = Layout<192, 4, 8, 2>;
 using Short = Layout<128, 8, 2, 4>;      // rows of up to kShortRow vectors
 constexpr int kShortRow = 1024;
 
