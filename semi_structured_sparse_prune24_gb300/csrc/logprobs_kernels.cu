@@ -57,8 +57,9 @@ constexpr int kItems = 1024; // parts looked at a second time before something e
 template <int NT>
 struct TopShared {
   uint64_t list[kList];       // candidates
-  uint16_t part[kParts][NT];  // upper half of the largest element of each thread's parts
-  uint16_t item[kItems];      // parts to look at: part * NT + thread
+  // upper half of the largest element of each thread's parts; rows of 9 words: no bank conflicts
+  uint16_t part[NT][kParts + 2];
+  uint16_t item[kItems];      // parts to look at: thread * kParts + part
   uint32_t hist[256];
   int warp[16];
   uint32_t low[16], high[16];
@@ -211,22 +212,32 @@ __device__ __forceinline__ int list_from(const RowPart<T>& p, uint32_t from, uin
   constexpr int N = Vec<T>::N, NT = L::NT;
   static_assert(kParts * NT <= 65536, "an item is 16 bits");
   const int tid = threadIdx.x;
+  const float least = from ? key_value(from) : ninf();  // as numbers: no NaN comes here
   auto list = [&](float x, int pos) {
-    const uint32_t key = order_key(x);
-    if (key >= from) {
-      const int at = atomicAdd(&sh.n, 1);
-      if (at < kList) sh.list[at] = entry(key, pos);
-    }
+    const int at = atomicAdd(&sh.n, 1);
+    if (at < kList) sh.list[at] = entry(order_key(x), pos);
   };
   if (own16 >= (from >> 16) && own16 > 0) {
-    for (int i = 0; i << shift < stages; ++i)
-      if (order_key(__uint_as_float(static_cast<uint32_t>(sh.part[i][tid]) << 16)) >> 16 >= (from >> 16)) {
-        const int at = atomicAdd(&sh.items, 1);
-        if (at < kItems) sh.item[at] = static_cast<uint16_t>(i * NT + tid);
-      }
+    // a part's upper half stands for a number no smaller than the bound's where an element is (a
+    // negative one's lower half only takes it further down)
+    const float bound = least > 0.f ? __uint_as_float(__float_as_uint(least) & 0xffff0000u) : least;
+    const uint32_t* parts = reinterpret_cast<const uint32_t*>(sh.part[tid]);
+    uint32_t found = 0;
+#pragma unroll
+    for (int i = 0; i < kParts / 2; ++i) {
+      const uint32_t w = parts[i];
+      if (__uint_as_float(w << 16) >= bound) found |= 1u << (2 * i);
+      if (__uint_as_float(w & 0xffff0000u) >= bound) found |= 2u << (2 * i);
+    }
+    found &= (2u << ((stages - 1) >> shift)) - 1u;
+    for (; found; found &= found - 1) {
+      const int at = atomicAdd(&sh.items, 1);
+      if (at < kItems) sh.item[at] = static_cast<uint16_t>(tid * kParts + __ffs(found) - 1);
+    }
     if (tid < p.edges) {
       const int pos = p.edge_pos(tid);
-      list(to_f32(p.row[pos]), pos);
+      const float x = to_f32(p.row[pos]);
+      if (x >= least) list(x, pos);
     }
   }
   walk_sync<NT>();
@@ -234,11 +245,19 @@ __device__ __forceinline__ int list_from(const RowPart<T>& p, uint32_t from, uin
   if (items > kItems) return kList + 1;
   const int lg = shift + 31 - __clz(L::SV);  // log2 of a part's vectors
   for (int i = tid; i < items << lg; i += NT) {
-    const int item = sh.item[i >> lg], v = p.lo + (((item / NT) << lg) + (i & ((1 << lg) - 1))) * NT + item % NT;
+    const int item = sh.item[i >> lg];
+    const int v = p.lo + ((item % kParts << lg) + (i & ((1 << lg) - 1))) * NT + item / kParts;
     if (v >= p.hi) continue;
     const uint4 r = p.body[v];
+    uint32_t found = 0;
 #pragma unroll
-    for (int j = 0; j < N; ++j) list(elem_of<T>(r, j), p.vec_pos(v) + j);
+    for (int j = 0; j < N; ++j)
+      if (elem_of<T>(r, j) >= least) found |= 1u << j;
+    for (; found; found &= found - 1) {
+      const int j = __ffs(found) - 1;
+      const uint32_t w = j < N / 2 ? (j < N / 4 ? r.x : r.y) : (j < 3 * N / 4 ? r.z : r.w);
+      list(sizeof(T) == 4 ? __uint_as_float(w) : __uint_as_float((j & 1) ? w & 0xffff0000u : w << 16), p.vec_pos(v) + j);
+    }
   }
   walk_sync<NT>();
   return sh.n;
@@ -368,7 +387,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) logprobs_kernel(const p
       if constexpr (kTop) {
         part_max = fmaxf(part_max, vm);
         if (((at + 1) & ((1 << shift) - 1)) == 0 || at + 1 == stages) {
-          top.part[at >> shift][tid] = static_cast<uint16_t>(__float_as_uint(part_max) >> 16);
+          top.part[tid][at >> shift] = static_cast<uint16_t>(__float_as_uint(part_max) >> 16);
           part_max = ninf();
         }
       }
@@ -400,7 +419,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) logprobs_kernel(const p
       // entries that come after all others
       // (four lanes to an entry)
       const int all = ranks > 1 ? max(n, k) : n, sub = tid & 3;
-      for (int i0 = 0; i0 < all; i0 += NT / 4) {
+      for (int i0 = 0; i0 + (tid >> 5) * 8 < all; i0 += NT / 4) {  // the warp has entries
         const int i = i0 + (tid >> 2);
         const uint64_t e = i < n ? top.list[i] : 0;
         int place = 0;
