@@ -135,8 +135,15 @@ def _check(code: int, where: str) -> None:
         raise P24Error(code, where)
 
 
+# the current stream's handle without building a torch.cuda.Stream around it: a microsecond
+# instead of four on the host, which a call on a few rows of logits would be waiting for
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int | None:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -629,23 +636,24 @@ _LOGIT_TYPES = {torch.bfloat16: P24_BF16, torch.float32: P24_F32}
 
 def _logits(t: torch.Tensor, name: str, like: torch.Tensor | None = None) -> tuple[int, int, int, int]:
     """(T, V, row stride, dtype code) of a matrix of logits or of their gradient."""
-    if t.dtype not in _LOGIT_TYPES:
+    code = _LOGIT_TYPES.get(t.dtype)
+    if code is None:
         raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
     T, V, ld = _mat(t, t.dtype, name)
     if like is not None and (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device):
         raise ValueError(f"{name} must have the logits' shape, type and device")
-    return T, V, ld, _LOGIT_TYPES[t.dtype]
+    return T, V, ld, code
 
 
 def _per_row(t: torch.Tensor | None, shape: tuple, dtype, name: str, device) -> int | None:
     """Pointer of a contiguous per-row tensor (None stays None)."""
     if t is None:
         return None
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {shape} tensor on the logits' device")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {shape} tensor on the logits' device")
 
 
 def p24_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, k: int = 0,
@@ -656,21 +664,19 @@ def p24_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None,
     probable entries top_logp, top_idx [T, k], and stats [T, 2] for the backward, as a dict.
     out: tensors to write to, under those names. See include/prune24.h."""
     T, V, ldz, dt = _logits(logits, "logits")
-    dev, f32 = logits.device, torch.float32
+    dev, f32, i32, row, top = logits.device, torch.float32, torch.int32, (T,), (T, k)
     o = {} if out is None else dict(out)
-    want = [("stats", (T, 2), f32)]
-    if tokens is not None:
-        want.append(("logp", (T,), f32))
-    if entropy:
-        want.append(("entropy", (T,), f32))
-    if k > 0:
-        want += [("top_logp", (T, k), f32), ("top_idx", (T, k), torch.int32)]
-    a = p24_logprobs_args(T, V, k, dt, temperature, logits.data_ptr(), ldz,
-                          _per_row(tokens, (T,), torch.int32, "tokens", dev))
-    for name, shape, dtype in want:
+
+    def to(name, wanted, shape, dtype=f32):
+        if not wanted:
+            return None
         if o.get(name) is None:
             o[name] = torch.empty(shape, dtype=dtype, device=dev)
-        setattr(a, name, _per_row(o[name], shape, dtype, name, dev))
+        return _per_row(o[name], shape, dtype, name, dev)
+
+    a = p24_logprobs_args(T, V, k, dt, temperature, logits.data_ptr(), ldz, _per_row(tokens, row, i32, "tokens", dev),
+                          to("logp", tokens is not None, row), to("entropy", entropy, row), to("stats", True, (T, 2)),
+                          to("top_logp", k > 0, top), to("top_idx", k > 0, top, i32))
     _check(lib.p24_token_logprobs(C.byref(a), _stream(stream)), "p24_token_logprobs")
     return o
 
