@@ -437,10 +437,13 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) logprobs_kernel(const p
       if (ranks > 1 && rank == 0) {
         wait_cluster(&best_in[r & 1], (r >> 1) & 1, &ring_sh.abort, status);
         const uint64_t* lists = best + (r & 1) * ranks * kTopMax;
+        // each list's first k / ranks (rounded up) are k entries or more: what is below all of them is out
+        uint64_t least = ~uint64_t(0);
+        for (int r2 = 0; r2 < ranks; ++r2) least = min(least, lists[r2 * kTopMax + (k + ranks - 1) / ranks - 1]);
         for (int i = tid; i < ranks * k; i += NT) {
           const int from = i / k, at = i % k;
           const uint64_t e = lists[from * kTopMax + at];
-          if (e == 0) continue;
+          if (e == 0 || e < least) continue;
           int place = at;  // and the entries of the other lists that come before it
           for (int r2 = 0; r2 < ranks; ++r2) {
             if (r2 == from) continue;
