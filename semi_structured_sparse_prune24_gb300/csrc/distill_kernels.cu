@@ -452,7 +452,7 @@ cudaError_t launch_distill_as(const p24_distill_args& g, int* status, cudaStream
   // the rows in flight stay in L2 until they come the second time
   constexpr int64_t kL2Rows = 64 << 20;
   while (kGrad && ranks < kMaxRanks && std::min<int64_t>(g.T, sm_count() * L::kCtas / ranks) * vecs * 16 > kL2Rows) ranks *= 2;
-  ranks = std::max(ranks, row_split(g.T, vecs, sm_count() * L::kCtas, kMaxRanks, 1024));
+  ranks = std::max(ranks, row_split(g.T, vecs, sm_count() * L::kCtas, kMaxRanks, 2048));
   return launch_rows(distill_kernel<T, kTwo, kGrad, L>, L::kThreads + 32, g.T, ranks, smem(L(), ranks), s, g, status);
 }
 
