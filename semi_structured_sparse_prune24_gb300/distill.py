@@ -1,0 +1,84 @@
+"""Distillation of a 2:4 sparse student from its dense teacher.
+
+A pruned model recovers by learning from the model it was pruned from. What the
+student sees of the teacher is a list per token: the teacher's most probable
+tokens and their log probabilities, as p24_token_logprobs finds them. DistillHead
+holds the student's head (the unembedding): logits, loss and gradients, one pass
+over the logits and in place, so that one [M, V] buffer is all it needs.
+DistillStep runs a whole step of a student whose last layer is a 2:4 FFN: prune,
+forward, head, loss and backward, on the library's calls.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import _native as N
+
+
+class DistillHead:
+    """Logits = Y W^T of M tokens over a vocabulary of V (a multiple of 8), with the loss
+    of p24_distill_topk on them."""
+
+    def __init__(self, M: int, d: int, V: int, device="cuda"):
+        if V % 8 or d % 8:
+            raise ValueError("the head's products need V and d to be multiples of 8")
+        bf = torch.bfloat16
+        self.M, self.d, self.V = M, d, V
+        self.logits = torch.empty((M, V), dtype=bf, device=device)    # and their gradient, in place
+        self.W_T = torch.empty((d, V), dtype=bf, device=device)       # for the product with the gradient
+
+    def teacher_list(self, Y: torch.Tensor, W: torch.Tensor, k: int, temperature: float = 1.0,
+                     out: dict | None = None, stream=None) -> dict:
+        """A teacher's list for these tokens from its last hidden states Y [M, d] and its head
+        W [V, d]: top_idx, top_logp [M, k], and its entropy. Uses this head's logits buffer."""
+        N.p24_gemm_nt(Y, W, self.logits, stream=stream)
+        return N.p24_token_logprobs(self.logits, k=k, temperature=temperature, out=out, stream=stream)
+
+    def score(self, Y: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, stream=None) -> dict:
+        """Log probabilities of tokens (int32 [M]) and the entropy, e.g. of held-out text."""
+        N.p24_gemm_nt(Y, W, self.logits, stream=stream)
+        return N.p24_token_logprobs(self.logits, tokens, stream=stream)
+
+    def step(self, Y: torch.Tensor, W: torch.Tensor, top_idx: torch.Tensor, top_logp: torch.Tensor, dkl: torch.Tensor,
+             labels: torch.Tensor | None = None, dce: torch.Tensor | None = None, temperature: float = 1.0,
+             tail: bool = True, out: dict | None = None, stream=None) -> dict:
+        """The loss of hidden states Y [M, d] under the head W [V, d], and its gradients: kl (and ce)
+        [M], dY [M, d], dW [V, d]. dkl, dce: each token's weight in the loss (fp32 [M])."""
+        o = {} if out is None else dict(out)
+        N.p24_gemm_nt(Y, W, self.logits, stream=stream)
+        o.update(N.p24_distill_topk(self.logits, top_idx, top_logp, labels, temperature, tail, dkl, dce,
+                                    out={**{k: o[k] for k in ("kl", "ce", "stats") if k in o}, "dlogits": self.logits},
+                                    stream=stream))
+        N.p24_transpose(W, self.W_T, stream=stream)
+        o["dY"] = N.p24_gemm_nt(self.logits, self.W_T, o.get("dY"), stream=stream)
+        o["dW"] = N.p24_gemm_tn(self.logits, Y, o.get("dW"), stream=stream)
+        return o
+
+
+class DistillStep:
+    """One training step of a student Y = FFN(X), logits = Y W_head^T, with a 2:4 FFN (up, ReLU, down;
+    fresh masks every step) and double-pruned backward products, against a teacher's list."""
+
+    def __init__(self, M: int, d: int, ffn: int, V: int, device="cuda"):
+        self.head = DistillHead(M, d, V, device)
+        S = N.Sparse24.empty
+        self.up, self.up_T = S(ffn, d, device), S(d, ffn, device)
+        self.down, self.down_T = S(d, ffn, device), S(ffn, d, device)
+
+    def run(self, X, W_up, b_up, W_down, b_down, W_head, top_idx, top_logp, dkl, labels=None, dce=None,
+            temperature: float = 1.0, tail: bool = True, stream=None) -> dict:
+        """Returns kl (and ce) per token and the gradients dX, dW_up, db_up, dW_down, db_down, dW_head."""
+        N.prune24_compress_both(W_up, self.up, self.up_T, stream=stream)
+        N.prune24_compress_both(W_down, self.down, self.down_T, stream=stream)
+        H = N.spmm24_fwd(X, self.up, b_up, relu=True, stream=stream)
+        Y = N.spmm24_fwd(H, self.down, b_down, stream=stream)
+        o = self.head.step(Y, W_head, top_idx, top_logp, dkl, labels, dce, temperature, tail, stream=stream)
+        o["dW_head"] = o.pop("dW")
+        dY = o.pop("dY")
+        o["db_up"] = torch.empty(H.shape[1], dtype=torch.float32, device=X.device)
+        dH = N.spmm24_bwd_dx(dY, self.down_T, gate=H, dbias=o["db_up"], stream=stream)
+        o["db_down"] = N.p24_colsum(dY, stream=stream)
+        o["dW_down"] = N.masked_dw_gemm(dY, H, self.down, stream=stream)
+        o["dX"] = N.spmm24_bwd_dx(dH, self.up_T, stream=stream)
+        o["dW_up"] = N.masked_dw_gemm(dH, X, self.up, stream=stream)
+        return o
