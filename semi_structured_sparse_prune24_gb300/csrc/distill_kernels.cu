@@ -158,7 +158,7 @@ __device__ __forceinline__ RowGrad row_grad(const ListShared& sh, bool two, floa
 template <typename T, bool kTwo, typename R>
 __device__ __forceinline__ void store_row(R& ring, T* out, bool aligned, const RowPart<T>& p, int stages,
                                           const Terms& terms) {
-  constexpr int N = Vec<T>::N, NT = R::kThreads;
+  constexpr int N = Vec<T>::N, NT = R::kWalkers;
   for (int at = 0; at < stages; ++at) {
     const uint4* data = ring.wait();
     const int v0 = p.lo + at * R::kStage + static_cast<int>(threadIdx.x);
@@ -188,7 +188,7 @@ __device__ __forceinline__ void store_listed(T* out, const RowPart<T>& p, const 
 using Loss = Layout<128, 6, 8, 2>;
 using Step = Layout<256, 3, 8, 2>;
 using Grad = Layout<192, 4, 8, 2>;
-using Short = Layout<128, 6, 2, 4>;  // rows of up to kShortRow vectors
+using Short = Layout<64, 10, 4, 2>;  // rows of up to kShortRow vectors
 constexpr int kShortRow = 1024;
 
 // The listed elements of a CTA's share, chained up by the stage and the warp that reads them:
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(L::kThreads + 32, L::kCtas) distill_kernel(con
       prepare(r + 2);
     }
   } else {
-    float edge = load_edge(RowPart<T>(logits + ring.first * g.ldz, V, rank, ranks), true);
+    float edge = load_edge(RowPart<T>(logits + ring.first * g.ldz, V, rank, ranks));
     int64_t r = 0;
     for (int64_t t = ring.first; t < g.T; t += ring.step, ++r) {
       const int par = r & 1;
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(L::kThreads + 32, L::kCtas) distill_kernel(con
         if (!tail || !((mk.edges >> tid) & 1u)) w.add_one(edge, c);
       }
       const float edge_here = edge;
-      if (t + ring.step < g.T) edge = load_edge(RowPart<T>(logits + (t + ring.step) * g.ldz, V, rank, ranks), true);
+      if (t + ring.step < g.T) edge = load_edge(RowPart<T>(logits + (t + ring.step) * g.ldz, V, rank, ranks));
       for (int at = 0; at < stages; ++at) {
         uint4* data = ring.wait();
         const int n = vecs - at * L::kStage;
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) distill_bwd_kernel(cons
     if (tid == NT) ring.run();
     return;
   }
-  float edge = load_edge(RowPart<T>(logits + ring.first * g.ldz, V, part, parts), true);
+  float edge = load_edge(RowPart<T>(logits + ring.first * g.ldz, V, part, parts));
   int64_t r = 0;
   for (int64_t t = ring.first; t < g.T; t += ring.step, ++r) {
     const RowPart<T> p(logits + t * g.ldz, V, part, parts);
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) distill_bwd_kernel(cons
     const bool aligned = (reinterpret_cast<uintptr_t>(out) & 15u) == (reinterpret_cast<uintptr_t>(p.row) & 15u);
     const RowGrad rg = row_grad(sh, kTwo, tau, st.m, st.ls, st.lr, st.l1);
     if (tid < p.edges) out[p.edge_pos(tid)] = static_cast<T>(rg.off.template one<kTwo>(edge));
-    if (t + ring.step < g.T) edge = load_edge(RowPart<T>(logits + (t + ring.step) * g.ldz, V, part, parts), true);
+    if (t + ring.step < g.T) edge = load_edge(RowPart<T>(logits + (t + ring.step) * g.ldz, V, part, parts));
     store_row<T, kTwo, R>(ring, out, aligned, p, stages, rg.off);
     walk_sync<NT>();
     store_listed<T, kTwo, NT>(out, p, sh, K, rg);

@@ -13,8 +13,8 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
-
 #include <cstdint>
+#include <utility>
 
 #include "p24_internal.h"
 #include "p24_ptx.cuh"
@@ -95,11 +95,6 @@ struct Vec {
   static constexpr uint32_t kFill = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;  // -inf
 };
 
-template <typename T>
-__device__ __forceinline__ uint4 fill_vec() {
-  return make_uint4(Vec<T>::kFill, Vec<T>::kFill, Vec<T>::kFill, Vec<T>::kFill);
-}
-
 // Element pairs j of a vector as fp32: j < N / 2.
 template <typename T>
 __device__ __forceinline__ F2 pair(const uint4& r, int j) {
@@ -176,9 +171,9 @@ struct RowPart {
 };
 
 template <typename T>
-__device__ __forceinline__ float load_edge(const RowPart<T>& p, bool on) {
+__device__ __forceinline__ float load_edge(const RowPart<T>& p) {
   const int e = static_cast<int>(threadIdx.x);
-  return on && e < p.edges ? to_f32(p.row[p.edge_pos(e)]) : ninf();
+  return e < p.edges ? to_f32(p.row[p.edge_pos(e)]) : ninf();
 }
 
 // ---------------------------------------------------------------- softmax sums
@@ -420,19 +415,6 @@ __device__ __forceinline__ void row_join(Sums& u, float c, Sums& v, float cv, Jo
 }
 
 // ---------------------------------------------------------------- the ring
-// Whether a phase is complete, without waiting.
-__device__ __forceinline__ bool mbar_test(const uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 template <int S>
 struct RingShared {
   uint64_t full[S];    // a stage's data has arrived
@@ -446,7 +428,7 @@ struct RingShared {
 // only wait for data and say when they have read it.
 template <typename T, typename L>
 struct Ring {
-  static constexpr int S = L::S, kStage = L::kStage, kThreads = L::NT;
+  static constexpr int S = L::S, kStage = L::kStage, kWalkers = L::NT;
   const T* logits;
   int64_t ld, first, step, rows;
   int V, rank, ranks, stages, visits;
@@ -508,8 +490,6 @@ struct Ring {
 
   // ---- the filling lane
   __device__ __forceinline__ bool more() const { return first + row * step < rows; }
-  // Whether the next slot is free. The slots are free to begin with.
-  __device__ __forceinline__ bool free() const { return fills < S || mbar_test(&sh->empty[slot], parity ^ 1); }
   __device__ __forceinline__ void fill() {
     if (at == 0) {
       const RowPart<T> p(logits + (first + row * step) * ld, V, rank, ranks);
@@ -545,11 +525,7 @@ struct Ring {
       }
     }
   }
-  // Fill what can be filled without waiting.
-  __device__ __forceinline__ void pump() {
-    while (more() && free()) fill();
-  }
-  // Fill everything; for a lane that has nothing else to do.
+  // Fill everything, each slot once it has been read. The slots are free to begin with.
   __device__ __forceinline__ void run() {
     while (more()) {
       if (fills >= S && !p24_wait(&sh->empty[slot], parity ^ 1, &sh->abort, status)) break;

@@ -47,7 +47,8 @@ __device__ __forceinline__ uint32_t entry_key(uint64_t e) { return static_cast<u
 using Long = Layout<256, 4, 4, 2>;       // with alternatives (17 KB for them)
 using LongPlain = Layout<192, 5, 4, 3>;  // without
 using LongGrad = Layout<192, 4, 8, 2>;
-using Short = Layout<128, 8, 2, 4>;      // rows of up to kShortRow vectors
+using Short = Layout<128, 6, 2, 4>;      // rows of up to kShortRow vectors
+using ShortPlain = Layout<128, 8, 2, 4>;
 constexpr int kShortRow = 1024;
 
 constexpr int kList = 1024;  // candidates listed before something else has to be done
@@ -211,6 +212,7 @@ __device__ __forceinline__ int list_from(const RowPart<T>& p, uint32_t from, uin
                                          TopShared<L::NT>& sh) {
   constexpr int N = Vec<T>::N, NT = L::NT;
   static_assert(kParts * NT <= 65536, "an item is 16 bits");
+  static_assert(NT >= kTopMax, "k threads' maxima bound the k-th element");
   const int tid = threadIdx.x;
   const float least = from ? key_value(from) : ninf();  // as numbers: no NaN comes here
   auto list = [&](float x, int pos) {
@@ -362,7 +364,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) logprobs_kernel(const p
     return;
   }
 
-  float edge = load_edge(RowPart<T>(logits + ring.first * g.ldz, V, rank, ranks), true);
+  float edge = load_edge(RowPart<T>(logits + ring.first * g.ldz, V, rank, ranks));
   int64_t r = 0;
   for (int64_t t = ring.first; t < g.T; t += ring.step, ++r) {
     const RowPart<T> p(logits + t * g.ldz, V, rank, ranks);
@@ -376,7 +378,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) logprobs_kernel(const p
     Walk<kEntropy> w;
     float part_max = ninf();
     if (tid < p.edges) w.add_one(edge, c);
-    if (t + ring.step < g.T) edge = load_edge(RowPart<T>(logits + (t + ring.step) * g.ldz, V, rank, ranks), true);
+    if (t + ring.step < g.T) edge = load_edge(RowPart<T>(logits + (t + ring.step) * g.ldz, V, rank, ranks));
     for (int at = 0; at < stages; ++at) {
       const uint4* data = ring.wait();
       const int n = p.hi - p.lo - at * L::kStage;
@@ -497,7 +499,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) logprobs_bwd_kernel(con
     r.dl = g.dlogp ? g.dlogp[t] : 0.f;
     r.dh = kEntropy ? g.dentropy[t] : 0.f;
     r.H = kEntropy ? g.entropy[t] : 0.f;
-    r.edge = load_edge(RowPart<T>(logits + t * g.ldz, V, part, parts), true);
+    r.edge = load_edge(RowPart<T>(logits + t * g.ldz, V, part, parts));
     return r;
   };
   Row row = row_of(ring.first);
@@ -557,8 +559,10 @@ cudaError_t launch_logprobs_as(const p24_logprobs_args& g, int* status, cudaStre
     using M = decltype(layout);
     return M::kRing + (kTop ? sizeof(TopShared<M::NT>) + (ranks > 1 ? 2 * ranks * kTopMax * sizeof(uint64_t) : 0) : 0);
   };
-  if (vecs <= kShortRow && g.T > sm_count())
-    return launch_rows(logprobs_kernel<T, kEntropy, kTop, Short>, Short::kThreads, g.T, 1, smem(Short(), 1), s, g, status);
+  if (vecs <= kShortRow && g.T > sm_count()) {
+    using M = std::conditional_t<kTop, Short, ShortPlain>;
+    return launch_rows(logprobs_kernel<T, kEntropy, kTop, M>, M::kThreads, g.T, 1, smem(M(), 1), s, g, status);
+  }
   // the alternatives cost a CTA about as much as walking 8192 vectors: 697 rows of 91196 with 20 of
   // them took 37 us as whole rows, 78 us in fours
   const int ranks = row_split(g.T, vecs, sm_count() * L::kCtas, kMaxRanks, kTop ? 8192 : 1024);
@@ -569,7 +573,8 @@ template <typename T, bool kEntropy>
 cudaError_t launch_logprobs_bwd_as(const p24_logprobs_args& g, int* status, cudaStream_t s) {
   const int64_t vecs = g.V / Vec<T>::N;
   if (vecs <= kShortRow)
-    return launch_parts(logprobs_bwd_kernel<T, kEntropy, Short>, Short::kThreads, g.T, 1, Short::kRing, s, g, 1, status);
+    return launch_parts(logprobs_bwd_kernel<T, kEntropy, ShortPlain>, ShortPlain::kThreads, g.T, 1, ShortPlain::kRing, s, g, 1,
+                        status);
   const int parts = row_split(g.T, vecs, sm_count() * LongGrad::kCtas, 64, 256);
   return launch_parts(logprobs_bwd_kernel<T, kEntropy, LongGrad>, LongGrad::kThreads, g.T, parts, LongGrad::kRing, s, g, parts,
                       status);
