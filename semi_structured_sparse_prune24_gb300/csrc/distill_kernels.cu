@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(L::kThreads + 32, L::kCtas) distill_kernel(con
   if (tail)
     for (int i = tid; i < 2 * stages * L::kWarps; i += L::kThreads + 32) heads[i] = -1;
   ring.start();
-  if (ranks > 1) cluster_barrier();  // every CTA runs before another writes to its shared memory
+  begin(ranks);
 
   if (warp == L::kWarps) {
     if (tid == NT) ring.run();
@@ -411,6 +411,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) distill_bwd_kernel(cons
   const int stages = row_stages(V / N, parts, L::kStage);
   R ring{logits, g.ldz, blockIdx.x / parts, gridDim.x / parts, g.T, V, part, parts, stages, 1, ring_data, &ring_sh, status};
   ring.start();
+  begin(1);
   if (tid >= NT) {
     if (tid == NT) ring.run();
     return;

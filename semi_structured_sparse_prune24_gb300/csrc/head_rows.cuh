@@ -443,7 +443,7 @@ struct Ring {
   int left = 0, at = 0, visit = 0;
   int64_t row = 0, fills = 0;
 
-  // All threads of the CTA; ends with a barrier.
+  // All threads of the CTA; ends with a barrier, and no global memory is touched before.
   __device__ __forceinline__ void start() {
     if (threadIdx.x == 0) {
       sh->abort = 0;
@@ -589,28 +589,47 @@ __device__ __forceinline__ void store_vec(T* row, int i0, bool aligned, const ui
   }
 }
 
+// What every kernel here begins with, in all threads, once its shared memory is set up: the
+// cluster's CTAs run before one of them writes to another's shared memory, and the stream's
+// previous kernel has finished before global memory is touched.
+__device__ __forceinline__ void begin(int ranks) {
+  if (ranks > 1) cluster_barrier();
+  pdl_wait();
+  pdl_trigger();
+}
+
 // ---------------------------------------------------------------- launch
+// `blocks` CTAs in clusters of `ranks`, with programmatic stream serialization: a call's set-up
+// overlaps the end of the kernel before it, which is a good part of a call on few rows.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_blocks(void (*kern)(KArgs...), int64_t blocks, int threads, int ranks, size_t smem, cudaStream_t s,
+                          Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(ranks);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = ranks > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+  if (e == cudaSuccess) count_launch();
+  return e;
+}
+
 // A persistent grid of clusters of `ranks` CTAs over `rows` items.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_rows(void (*kern)(KArgs...), int threads, int64_t rows, int ranks, size_t smem, cudaStream_t s,
                         Args&&... args) {
   int slots = 0;
-  cudaError_t e = row_kernel_slots(reinterpret_cast<const void*>(kern), threads, ranks, smem, &slots);
+  const cudaError_t e = row_kernel_slots(reinterpret_cast<const void*>(kern), threads, ranks, smem, &slots);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(rows, slots) * ranks));
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(ranks);
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = ranks > 1 ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
-  if (e == cudaSuccess) count_launch();
-  return e;
+  return launch_blocks(kern, std::min<int64_t>(rows, slots) * ranks, threads, ranks, smem, s, std::forward<Args>(args)...);
 }
 
 // Over how many CTAs (a power of two up to `most`) to split rows of `vecs` vectors, T of them on
@@ -629,12 +648,10 @@ inline int row_split(int64_t T, int64_t vecs, int64_t slots, int most, int64_t f
 template <typename... KArgs, typename... Args>
 cudaError_t launch_parts(void (*kern)(KArgs...), int threads, int64_t T, int parts, size_t smem, cudaStream_t s, Args&&... args) {
   int slots = 0;
-  cudaError_t e = row_kernel_slots(reinterpret_cast<const void*>(kern), threads, 1, smem, &slots);
+  const cudaError_t e = row_kernel_slots(reinterpret_cast<const void*>(kern), threads, 1, smem, &slots);
   if (e != cudaSuccess) return e;
-  const int64_t rows = std::min<int64_t>(T, std::max(1, slots / parts));
-  e = launch_plain(kern, dim3(static_cast<unsigned>(rows * parts)), dim3(threads), smem, s, std::forward<Args>(args)...);
-  if (e == cudaSuccess) count_launch();
-  return e;
+  return launch_blocks(kern, std::min<int64_t>(T, std::max(1, slots / parts)) * parts, threads, 1, smem, s,
+                       std::forward<Args>(args)...);
 }
 
 // Stages that the longest share of a row of `vecs` vectors takes.

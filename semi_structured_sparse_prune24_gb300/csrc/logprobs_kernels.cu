@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) logprobs_kernel(const p
     for (int i = 0; i < 2; ++i) mbar_init(&best_in[i], ranks);
   }
   ring.start();
-  if (ranks > 1) cluster_barrier();  // every CTA runs before another writes to its shared memory
+  begin(ranks);
   if (tid >= NT) {
     if (tid == NT) ring.run();
     return;
@@ -486,6 +486,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) logprobs_bwd_kernel(con
   const int stages = row_stages(V / N, parts, L::kStage);
   R ring{logits, g.ldz, blockIdx.x / parts, gridDim.x / parts, g.T, V, part, parts, stages, 1, ring_data, &ring_sh, status};
   ring.start();
+  begin(1);
   if (tid >= NT) {
     if (tid == NT) ring.run();
     return;
