@@ -525,6 +525,9 @@ int ffn24_step_traced(const p24_ffn_args* a, void* workspace, size_t ws_bytes, v
  * A logit of -inf is masked: probability 0, gradient 0. A row of nothing else has no
  * distribution: log probabilities -inf, entropy 0, losses +inf, gradients 0. A row with a
  * NaN or +inf gives NaN. Logits of the type's lowest finite value are ordinary numbers.
+ *
+ * A call's first launch of a kernel looks up how many of its CTAs the device holds; like
+ * every first call it belongs before a stream capture.
  */
 typedef enum { P24_BF16 = 0, P24_F32 = 1 } p24_dtype;
 
@@ -548,7 +551,9 @@ typedef enum { P24_BF16 = 0, P24_F32 = 1 } p24_dtype;
  *   dlogp, dentropy : fp32 [T] upstream gradients; either may be NULL (then not part of
  *             it). dlogp needs tokens, dentropy the forward's entropy.
  *   dlogits : the logits' type, [T, V], row stride ldd >= V; it may be the logits
- *             themselves (in place, ldd == ldz). The alternatives carry no gradient.
+ *             themselves (in place, ldd == ldz), and overlaps them in no other way. It is
+ *             stored 16 bytes at a time where its rows have the logits' alignment. The
+ *             alternatives carry no gradient.
  *
  * tokens: int32 [T]. 1e-4 <= temperature <= 1e4. 0 <= k <= P24_TOPK_MAX and
  * 1 <= V <= 2^30 (P24_EUNSUPPORTED beyond). Pointers are aligned to their element.

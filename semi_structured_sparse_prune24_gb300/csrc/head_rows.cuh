@@ -8,7 +8,15 @@
 //
 // A CTA's share of its rows comes through a ring of stages in shared memory, filled by bulk
 // copies (cp.async.bulk) that run ahead of the threads by the ring's length, over row ends too:
-// loads are under way while the CTA reduces, waits and stores.
+// loads are under way while the CTA reduces, waits and stores. A warp of its own issues the
+// copies. Measured against that (the loss of 4096 rows of 50257, 112 us then): with the last warp
+// to read a stage refilling it the slowest warp of every stage issued the next copy as well, and
+// each stage took about 0.9 us longer; loads into registers, refilled as they were used, gave
+// 2.3 ms against 0.75 ms for the loss and gradient of 8192 x 131072.
+//
+// Several CTAs of 2 to 8 warps share an SM, each at another point of another row: a row's
+// reductions and waits (about 2 us) hide behind the others' walks. One CTA of 16 or 24 warps on an
+// SM took 1.2 to 1.9 ms for that gradient.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -52,7 +60,8 @@ __device__ __forceinline__ float floored(float x) {
   return y;
 }
 
-// Two fp32 operations in one instruction.
+// Two fp32 operations in one instruction: a gradient's vector of 8 bf16 takes 37 instructions
+// instead of 50 (of them 8 exponentials, at a quarter of the issue rate).
 struct F2 {
   unsigned long long v;
 };
@@ -178,7 +187,10 @@ __device__ __forceinline__ float load_edge(const RowPart<T>& p) {
 
 // ---------------------------------------------------------------- softmax sums
 // Sums over part of a row relative to its maximum m: s = sum exp((z - m)/tau) and
-// a = sum exp((z - m)/tau) (z - m). s == 0: nothing above -inf yet. c = log2(e) / tau below.
+// a = sum exp((z - m)/tau) (z - m). s == 0: nothing above -inf yet. c = log2(e) / tau below. The
+// difference z - m is formed first: z c - m c would lose it for logits of large magnitude, and
+// give NaN for rows whose every logit is the type's lowest value. Everything is fp32; the
+// exponential is the hardware's, 2^-22 relative.
 struct Sums {
   float m, s, a;
 };
