@@ -20,8 +20,8 @@
 // Bound: HBM, one read of the logits (and one write of the gradient). Measured on GB300, of the
 // 6.69 TB/s of a plain copy: scores of 4096 x 50257 bf16 64 to 66 us, 0.93 to 0.96; gradient of
 // the same rows with entropy 134 us, 0.92, of 1000 x 32003 fp32 42 us, 0.91; entropy and top 64 of
-// 8192 x 131072 423 us, 0.76 (the alternatives' searches are then a quarter of the instructions,
-// and the walk waits for them); one row of 32000 with 20 alternatives 8.7 us, of which 2.4 us are
+// 8192 x 131072 419 us, 0.77 (the alternatives' searches are then a quarter of the instructions,
+// and the walk waits for them); one row of 32000 with 20 alternatives 7.5 us, of which 2.4 us are
 // the walk and the rest the alternatives' dependent steps.
 #include <algorithm>
 #include <type_traits>
@@ -69,7 +69,7 @@ constexpr int kItems = 1024; // parts looked at a second time before something e
 
 template <int NT>
 struct TopShared {
-  uint64_t list[kList];       // candidates
+  uint64_t list[kList + 32];  // candidates, and zeros after them
   // upper half of the largest element of each thread's parts; rows of 9 words: no bank conflicts
   uint16_t part[NT][kParts + 2];
   uint16_t item[kItems];      // parts to look at: thread * kParts + part
@@ -428,49 +428,53 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) logprobs_kernel(const p
         g.top_idx[t * k + place] = entry_pos(e);
         g.top_logp[t * k + place] = logp(key_value(entry_key(e)));
       };
-      const int n = top_of_part<T, L>(p, k, own ? order_key(own_max) >> 16 : 0u, !(u.s == u.s), stages, shift, top);
-      // each entry's place among them; of several ranks, rank 0 gets every list, filled up with
-      // entries that come after all others
-      // (four lanes to an entry)
-      const int all = ranks > 1 ? max(n, k) : n, sub = tid & 3;
-      for (int i0 = 0; i0 + (tid >> 5) * 8 < all; i0 += NT / 4) {  // the warp has entries
-        const int i = i0 + (tid >> 2);
-        const uint64_t e = i < n ? top.list[i] : 0;
-        int place = 0;
-#pragma unroll 4
-        for (int j = sub; j < n; j += 4) place += top.list[j] > e;
-        place += __shfl_xor_sync(~0u, place, 1);
-        place += __shfl_xor_sync(~0u, place, 2);
-        if (i >= n) place = i;
-        if (sub != 0 || place >= k || i >= all) continue;
-        if (ranks > 1) store_remote(remote(best + ((r & 1) * ranks + rank) * kTopMax + place, 0), e);
-        else put(e, place);
-      }
-      walk_sync<NT>();  // the list and the parts' maxima are free for the next row
-      if (ranks > 1 && tid == 0) arrive_remote(&best_in[r & 1], 0);
-      if (ranks > 1 && rank == 0) {
-        wait_cluster(&best_in[r & 1], (r >> 1) & 1, &ring_sh.abort, status);
-        const uint64_t* lists = best + (r & 1) * ranks * kTopMax;
-        // each list's first k / ranks (rounded up) are k entries or more: what is below all of them is out
-        uint64_t least = ~uint64_t(0);
-        for (int r2 = 0; r2 < ranks; ++r2) least = min(least, lists[r2 * kTopMax + (k + ranks - 1) / ranks - 1]);
-        for (int i = tid; i < ranks * k; i += NT) {
-          const int from = i / k, at = i % k;
-          const uint64_t e = lists[from * kTopMax + at];
-          if (e == 0 || e < least) continue;
-          int place = at;  // and the entries of the other lists that come before it
-          for (int r2 = 0; r2 < ranks; ++r2) {
-            if (r2 == from) continue;
-            int lo = 0, hi = k;
-            while (lo < hi) {
-              const int mid = (lo + hi) / 2;
-              if (lists[r2 * kTopMax + mid] > e) lo = mid + 1;
-              else hi = mid;
-            }
-            place += lo;
+      int n = top_of_part<T, L>(p, k, own ? order_key(own_max) >> 16 : 0u, !(u.s == u.s), stages, shift, top);
+      // Each entry's place is the number of entries before it. Of several ranks, each sends its first
+      // k to rank 0, which does the same with those: one copy of the code for both.
+#pragma unroll 1
+      for (int last = ranks > 1 ? 0 : 1; last < 2; ++last) {
+        if (tid < 32) top.list[n + tid] = 0;  // no entry is before any other there: a multiple of 32
+        walk_sync<NT>();
+        const int all = !last ? max(n, k) : n, sub = tid & 3;
+#pragma unroll 1
+        for (int i0 = 0; i0 + (tid >> 5) * 8 < all; i0 += NT / 4) {  // four lanes to an entry
+          const int i = i0 + (tid >> 2);
+          const uint64_t e = i < n ? top.list[i] : 0;
+          int place = 0;
+#pragma unroll 1
+          for (int j0 = sub; j0 < n; j0 += 32) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) place += top.list[j0 + j] > e;
           }
-          if (place < k) put(e, place);
+          place += __shfl_xor_sync(~0u, place, 1);
+          place += __shfl_xor_sync(~0u, place, 2);
+          if (i >= n) place = i;  // what a share lacks of k entries comes after all others
+          if (sub != 0 || place >= k || i >= all) continue;
+          if (!last) store_remote(remote(best + ((r & 1) * ranks + rank) * kTopMax + place, 0), e);
+          else put(e, place);
         }
+        walk_sync<NT>();  // the list and the parts' maxima are free
+        if (last) break;
+        if (tid == 0) {
+          arrive_remote(&best_in[r & 1], 0);
+          top.n = 0;
+        }
+        if (rank != 0) break;
+        wait_cluster(&best_in[r & 1], (r >> 1) & 1, &ring_sh.abort, status);
+        walk_sync<NT>();
+        // each list's first k / ranks (rounded up) are k entries or more: what is below all of them is out
+        const uint64_t* lists = best + (r & 1) * ranks * kTopMax;
+        uint64_t least = ~uint64_t(0);
+        const int first = ((k + ranks - 1) >> (31 - __clz(ranks))) - 1;
+#pragma unroll 1
+        for (int i = 0; i < ranks; ++i) least = min(least, lists[i * kTopMax + first]);
+#pragma unroll 1
+        for (int i = tid; i < ranks * kTopMax; i += NT) {
+          const uint64_t e = i % kTopMax < k ? lists[i] : 0;
+          if (e != 0 && e >= least) top.list[atomicAdd(&top.n, 1)] = e;
+        }
+        walk_sync<NT>();
+        n = top.n;
       }
       for (int i = V + tid; rank == 0 && i < k; i += NT) {  // fewer entries than alternatives asked for
         g.top_idx[t * k + i] = -1;
