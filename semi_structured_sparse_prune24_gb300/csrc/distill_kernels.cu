@@ -402,6 +402,7 @@ __global__ void __launch_bounds__(L::kThreads + 32, L::kCtas) distill_kernel(con
       __syncwarp();
       if ((tid & 31) == 0) mbar_arrive(&hand.freed[par]);
     }
+    end(ranks, &ring_sh.abort);
   }
 }
 

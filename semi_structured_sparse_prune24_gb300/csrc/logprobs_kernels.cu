@@ -431,6 +431,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) logprobs_kernel(const p
       int n = top_of_part<T, L>(p, k, own ? order_key(own_max) >> 16 : 0u, !(u.s == u.s), stages, shift, top);
       // Each entry's place is the number of entries before it. Of several ranks, each sends its first
       // k to rank 0, which does the same with those: one copy of the code for both.
+      const bool sends = *const_cast<volatile int*>(&ring_sh.abort) == 0;
 #pragma unroll 1
       for (int last = ranks > 1 ? 0 : 1; last < 2; ++last) {
         if (tid < 32) top.list[n + tid] = 0;  // no entry is before any other there: a multiple of 32
@@ -450,13 +451,13 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) logprobs_kernel(const p
           place += __shfl_xor_sync(~0u, place, 2);
           if (i >= n) place = i;  // what a share lacks of k entries comes after all others
           if (sub != 0 || place >= k || i >= all) continue;
-          if (!last) store_remote(remote(best + ((r & 1) * ranks + rank) * kTopMax + place, 0), e);
-          else put(e, place);
+          if (last) put(e, place);
+          else if (sends) store_remote(remote(best + ((r & 1) * ranks + rank) * kTopMax + place, 0), e);
         }
         walk_sync<NT>();  // the list and the parts' maxima are free
         if (last) break;
         if (tid == 0) {
-          arrive_remote(&best_in[r & 1], 0);
+          if (sends) arrive_remote(&best_in[r & 1], 0);
           top.n = 0;
         }
         if (rank != 0) break;
@@ -482,6 +483,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) logprobs_kernel(const p
       }
     }
   }
+  end(ranks, &ring_sh.abort);
 }
 
 // The gradient, elementwise: a CTA takes parts of rows.
