@@ -9,14 +9,14 @@
 //  distill_kernel      a cluster per row (head_rows.cuh). With the bucket the listed elements
 //                      stay out of the pass's sums (p_r by subtraction would lose all digits
 //                      when the list holds nearly everything). The gradient follows from the
-//                      row's second way through the ring (from L2); the listed columns and the label are then stored again
-//                      with their own terms.
+//                      row's second way through the ring (from L2); the listed columns and the
+//                      label are then stored again with their own terms.
 //  distill_bwd_kernel  the gradient alone, elementwise from the saved statistics.
 //
 // Bound: HBM, one read of the logits (and one write of the gradient). Measured on GB300, of the
 // 6.69 TB/s of a plain copy: loss and gradient of 8192 x 131072 bf16 with 64 entries and the bucket
 // 748 us, 0.86 (the rest: rows in flight that L2 loses before their second visit, and the clusters'
-// joins); of 1023 x 50257 fp32 at two temperatures 80 to 82 us, 0.75 (rows come out uneven on 456
+// joins); of 1023 x 50257 fp32 at two temperatures 82 us, 0.75 (rows come out uneven on 456
 // CTAs); loss alone of 4096 x 50257 67 us, 0.91; gradient alone of 2048 x 131072 173 us, 0.93.
 #include <algorithm>
 #include <type_traits>

@@ -20,7 +20,7 @@
 // Bound: HBM, one read of the logits (and one write of the gradient). Measured on GB300, of the
 // 6.69 TB/s of a plain copy: scores of 4096 x 50257 bf16 64 to 66 us, 0.93 to 0.96; gradient of
 // the same rows with entropy 134 us, 0.92, of 1000 x 32003 fp32 42 us, 0.91; entropy and top 64 of
-// 8192 x 131072 419 us, 0.77 (the alternatives' searches are then a quarter of the instructions,
+// 8192 x 131072 420 us, 0.77 (the alternatives' searches are then a quarter of the instructions,
 // and the walk waits for them); one row of 32000 with 20 alternatives 7.5 us, of which 2.4 us are
 // the walk and the rest the alternatives' dependent steps.
 #include <algorithm>
