@@ -227,27 +227,32 @@ struct Walk {
   __device__ __forceinline__ void add(const uint4& r, float c) {
     const float ref_ = -ref();
     const F2 off = f2(ref_, ref_), c2 = f2(c, c);
-    F2 av = f2(0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < Vec<T>::N / 2; ++j) {
       const F2 t = add2(pair<T>(r, j), off);
       const F2 e = ex2x2(mul2(t, c2));
       s = add2(s, e);
-      if constexpr (kEntropy) av = j == 0 ? mul2(e, t) : fma2(e, t, av);
+      if constexpr (kEntropy) a = fma2(e, t, a);
     }
-    if constexpr (kEntropy) {
-      float x, y;
-      split(av, x, y);
-      if (x + y != x + y) {  // an element of -inf (0 times -inf), or a NaN: once more with the difference floored
-        av = f2(0.f, 0.f);
+  }
+  // Whether an element of -inf (0 times -inf), or a NaN, has gone into `a`: then `a` of the vectors
+  // since it was last right is summed again with the difference floored. Looked at once a stage:
+  // at each vector it took 6 of its 48 instructions.
+  __device__ __forceinline__ bool lost() const {
+    float x, y;
+    split(a, x, y);
+    return x + y != x + y;
+  }
+  template <typename T>
+  __device__ __forceinline__ void add_floored(const uint4& r, float c) {
+    const float ref_ = -ref();
+    const F2 off = f2(ref_, ref_), c2 = f2(c, c);
 #pragma unroll
-        for (int j = 0; j < Vec<T>::N / 2; ++j) {
-          split(add2(pair<T>(r, j), off), x, y);
-          const F2 t = f2(floored(x), floored(y));
-          av = fma2(ex2x2(mul2(t, c2)), t, av);
-        }
-      }
-      a = add2(a, av);
+    for (int j = 0; j < Vec<T>::N / 2; ++j) {
+      float x, y;
+      split(add2(pair<T>(r, j), off), x, y);
+      const F2 t = f2(floored(x), floored(y));
+      a = fma2(ex2x2(mul2(t, c2)), t, a);
     }
   }
   __device__ __forceinline__ void add_one(float x, float c) {

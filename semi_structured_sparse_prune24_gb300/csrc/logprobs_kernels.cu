@@ -405,7 +405,12 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) logprobs_kernel(const p
           part_max = ninf();
         }
       }
+      const F2 a = w.a;
       R::each(data, n, [&](const uint4& x, int) { w.template add<T>(x, c); });
+      if (kEntropy && w.lost()) {
+        w.a = a;
+        R::each(data, n, [&](const uint4& x, int) { w.template add_floored<T>(x, c); });
+      }
       ring.release();
     }
     const float own_max = w.m;
