@@ -53,6 +53,9 @@ __device__ __forceinline__ uint32_t entry_key(uint64_t e) { return static_cast<u
 // CTAs on an SM, 481 with 192 and 5, 506 with 256 and 2. Fewer threads have fewer maxima, so more
 // candidates; more threads pay more for each search.
 using Long = Layout<256, 4, 4, 2>;
+// With alternatives, where an SM has no more than two CTAs: registers to spare. Top 20 of one row of
+// 32000 6.9 us, 7.6 in Long; of 256 rows of 50257 with 200 tokens allowed 15.6 us, 19.4.
+using Few = Layout<256, 2, 4, 2>;
 // Without: scores of 4096 x 50257 64 us; 75 with 256 threads and 4 CTAs, 82 with 512 and 2.
 using LongPlain = Layout<192, 5, 4, 3>;
 // Gradients: 2048 x 131072 175 us with all of 128 to 512 threads and 16 to 24 KB stages, 191 with 8 KB.
@@ -575,6 +578,23 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) logprobs_bwd_kernel(con
   }
 }
 
+// As row_split, with alternatives. A share costs its vectors (0.63 us for 1000) in each round. Several
+// of them cost a second join, about 2200 vectors; each CTA that an SM has costs about 2300 more, for
+// the searches of an SM's CTAs hold each other up. Of several shares 3 fit on an SM at a time, of whole
+// rows 4. Measured with 1, 2, 4, 8 shares: 32 rows of 131072 16.2, 12.4, 9.9, 10.5 us; 64 of 32000 8.1,
+// 8.2, 9.1, 16.8; 200 of 131072 20.5, 19.2 with the first two.
+int top_split(int64_t T, int64_t vecs) {
+  const int64_t sms = sm_count();
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int n = 1; n <= kMaxRanks && (n == 1 || vecs >= n * int64_t(128)); n *= 2) {
+    const int64_t rounds = (T * n + (n > 1 ? 3 : 4) * sms - 1) / ((n > 1 ? 3 : 4) * sms);
+    const int64_t cost = rounds * (vecs / n) + (n > 1 ? 2200 : 0) + (T * n + sms - 1) / sms * 2300;
+    if (cost < least) least = cost, best = n;
+  }
+  return best;
+}
+
 template <typename T, bool kEntropy, bool kTop>
 cudaError_t launch_logprobs_as(const p24_logprobs_args& g, int* status, cudaStream_t s) {
   using L = std::conditional_t<kTop, Long, LongPlain>;
@@ -587,9 +607,10 @@ cudaError_t launch_logprobs_as(const p24_logprobs_args& g, int* status, cudaStre
     using M = std::conditional_t<kTop, Short, ShortPlain>;
     return launch_rows(logprobs_kernel<T, kEntropy, kTop, M>, M::kThreads, g.T, 1, smem(M(), 1), s, g, status);
   }
-  // the alternatives cost a CTA about as much as walking 8192 vectors: 697 rows of 91196 with 20 of
-  // them took 37 us as whole rows, 78 us in fours
-  const int ranks = row_split(g.T, vecs, sm_count() * L::kCtas, kMaxRanks, kTop ? 8192 : 1024);
+  const int ranks = kTop ? top_split(g.T, vecs) : row_split(g.T, vecs, sm_count() * L::kCtas, kMaxRanks, 1024);
+  if (kTop && g.T * ranks <= sm_count() * Few::kCtas)
+    return launch_rows(logprobs_kernel<T, kEntropy, kTop, std::conditional_t<kTop, Few, L>>, Few::kThreads, g.T, ranks,
+                       smem(Few(), ranks), s, g, status);
   return launch_rows(logprobs_kernel<T, kEntropy, kTop, L>, L::kThreads, g.T, ranks, smem(L(), ranks), s, g, status);
 }
 
