@@ -464,7 +464,7 @@ cudaError_t launch_distill_as(const p24_distill_args& g, int* status, cudaStream
   // 61 MB of them every second visit hit, with 80 MB a quarter went to memory, with 160 MB nearly all.
   constexpr int64_t kL2Rows = 64 << 20;
   while (kGrad && ranks < kMaxRanks && std::min<int64_t>(g.T, sm_count() * L::kCtas / ranks) * vecs * 16 > kL2Rows) ranks *= 2;
-  ranks = std::max(ranks, row_split(g.T, vecs, sm_count() * L::kCtas, kMaxRanks, 2048));
+  ranks = std::max(ranks, row_split(g.T, vecs, sm_count() * L::kCtas, kMaxRanks, 800));
   return launch_rows(distill_kernel<T, kTwo, kGrad, L>, L::kThreads + 32, g.T, ranks, smem(L(), ranks), s, g, status);
 }
 
