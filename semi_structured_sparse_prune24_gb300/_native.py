@@ -639,10 +639,13 @@ def _logits(t: torch.Tensor, name: str, like: torch.Tensor | None = None) -> tup
     code = _LOGIT_TYPES.get(t.dtype)
     if code is None:
         raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
-    T, V, ld = _mat(t, t.dtype, name)
-    if like is not None and (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device):
+    strides = t.stride()
+    if len(strides) != 2 or strides[1] != 1 or not t.is_cuda:
+        _mat(t, t.dtype, name)  # says what is wrong, if anything is
+    if like is not None and (t.shape != like.shape or t.dtype is not like.dtype or t.device != like.device):
         raise ValueError(f"{name} must have the logits' shape, type and device")
-    return T, V, ld, code
+    T, V = t.shape
+    return T, V, strides[0] if T > 1 else max(V, strides[0]), code
 
 
 def _per_row(t: torch.Tensor | None, shape: tuple, dtype, name: str, device) -> int | None:
@@ -656,6 +659,15 @@ def _per_row(t: torch.Tensor | None, shape: tuple, dtype, name: str, device) -> 
     raise ValueError(f"{name} must be a contiguous {shape} tensor on the logits' device")
 
 
+def _out(o: dict, name: str, shape: tuple, dtype, device) -> int:
+    """Pointer of the output `name` of a call: the caller's tensor in o, or a new one put there."""
+    t = o.get(name)
+    if t is not None:
+        return _per_row(t, shape, dtype, name, device)
+    t = o[name] = torch.empty(shape, dtype=dtype, device=device)
+    return t.data_ptr()
+
+
 def p24_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, k: int = 0,
                        temperature: float = 1.0, entropy: bool = True, out: dict | None = None,
                        stream=None) -> dict:
@@ -664,19 +676,14 @@ def p24_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None,
     probable entries top_logp, top_idx [T, k], and stats [T, 2] for the backward, as a dict.
     out: tensors to write to, under those names. See include/prune24.h."""
     T, V, ldz, dt = _logits(logits, "logits")
-    dev, f32, i32, row, top = logits.device, torch.float32, torch.int32, (T,), (T, k)
+    dev, f32, row = logits.device, torch.float32, (T,)
     o = {} if out is None else dict(out)
-
-    def to(name, wanted, shape, dtype=f32):
-        if not wanted:
-            return None
-        if o.get(name) is None:
-            o[name] = torch.empty(shape, dtype=dtype, device=dev)
-        return _per_row(o[name], shape, dtype, name, dev)
-
-    a = p24_logprobs_args(T, V, k, dt, temperature, logits.data_ptr(), ldz, _per_row(tokens, row, i32, "tokens", dev),
-                          to("logp", tokens is not None, row), to("entropy", entropy, row), to("stats", True, (T, 2)),
-                          to("top_logp", k > 0, top), to("top_idx", k > 0, top, i32))
+    a = p24_logprobs_args(T, V, k, dt, temperature, logits.data_ptr(), ldz,
+                          None if tokens is None else _per_row(tokens, row, torch.int32, "tokens", dev),
+                          None if tokens is None else _out(o, "logp", row, f32, dev),
+                          _out(o, "entropy", row, f32, dev) if entropy else None, _out(o, "stats", (T, 2), f32, dev),
+                          _out(o, "top_logp", (T, k), f32, dev) if k > 0 else None,
+                          _out(o, "top_idx", (T, k), torch.int32, dev) if k > 0 else None)
     _check(lib.p24_token_logprobs(C.byref(a), _stream(stream)), "p24_token_logprobs")
     return o
 
@@ -700,16 +707,18 @@ def p24_token_logprobs_bwd(logits: torch.Tensor, tokens: torch.Tensor | None, st
     return dlogits
 
 
-def _distill_args(logits, top_idx, top_val, labels, temperature, tail, dkl, dce, dlogits) -> p24_distill_args:
+def _distill_args(logits, top_idx, top_val, labels, temperature, tail, dkl, dce, dlogits, results) -> p24_distill_args:
+    """results(T): the pointers of kl, ce and stats."""
     T, V, ldz, dt = _logits(logits, "logits")
     if top_idx.dim() != 2:
         raise ValueError("top_idx must be 2-D [T, K]")
-    dev, f32, i32, K = logits.device, torch.float32, torch.int32, top_idx.shape[1]
+    dev, f32, i32, K, row = logits.device, torch.float32, torch.int32, top_idx.shape[1], (T,)
     return p24_distill_args(T, V, K, dt, temperature, P24_DISTILL_TAIL if tail else 0, logits.data_ptr(), ldz,
                             _per_row(top_idx, (T, K), i32, "top_idx", dev),
                             _per_row(top_val, (T, K), f32, "top_val", dev),
-                            _per_row(labels, (T,), i32, "labels", dev), None, None, None,
-                            _per_row(dkl, (T,), f32, "dkl", dev), _per_row(dce, (T,), f32, "dce", dev),
+                            None if labels is None else _per_row(labels, row, i32, "labels", dev), *results(T),
+                            None if dkl is None else _per_row(dkl, row, f32, "dkl", dev),
+                            None if dce is None else _per_row(dce, row, f32, "dce", dev),
                             _ptr(dlogits), 0 if dlogits is None else _logits(dlogits, "dlogits", logits)[2])
 
 
@@ -724,14 +733,15 @@ def p24_distill_topk(logits: torch.Tensor, top_idx: torch.Tensor, top_val: torch
     (fp32 [T]), or a tensor under out["dlogits"], the same call also gives the gradient dlogits
     (out["dlogits"] may be the logits themselves). See include/prune24.h."""
     o = {} if out is None else dict(out)
-    T, dev, f32 = logits.shape[0], logits.device, torch.float32
     if (dkl is not None or dce is not None) and o.get("dlogits") is None:
-        o["dlogits"] = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
-    a = _distill_args(logits, top_idx, top_val, labels, temperature, tail, dkl, dce, o.get("dlogits"))
-    for name, shape in (("kl", (T,)), ("stats", (T, 4))) + ((("ce", (T,)),) if labels is not None else ()):
-        if o.get(name) is None:
-            o[name] = torch.empty(shape, dtype=f32, device=dev)
-        setattr(a, name, _per_row(o[name], shape, f32, name, dev))
+        o["dlogits"] = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+
+    def results(T):
+        dev, f32 = logits.device, torch.float32
+        return (_out(o, "kl", (T,), f32, dev), None if labels is None else _out(o, "ce", (T,), f32, dev),
+                _out(o, "stats", (T, 4), f32, dev))
+
+    a = _distill_args(logits, top_idx, top_val, labels, temperature, tail, dkl, dce, o.get("dlogits"), results)
     _check(lib.p24_distill_topk(C.byref(a), _stream(stream)), "p24_distill_topk")
     return o
 
@@ -743,7 +753,7 @@ def p24_distill_topk_bwd(logits: torch.Tensor, top_idx: torch.Tensor, top_val: t
     """The gradient of p24_distill_topk's kl and ce for the rows' weights dkl and dce (fp32 [T],
     either may be None), from its stats: dlogits [T, V], which may be the logits themselves."""
     dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device) if dlogits is None else dlogits
-    a = _distill_args(logits, top_idx, top_val, labels, temperature, tail, dkl, dce, dlogits)
-    a.stats = _per_row(stats, (a.T, 4), torch.float32, "stats", logits.device)
+    a = _distill_args(logits, top_idx, top_val, labels, temperature, tail, dkl, dce, dlogits,
+                      lambda T: (None, None, _per_row(stats, (T, 4), torch.float32, "stats", logits.device)))
     _check(lib.p24_distill_topk_bwd(C.byref(a), _stream(stream)), "p24_distill_topk_bwd")
     return dlogits
