@@ -19,10 +19,10 @@
 //
 // Bound: HBM, one read of the logits (and one write of the gradient). Measured on GB300, of the
 // 6.69 TB/s of a plain copy: scores of 4096 x 50257 bf16 64 to 66 us, 0.93 to 0.96; gradient of
-// the same rows with entropy 134 us, 0.92, of 1000 x 32003 fp32 42 us, 0.91; entropy and top 64 of
-// 8192 x 131072 420 us, 0.77 (the alternatives' searches are then a quarter of the instructions,
-// and the walk waits for them); one row of 32000 with 20 alternatives 7.5 us, of which 2.4 us are
-// the walk and the rest the alternatives' dependent steps.
+// the same rows with entropy 133 us, 0.92, of 1000 x 32003 fp32 42 us, 0.91; entropy and top 64 of
+// 8192 x 131072 409 us, 0.79 (the alternatives' searches are a fifth of the instructions, and the
+// walk waits for them; top 20 357 us, 0.90); one row of 32000 with 20 alternatives 7.0 us, of which
+// 2.4 us are the walk and the rest the alternatives' dependent steps.
 #include <algorithm>
 #include <type_traits>
 
@@ -49,19 +49,19 @@ __device__ __forceinline__ uint64_t entry(uint32_t key, int i) {
 __device__ __forceinline__ int entry_pos(uint64_t e) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(e)); }
 __device__ __forceinline__ uint32_t entry_key(uint64_t e) { return static_cast<uint32_t>(e >> 32); }
 
-// With alternatives (19 KB for them). Top 64 of 8192 x 131072: 425 us; 454 with 320 threads and 3
-// CTAs on an SM, 481 with 192 and 5, 506 with 256 and 2. Fewer threads have fewer maxima, so more
-// candidates; more threads pay more for each search.
+// With alternatives (19 KB for them). Top 64 of 8192 x 131072: 409 us; 427 with 320 or 256 threads
+// and 3 CTAs on an SM, 472 with 192 and 5, 465 with 256 and 2. Fewer threads have fewer maxima, so
+// more candidates; more threads pay more for each search.
 using Long = Layout<256, 4, 4, 2>;
 // With alternatives, where an SM has no more than two CTAs: registers to spare. Top 20 of one row of
 // 32000 6.9 us, 7.6 in Long; of 256 rows of 50257 with 200 tokens allowed 15.6 us, 19.4.
 using Few = Layout<256, 2, 4, 2>;
 // Without: scores of 4096 x 50257 64 us; 75 with 256 threads and 4 CTAs, 82 with 512 and 2.
 using LongPlain = Layout<192, 5, 4, 3>;
-// Gradients: 2048 x 131072 175 us with all of 128 to 512 threads and 16 to 24 KB stages, 191 with 8 KB.
+// Gradients: 2048 x 131072 173 us with all of 128 to 512 threads and 16 to 24 KB stages, 191 with 8 KB.
 using LongGrad = Layout<192, 4, 8, 2>;
 // Rows of up to kShortRow vectors, where there are more than SMs: 8192 x 1001 with 5 alternatives
-// 52 us in 128 threads and 6 CTAs, 61 with 8; without 17 us with 8, 20 with 6.
+// 51 us in 128 threads and 6 CTAs, 60 with 8; without 18 us with 8, 20 with 6.
 using Short = Layout<128, 6, 2, 4>;
 using ShortPlain = Layout<128, 8, 2, 4>;
 constexpr int kShortRow = 1024;
