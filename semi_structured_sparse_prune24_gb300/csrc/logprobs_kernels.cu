@@ -323,26 +323,31 @@ __device__ __forceinline__ int top_of_part(const RowPart<T>& p, int k, uint32_t 
     n = list_from<T, L>(p, tie + 1, own16, stages, shift, sh);
     if (n >= k && n <= kList) return n;
     walk_sync<NT>();
-    if (n < k && tid < 32) {
-      constexpr int kEach = 4, kSteps = 32;
-      for (int step = 0; step < kSteps && n < k; ++step) {
-        const int i0 = step * 32 * kEach + lane;
-        float x[kEach];
+    // Ties complete a list that holds everything above them. One that ran out of room does not (and
+    // sh.n is no count of what is above them then: an fp32 bound of 0x80 covers values next to the
+    // lowest one, whose parts alone can be too many).
+    if (n < k) {
+      if (tid < 32) {
+        constexpr int kEach = 4, kSteps = 32;
+        for (int step = 0; step < kSteps && n < k; ++step) {
+          const int i0 = step * 32 * kEach + lane;
+          float x[kEach];
 #pragma unroll
-        for (int j = 0; j < kEach; ++j) x[j] = i0 + 32 * j < have ? to_f32(p.row[nth_pos(p, i0 + 32 * j)]) : 0.f;
+          for (int j = 0; j < kEach; ++j) x[j] = i0 + 32 * j < have ? to_f32(p.row[nth_pos(p, i0 + 32 * j)]) : 0.f;
 #pragma unroll
-        for (int j = 0; j < kEach; ++j) {
-          const uint32_t same = __ballot_sync(~0u, i0 + 32 * j < have && order_key(x[j]) == tie);
-          const int at = n + __popc(same & ((1u << lane) - 1));
-          if (((same >> lane) & 1u) && at < k) sh.list[at] = entry(tie, nth_pos(p, i0 + 32 * j));
-          n += __popc(same);
+          for (int j = 0; j < kEach; ++j) {
+            const uint32_t same = __ballot_sync(~0u, i0 + 32 * j < have && order_key(x[j]) == tie);
+            const int at = n + __popc(same & ((1u << lane) - 1));
+            if (((same >> lane) & 1u) && at < k) sh.list[at] = entry(tie, nth_pos(p, i0 + 32 * j));
+            n += __popc(same);
+          }
         }
+        if (lane == 0) sh.n = min(n, k);
       }
-      if (lane == 0) sh.n = min(n, k);
+      walk_sync<NT>();
+      n = sh.n;
+      if (n == k) return n;
     }
-    walk_sync<NT>();
-    n = sh.n;
-    if (n == k) return n;
   }
   select_exact<T, NT>(p, k, sh);
   return k;
