@@ -605,6 +605,8 @@ int p24_token_logprobs_bwd(const p24_logprobs_args* a, void* stream);
  *
  * p24_distill_topk_bwd -- that gradient alone, from the forward's stats (the list, labels,
  * temperature and flags as there), where the weights are known only after the loss.
+ * A row whose p_r is below e^-64 (everything off the list is masked by a finite value, say)
+ * has its sum off the list taken from the logits again: stats do not hold enough digits of it.
  *
  * 0 <= K <= P24_TOPK_MAX and 1 <= V <= 2^30, with P24_DISTILL_TAIL V <= 2^19
  * (P24_EUNSUPPORTED beyond); 1e-4 <= temperature <= 1e4.

@@ -11,7 +11,9 @@
 //                      when the list holds nearly everything). The gradient follows from the
 //                      row's second way through the ring (from L2); the listed columns and the
 //                      label are then stored again with their own terms.
-//  distill_bwd_kernel  the gradient alone, elementwise from the saved statistics.
+//  distill_bwd_kernel  the gradient alone, elementwise from the saved statistics. Where p_r is
+//                      below e^-64 (all of the bucket masked by a finite value, say) they have
+//                      too few digits of it, and the row's sum off the list is taken again.
 //
 // Bound: HBM, one read of the logits (and one write of the gradient). Measured on GB300, of the
 // 6.69 TB/s of a plain copy: loss and gradient of 8192 x 131072 bf16 with 64 entries and the bucket
@@ -125,20 +127,25 @@ __device__ __forceinline__ void list_row(const p24_distill_args& g, int64_t t, c
   }
 }
 
+struct RowStats {
+  float m, ls, lr, l1;  // maximum; ln of the sums over all, off the list, over all at temperature 1
+  // The sum off the list once more, as a reference and its ln there. Where everything off the list
+  // lies far below the maximum (masked by -1e9, say), lr has no digits left for it.
+  float rest_m, rest_ls;
+};
+
 // A row's gradient: its terms off the list and on it, the factor on q and the label's.
 struct RowGrad {
   Terms off, on;
   float wq, wl;
 };
-// m, ls, lr, l1: the row's statistics.
-__device__ __forceinline__ RowGrad row_grad(const ListShared& sh, bool two, float tau, float m, float ls, float lr,
-                                            float l1) {
+__device__ __forceinline__ RowGrad row_grad(const ListShared& sh, bool two, float tau, const RowStats& st) {
   RowGrad r;
-  float dkl = sh.dkl, dce = sh.dce;
+  float m = st.m, ls = st.ls, l1 = st.l1, dkl = sh.dkl, dce = sh.dce;
   // a row with nothing above -inf: all terms 0
   const bool none = ls == ninf();
   if (none) m = ls = l1 = dkl = dce = 0.f;
-  const float q_rest = lr == ninf() ? 0.f : sh.q_rest;  // a bucket in which the student can have nothing is dropped
+  const float q_rest = st.rest_ls == ninf() ? 0.f : sh.q_rest;  // a bucket in which the student can have nothing is dropped
   r.wq = dkl / tau;
   r.wl = dce;
   r.on.m = m, r.on.c = kLog2e / tau, r.on.off = -ls * kLog2e, r.on.off1 = -l1 * kLog2e;
@@ -146,9 +153,12 @@ __device__ __forceinline__ RowGrad row_grad(const ListShared& sh, bool two, floa
   r.on.w1 = dce;
   r.off = r.on;
   if (q_rest > 0.f) {
-    // Q p - q_r p / p_r = (Q p_r - q_r) exp(x - lr), where neither p nor p_r alone may underflow
-    const float p_rest = expf(lr - ls);
-    r.off.off = -lr * kLog2e;
+    // Q p - q_r p / p_r = (Q p_r - q_r) times the softmax of what is off the list by itself: neither
+    // p nor p_r has to be representable
+    const float p_rest = expf(st.lr - ls);
+    r.off.m = st.rest_m;
+    r.off.off = -st.rest_ls * kLog2e;
+    r.off.off1 = ((st.rest_m - m) - l1) * kLog2e;
     r.off.w = r.wq * ((sh.q_sum + q_rest) * p_rest - q_rest);
     if (!two) r.off.w += dce * p_rest;
   } else if (!two) {
@@ -198,6 +208,8 @@ using Step = Layout<256, 3, 8, 2>;
 using Grad = Layout<192, 4, 8, 2>;
 // Rows of up to kShortRow vectors: loss of 8192 x 1001 25 us, 36 with 128 threads and 6 CTAs.
 using Short = Layout<64, 10, 4, 2>;
+// Gradient of 8192 x 1001 with the bucket 18.6 us; 20.8 with 10 CTAs, whose 63 registers let no more in.
+using ShortGrad = Layout<64, 12, 4, 2>;
 constexpr int kShortRow = 1024;
 
 // The listed elements of a CTA's share, chained up by the stage and the warp that reads them:
@@ -230,10 +242,6 @@ __device__ __forceinline__ void mark_listed(const RowPart<T>& p, const ListRegs&
   }
 }
 
-struct RowStats {
-  float m, ls, lr, l1;  // maximum; ln of the sums over all, off the list, over all at temperature 1
-};
-
 // What passes between the warp that prepares the lists and the ones that walk the rows, by row
 // parity.
 struct Handover {
@@ -255,8 +263,9 @@ __device__ __forceinline__ void store_loss(const p24_distill_args& g, int64_t t,
   }
   kl = warp_sum(kl);
   if (lane != 0) return;
-  const float qr = st.lr == ninf() ? 0.f : sh.q_rest;
-  if (qr > 0.f) kl += qr * (logf(qr) - (st.lr - st.ls));
+  const float qr = st.rest_ls == ninf() ? 0.f : sh.q_rest;
+  // the factor on the distance first: the distance over tau may be beyond fp32
+  if (qr > 0.f) kl += qr * (logf(qr) - (st.rest_ls - st.ls)) + qr / g.temperature * (st.m - st.rest_m);
   g.kl[t] = kl;
   if (g.ce) g.ce[t] = sh.label < 0 ? 0.f : none ? -ninf() : st.l1 - (sh.z_label - st.m);
   if (g.stats) {
@@ -384,7 +393,9 @@ __global__ void __launch_bounds__(L::kThreads + 32, L::kCtas) distill_kernel(con
       RowStats st;
       st.m = all.s == 0.f ? ninf() : all.m;
       st.ls = all.s == 0.f ? ninf() : logf(all.s);
-      st.lr = !tail ? 0.f : rest.s == 0.f ? ninf() : logf(rest.s) + (rest.m - st.m) / tau;  // at the reference m
+      st.rest_m = rest.m;
+      st.rest_ls = !tail ? 0.f : rest.s == 0.f ? ninf() : logf(rest.s);
+      st.lr = !tail ? 0.f : rest.s == 0.f ? ninf() : st.rest_ls + (rest.m - st.m) / tau;  // at the reference m
       st.l1 = !g.labels ? 0.f : !kTwo ? st.ls : one.s == 0.f ? ninf() : logf(one.s);
       if (tid == 0) {
         hand.row[par] = st;
@@ -393,7 +404,7 @@ __global__ void __launch_bounds__(L::kThreads + 32, L::kCtas) distill_kernel(con
       if constexpr (kGrad) {
         T* out = static_cast<T*>(g.dlogits) + t * g.ldd;
         const bool aligned = (reinterpret_cast<uintptr_t>(out) & 15u) == (reinterpret_cast<uintptr_t>(p.row) & 15u);
-        const RowGrad rg = row_grad(sh, kTwo, tau, st.m, st.ls, st.lr, st.l1);
+        const RowGrad rg = row_grad(sh, kTwo, tau, st);
         if (tid < p.edges) out[p.edge_pos(tid)] = static_cast<T>(rg.off.template one<kTwo>(edge_here));
         store_row<T, kTwo, R>(ring, out, aligned, p, stages, rg.off);
         walk_sync<NT>();
@@ -406,46 +417,122 @@ __global__ void __launch_bounds__(L::kThreads + 32, L::kCtas) distill_kernel(con
   }
 }
 
+// ln p_r from which the saved statistics give the bucket's gradient: the softmax off the list comes
+// out of lr with an error of 4u |lr|, here 2^-16, as much as a sum of a long row may have. Rows
+// below take their sum off the list again: a whole batch of them, 2048 x 131072, 620 us instead of 173.
+constexpr float kFar = -64.f;
+
+// This CTA's sums off the list over its share of a row, from memory: all walking threads. hit: which
+// vectors (modulo 32 kHit) hold a listed element; the list is searched for those alone (with 32 words
+// nearly every warp searched it: 2000 us for that batch).
+constexpr int kHit = 256;
+template <typename T, int NT>
+__device__ __noinline__ Sums sums_off_list(const T* row, int V, int part, int parts, const ListShared& sh, int K, float c,
+                                           uint32_t (&hit)[kHit]) {
+  constexpr int N = Vec<T>::N;
+  const RowPart<T> p(row, V, part, parts);
+  const int tid = threadIdx.x;
+  for (int i = tid; i < kHit; i += NT) hit[i] = 0;
+  walk_sync<NT>();
+  for (int j = tid; j < K; j += NT) {
+    const int i = sh.idx[j];
+    if (i < p.head || i >= p.tail0) continue;
+    const int v = (i - p.head) / N;
+    atomicOr(&hit[v / 32 % kHit], 1u << (v & 31));
+  }
+  walk_sync<NT>();
+  Walk<false> w;
+  if (tid < p.edges) {
+    const int pos = p.edge_pos(tid);
+    bool listed = false;
+    for (int j = 0; j < K; ++j) listed |= sh.idx[j] == pos;
+    if (!listed) w.add_one(to_f32(p.row[pos]), c);
+  }
+#pragma unroll 1
+  for (int v = p.lo + tid; v < p.hi; v += NT) {
+    uint4 x = p.body[v];
+    if (hit[v / 32 % kHit] >> (v & 31) & 1u) {
+      uint32_t r[4] = {x.x, x.y, x.z, x.w};
+      const int i0 = p.vec_pos(v);
+#pragma unroll 1
+      for (int j = 0; j < K; ++j) {
+        const int e = sh.idx[j] - i0;
+        if (e < 0 || e >= N) continue;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          if (e != i) continue;
+          if constexpr (sizeof(T) == 2)
+            r[i / 2] = (i & 1) ? (r[i / 2] & 0xffffu) | 0xff800000u : (r[i / 2] & 0xffff0000u) | 0xff80u;
+          else
+            r[i] = Vec<T>::kFill;
+        }
+      }
+      x = make_uint4(r[0], r[1], r[2], r[3]);
+    }
+    w.raise(max_of<T>(max_vec<T>(Vec<T>::kFill, x)), c);
+    w.template add<T>(x, c);
+  }
+  return w.sums();
+}
+
 // The gradient from saved statistics. The CTA's last warp fills the ring, the others walk the rows.
-template <typename T, bool kTwo, typename L>
+// A row is split in `parts`. kBucket: over a cluster, whose CTAs join the sums off the list of a row
+// for which the statistics do not do.
+template <typename T, bool kTwo, bool kBucket, typename L>
 __global__ void __launch_bounds__(L::kThreads, L::kCtas) distill_bwd_kernel(const p24_distill_args g, int parts, int* status) {
   using R = Ring<T, L>;
   constexpr int NT = L::NT, N = Vec<T>::N;
   extern __shared__ __align__(128) uint4 ring_data[];
   __shared__ RingShared<L::S> ring_sh;
   __shared__ ListShared lists[2];
+  __shared__ JoinShared joins;  // kBucket
+  __shared__ uint32_t hit[kHit];  // kBucket
   const int tid = threadIdx.x, warp = tid >> 5, V = static_cast<int>(g.V), K = static_cast<int>(g.K);
   const int part = blockIdx.x % parts;
   const float tau = g.temperature;
   const T* logits = static_cast<const T*>(g.logits);
   const int stages = row_stages(V / N, parts, L::kStage);
   R ring{logits, g.ldz, blockIdx.x / parts, gridDim.x / parts, g.T, V, part, parts, stages, 1, ring_data, &ring_sh, status};
+  if (kBucket && tid == 0) join_init(joins, parts);
   ring.start();
-  begin(1);
+  begin(kBucket ? parts : 1);
   if (tid >= NT) {
     if (tid == NT) ring.run();
     return;
   }
   float edge = load_edge(RowPart<T>(logits + ring.first * g.ldz, V, part, parts));
-  int64_t r = 0;
+  int64_t r = 0, joined = 0;
   for (int64_t t = ring.first; t < g.T; t += ring.step, ++r) {
     const RowPart<T> p(logits + t * g.ldz, V, part, parts);
     ListShared& sh = lists[r & 1];
-    const RowStats st{g.stats[4 * t], g.stats[4 * t + 1], g.stats[4 * t + 2], g.stats[4 * t + 3]};
+    RowStats st{g.stats[4 * t], g.stats[4 * t + 1], g.stats[4 * t + 2], g.stats[4 * t + 3], 0.f, 0.f};
     if (warp == 0) {
       ListRegs list;
       list_row(g, t, p, true, sh, list);  // another part's logits are being overwritten, in place
     }
     walk_sync<NT>();
+    if constexpr (kBucket) {
+      st.rest_m = st.m;
+      st.rest_ls = st.lr;
+      // the same in every CTA of the cluster: from the statistics and the list
+      if (sh.q_rest > 0.f && st.ls != ninf() && !(st.lr - st.ls >= kFar)) {
+        const float c = kLog2e / tau;
+        Sums rest = sums_off_list<T, NT>(p.row, V, part, parts, sh, K, c, hit), unused{0.f, 0.f, 0.f};
+        row_join<false, false, NT>(rest, c, unused, c, joins, joined++, part, parts, &ring_sh.abort, status);
+        st.rest_m = rest.m;
+        st.rest_ls = rest.s == 0.f ? ninf() : logf(rest.s);
+      }
+    }
     T* out = static_cast<T*>(g.dlogits) + t * g.ldd;
     const bool aligned = (reinterpret_cast<uintptr_t>(out) & 15u) == (reinterpret_cast<uintptr_t>(p.row) & 15u);
-    const RowGrad rg = row_grad(sh, kTwo, tau, st.m, st.ls, st.lr, st.l1);
+    const RowGrad rg = row_grad(sh, kTwo, tau, st);
     if (tid < p.edges) out[p.edge_pos(tid)] = static_cast<T>(rg.off.template one<kTwo>(edge));
     if (t + ring.step < g.T) edge = load_edge(RowPart<T>(logits + (t + ring.step) * g.ldz, V, part, parts));
     store_row<T, kTwo, R>(ring, out, aligned, p, stages, rg.off);
     walk_sync<NT>();
     store_listed<T, kTwo, NT>(out, p, sh, K, rg);
   }
+  if constexpr (kBucket) end(parts, &ring_sh.abort);
 }
 
 template <typename T, bool kTwo, bool kGrad>
@@ -471,10 +558,14 @@ cudaError_t launch_distill_as(const p24_distill_args& g, int* status, cudaStream
 template <typename T, bool kTwo>
 cudaError_t launch_distill_bwd_as(const p24_distill_args& g, int* status, cudaStream_t s) {
   const int64_t vecs = g.V / Vec<T>::N;
+  const bool tail = (g.flags & P24_DISTILL_TAIL) != 0;
   if (vecs <= kShortRow)
-    return launch_parts(distill_bwd_kernel<T, kTwo, Short>, Short::kThreads, g.T, 1, Short::kRing, s, g, 1, status);
-  const int parts = row_split(g.T, vecs, sm_count() * Grad::kCtas, 64, 512);
-  return launch_parts(distill_bwd_kernel<T, kTwo, Grad>, Grad::kThreads, g.T, parts, Grad::kRing, s, g, parts, status);
+    return launch_parts(tail ? distill_bwd_kernel<T, kTwo, true, ShortGrad> : distill_bwd_kernel<T, kTwo, false, ShortGrad>,
+                        ShortGrad::kThreads, g.T, 1, ShortGrad::kRing, s, g, 1, status);
+  const int parts = row_split(g.T, vecs, sm_count() * Grad::kCtas, tail ? kMaxRanks : 64, 512);
+  if (tail)
+    return launch_rows(distill_bwd_kernel<T, kTwo, true, Grad>, Grad::kThreads, g.T, parts, Grad::kRing, s, g, parts, status);
+  return launch_parts(distill_bwd_kernel<T, kTwo, false, Grad>, Grad::kThreads, g.T, parts, Grad::kRing, s, g, parts, status);
 }
 
 template <typename T>
