@@ -8,6 +8,7 @@ if the shared library is missing, importing this module raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 from dataclasses import dataclass
@@ -146,6 +147,15 @@ def _stream(stream) -> int | None:
             return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _on(stream):
+    """Context in which torch allocates and launches on the stream of a call (None: the current one)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream))
+    return torch.cuda.stream(stream)
 
 
 def _ptr(t: torch.Tensor | None) -> int | None:

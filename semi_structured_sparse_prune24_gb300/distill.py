@@ -30,7 +30,8 @@ class DistillHead:
     def teacher_list(self, Y: torch.Tensor, W: torch.Tensor, k: int, temperature: float = 1.0,
                      out: dict | None = None, stream=None) -> dict:
         """A teacher's list for these tokens from its last hidden states Y [M, d] and its head
-        W [V, d]: top_idx, top_logp [M, k], and its entropy. Uses this head's logits buffer."""
+        W [V, d]: top_idx, top_logp [M, k], and its entropy, all of softmax(logits / temperature).
+        Uses this head's logits buffer."""
         N.p24_gemm_nt(Y, W, self.logits, stream=stream)
         return N.p24_token_logprobs(self.logits, k=k, temperature=temperature, out=out, stream=stream)
 
@@ -43,8 +44,14 @@ class DistillHead:
              labels: torch.Tensor | None = None, dce: torch.Tensor | None = None, temperature: float = 1.0,
              tail: bool = True, out: dict | None = None, stream=None) -> dict:
         """The loss of hidden states Y [M, d] under the head W [V, d], and its gradients: kl (and ce)
-        [M], dY [M, d], dW [V, d]. dkl, dce: each token's weight in the loss (fp32 [M])."""
+        [M], dY [M, d], dW [V, d]. dkl, dce: each token's weight in the loss (fp32 [M]).
+        top_logp: the teacher's log probabilities at this temperature, as teacher_list gives them; the
+        teacher is renormalised on its list (tail=False) or has the rest as one bucket (tail=True)."""
         o = {} if out is None else dict(out)
+        if not tail and temperature != 1.0:
+            # p24_distill_topk divides a list that it renormalises by the temperature: this one is at it
+            with N._on(stream):
+                top_logp = top_logp * temperature
         N.p24_gemm_nt(Y, W, self.logits, stream=stream)
         o.update(N.p24_distill_topk(self.logits, top_idx, top_logp, labels, temperature, tail, dkl, dce,
                                     out={**{k: o[k] for k in ("kl", "ce", "stats") if k in o}, "dlogits": self.logits},
