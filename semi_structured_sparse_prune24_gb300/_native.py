@@ -669,13 +669,16 @@ def _per_row(t: torch.Tensor | None, shape: tuple, dtype, name: str, device) -> 
     raise ValueError(f"{name} must be a contiguous {shape} tensor on the logits' device")
 
 
-def _out(o: dict, name: str, shape: tuple, dtype, device) -> int:
-    """Pointer of the output `name` of a call: the caller's tensor in o, or a new one put there."""
-    t = o.get(name)
-    if t is not None:
-        return _per_row(t, shape, dtype, name, device)
-    t = o[name] = torch.empty(shape, dtype=dtype, device=device)
-    return t.data_ptr()
+def _out(o: dict, given: dict, name: str, shape: tuple, dtype, device) -> int:
+    """Pointer of the output `name` of a call, put in its results o: the caller's tensor, or a new one."""
+    t = given.get(name)
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        p = t.data_ptr()
+    else:
+        p = _per_row(t, shape, dtype, name, device)
+    o[name] = t
+    return p
 
 
 def p24_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, k: int = 0,
@@ -684,16 +687,16 @@ def p24_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None,
     """Per row of logits [T, V] (bf16 or fp32), of softmax(logits / temperature): logp [T] of
     tokens (int32 [T]; one outside 0..V-1 gives 0), entropy [T] (if asked for), the k most
     probable entries top_logp, top_idx [T, k], and stats [T, 2] for the backward, as a dict.
-    out: tensors to write to, under those names. See include/prune24.h."""
+    out: tensors to write to, under those names; others of it are not in the result. See include/prune24.h."""
     T, V, ldz, dt = _logits(logits, "logits")
     dev, f32, row = logits.device, torch.float32, (T,)
-    o = {} if out is None else dict(out)
+    o, given = {}, {} if out is None else out
     a = p24_logprobs_args(T, V, k, dt, temperature, logits.data_ptr(), ldz,
                           None if tokens is None else _per_row(tokens, row, torch.int32, "tokens", dev),
-                          None if tokens is None else _out(o, "logp", row, f32, dev),
-                          _out(o, "entropy", row, f32, dev) if entropy else None, _out(o, "stats", (T, 2), f32, dev),
-                          _out(o, "top_logp", (T, k), f32, dev) if k > 0 else None,
-                          _out(o, "top_idx", (T, k), torch.int32, dev) if k > 0 else None)
+                          None if tokens is None else _out(o, given, "logp", row, f32, dev),
+                          _out(o, given, "entropy", row, f32, dev) if entropy else None, _out(o, given, "stats", (T, 2), f32, dev),
+                          _out(o, given, "top_logp", (T, k), f32, dev) if k > 0 else None,
+                          _out(o, given, "top_idx", (T, k), torch.int32, dev) if k > 0 else None)
     _check(lib.p24_token_logprobs(C.byref(a), _stream(stream)), "p24_token_logprobs")
     return o
 
@@ -741,17 +744,21 @@ def p24_distill_topk(logits: torch.Tensor, top_idx: torch.Tensor, top_val: torch
     entropy ce [T], and stats [T, 4] for the backward, as a dict. tail: the teacher's remaining
     probability is one bucket (else the list is renormalised). With the rows' weights dkl and/or dce
     (fp32 [T]), or a tensor under out["dlogits"], the same call also gives the gradient dlogits
-    (out["dlogits"] may be the logits themselves). See include/prune24.h."""
-    o = {} if out is None else dict(out)
-    if (dkl is not None or dce is not None) and o.get("dlogits") is None:
-        o["dlogits"] = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    (out["dlogits"] may be the logits themselves). What the call does not write of out is not in the
+    result. See include/prune24.h."""
+    o, given = {}, {} if out is None else out
+    dlogits = given.get("dlogits")
+    if (dkl is not None or dce is not None) and dlogits is None:
+        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    if dlogits is not None:
+        o["dlogits"] = dlogits
 
     def results(T):
         dev, f32 = logits.device, torch.float32
-        return (_out(o, "kl", (T,), f32, dev), None if labels is None else _out(o, "ce", (T,), f32, dev),
-                _out(o, "stats", (T, 4), f32, dev))
+        return (_out(o, given, "kl", (T,), f32, dev), None if labels is None else _out(o, given, "ce", (T,), f32, dev),
+                _out(o, given, "stats", (T, 4), f32, dev))
 
-    a = _distill_args(logits, top_idx, top_val, labels, temperature, tail, dkl, dce, o.get("dlogits"), results)
+    a = _distill_args(logits, top_idx, top_val, labels, temperature, tail, dkl, dce, dlogits, results)
     _check(lib.p24_distill_topk(C.byref(a), _stream(stream)), "p24_distill_topk")
     return o
 

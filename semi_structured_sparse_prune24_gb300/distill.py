@@ -47,18 +47,17 @@ class DistillHead:
         [M], dY [M, d], dW [V, d]. dkl, dce: each token's weight in the loss (fp32 [M]).
         top_logp: the teacher's log probabilities at this temperature, as teacher_list gives them; the
         teacher is renormalised on its list (tail=False) or has the rest as one bucket (tail=True)."""
-        o = {} if out is None else dict(out)
+        given = {} if out is None else out
         if not tail and temperature != 1.0:
             # p24_distill_topk divides a list that it renormalises by the temperature: this one is at it
             with N._on(stream):
                 top_logp = top_logp * temperature
         N.p24_gemm_nt(Y, W, self.logits, stream=stream)
-        o.update(N.p24_distill_topk(self.logits, top_idx, top_logp, labels, temperature, tail, dkl, dce,
-                                    out={**{k: o[k] for k in ("kl", "ce", "stats") if k in o}, "dlogits": self.logits},
-                                    stream=stream))
+        o = N.p24_distill_topk(self.logits, top_idx, top_logp, labels, temperature, tail, dkl, dce,
+                               out={**given, "dlogits": self.logits}, stream=stream)
         N.p24_transpose(W, self.W_T, stream=stream)
-        o["dY"] = N.p24_gemm_nt(self.logits, self.W_T, o.get("dY"), stream=stream)
-        o["dW"] = N.p24_gemm_tn(self.logits, Y, o.get("dW"), stream=stream)
+        o["dY"] = N.p24_gemm_nt(self.logits, self.W_T, given.get("dY"), stream=stream)
+        o["dW"] = N.p24_gemm_tn(self.logits, Y, given.get("dW"), stream=stream)
         return o
 
 
