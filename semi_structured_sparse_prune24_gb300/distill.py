@@ -15,6 +15,12 @@ import torch
 from . import _native as N
 
 
+def _shape(t: torch.Tensor | None, shape: tuple, name: str) -> None:
+    """The calls below take sizes from their inputs and write that much to this module's buffers."""
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
+
+
 class DistillHead:
     """Logits = Y W^T of M tokens over a vocabulary of V (a multiple of 8), with the loss
     of p24_distill_topk on them."""
@@ -27,17 +33,23 @@ class DistillHead:
         self.logits = torch.empty((M, V), dtype=bf, device=device)    # and their gradient, in place
         self.W_T = torch.empty((d, V), dtype=bf, device=device)       # for the product with the gradient
 
+    def _product(self, Y: torch.Tensor, W: torch.Tensor, stream) -> None:
+        """Logits of hidden states under a head of any width (a teacher's may differ from d)."""
+        _shape(Y, (self.M, Y.shape[-1]), "Y")
+        _shape(W, (self.V, Y.shape[-1]), "W")
+        N.p24_gemm_nt(Y, W, self.logits, stream=stream)
+
     def teacher_list(self, Y: torch.Tensor, W: torch.Tensor, k: int, temperature: float = 1.0,
                      out: dict | None = None, stream=None) -> dict:
         """A teacher's list for these tokens from its last hidden states Y [M, d] and its head
         W [V, d]: top_idx, top_logp [M, k], and its entropy, all of softmax(logits / temperature).
         Uses this head's logits buffer."""
-        N.p24_gemm_nt(Y, W, self.logits, stream=stream)
+        self._product(Y, W, stream)
         return N.p24_token_logprobs(self.logits, k=k, temperature=temperature, out=out, stream=stream)
 
     def score(self, Y: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, stream=None) -> dict:
         """Log probabilities of tokens (int32 [M]) and the entropy, e.g. of held-out text."""
-        N.p24_gemm_nt(Y, W, self.logits, stream=stream)
+        self._product(Y, W, stream)
         return N.p24_token_logprobs(self.logits, tokens, stream=stream)
 
     def step(self, Y: torch.Tensor, W: torch.Tensor, top_idx: torch.Tensor, top_logp: torch.Tensor, dkl: torch.Tensor,
@@ -48,11 +60,14 @@ class DistillHead:
         top_logp: the teacher's log probabilities at this temperature, as teacher_list gives them; the
         teacher is renormalised on its list (tail=False) or has the rest as one bucket (tail=True)."""
         given = {} if out is None else out
+        _shape(Y, (self.M, self.d), "Y")
+        _shape(given.get("dY"), (self.M, self.d), "dY")
+        _shape(given.get("dW"), (self.V, self.d), "dW")
         if not tail and temperature != 1.0:
             # p24_distill_topk divides a list that it renormalises by the temperature: this one is at it
             with N._on(stream):
                 top_logp = top_logp * temperature
-        N.p24_gemm_nt(Y, W, self.logits, stream=stream)
+        self._product(Y, W, stream)
         o = N.p24_distill_topk(self.logits, top_idx, top_logp, labels, temperature, tail, dkl, dce,
                                out={**given, "dlogits": self.logits}, stream=stream)
         N.p24_transpose(W, self.W_T, stream=stream)
@@ -67,6 +82,7 @@ class DistillStep:
 
     def __init__(self, M: int, d: int, ffn: int, V: int, device="cuda"):
         self.head = DistillHead(M, d, V, device)
+        self.ffn = ffn
         S = N.Sparse24.empty
         self.up, self.up_T = S(ffn, d, device), S(d, ffn, device)
         self.down, self.down_T = S(d, ffn, device), S(ffn, d, device)
@@ -74,6 +90,11 @@ class DistillStep:
     def run(self, X, W_up, b_up, W_down, b_down, W_head, top_idx, top_logp, dkl, labels=None, dce=None,
             temperature: float = 1.0, tail: bool = True, stream=None) -> dict:
         """Returns kl (and ce) per token and the gradients dX, dW_up, db_up, dW_down, db_down, dW_head."""
+        M, d, ffn = self.head.M, self.head.d, self.ffn
+        for t, shape, name in ((X, (M, d), "X"), (W_up, (ffn, d), "W_up"), (b_up, (ffn,), "b_up"),
+                               (W_down, (d, ffn), "W_down"), (b_down, (d,), "b_down"),
+                               (W_head, (self.head.V, d), "W_head")):
+            _shape(t, shape, name)
         N.prune24_compress_both(W_up, self.up, self.up_T, stream=stream)
         N.prune24_compress_both(W_down, self.down, self.down_T, stream=stream)
         H = N.spmm24_fwd(X, self.up, b_up, relu=True, stream=stream)
@@ -81,7 +102,7 @@ class DistillStep:
         o = self.head.step(Y, W_head, top_idx, top_logp, dkl, labels, dce, temperature, tail, stream=stream)
         o["dW_head"] = o.pop("dW")
         dY = o.pop("dY")
-        o["db_up"] = torch.empty(H.shape[1], dtype=torch.float32, device=X.device)
+        o["db_up"] = torch.empty(ffn, dtype=torch.float32, device=X.device)
         dH = N.spmm24_bwd_dx(dY, self.down_T, gate=H, dbias=o["db_up"], stream=stream)
         o["db_down"] = N.p24_colsum(dY, stream=stream)
         o["dW_down"] = N.masked_dw_gemm(dY, H, self.down, stream=stream)
