@@ -7,6 +7,9 @@ holds the student's head (the unembedding): logits, loss and gradients, one pass
 over the logits and in place, so that one [M, V] buffer is all it needs.
 DistillStep runs a whole step of a student whose last layer is a 2:4 FFN: prune,
 forward, head, loss and backward, on the library's calls.
+
+A call with stream=s is the call under torch.cuda.stream(s): what it allocates, intermediates that
+are dropped when it returns among them, is that stream's memory.
 """
 from __future__ import annotations
 
@@ -33,24 +36,26 @@ class DistillHead:
         self.logits = torch.empty((M, V), dtype=bf, device=device)    # and their gradient, in place
         self.W_T = torch.empty((d, V), dtype=bf, device=device)       # for the product with the gradient
 
-    def _product(self, Y: torch.Tensor, W: torch.Tensor, stream) -> None:
+    def _product(self, Y: torch.Tensor, W: torch.Tensor) -> None:
         """Logits of hidden states under a head of any width (a teacher's may differ from d)."""
         _shape(Y, (self.M, Y.shape[-1]), "Y")
         _shape(W, (self.V, Y.shape[-1]), "W")
-        N.p24_gemm_nt(Y, W, self.logits, stream=stream)
+        N.p24_gemm_nt(Y, W, self.logits)
 
     def teacher_list(self, Y: torch.Tensor, W: torch.Tensor, k: int, temperature: float = 1.0,
                      out: dict | None = None, stream=None) -> dict:
         """A teacher's list for these tokens from its last hidden states Y [M, d] and its head
         W [V, d]: top_idx, top_logp [M, k], and its entropy, all of softmax(logits / temperature).
         Uses this head's logits buffer."""
-        self._product(Y, W, stream)
-        return N.p24_token_logprobs(self.logits, k=k, temperature=temperature, out=out, stream=stream)
+        with N._on(stream):
+            self._product(Y, W)
+            return N.p24_token_logprobs(self.logits, k=k, temperature=temperature, out=out)
 
     def score(self, Y: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, stream=None) -> dict:
         """Log probabilities of tokens (int32 [M]) and the entropy, e.g. of held-out text."""
-        self._product(Y, W, stream)
-        return N.p24_token_logprobs(self.logits, tokens, stream=stream)
+        with N._on(stream):
+            self._product(Y, W)
+            return N.p24_token_logprobs(self.logits, tokens)
 
     def step(self, Y: torch.Tensor, W: torch.Tensor, top_idx: torch.Tensor, top_logp: torch.Tensor, dkl: torch.Tensor,
              labels: torch.Tensor | None = None, dce: torch.Tensor | None = None, temperature: float = 1.0,
@@ -63,16 +68,16 @@ class DistillHead:
         _shape(Y, (self.M, self.d), "Y")
         _shape(given.get("dY"), (self.M, self.d), "dY")
         _shape(given.get("dW"), (self.V, self.d), "dW")
-        if not tail and temperature != 1.0:
-            # p24_distill_topk divides a list that it renormalises by the temperature: this one is at it
-            with N._on(stream):
+        with N._on(stream):
+            if not tail and temperature != 1.0:
+                # p24_distill_topk divides a list that it renormalises by the temperature: this one is at it
                 top_logp = top_logp * temperature
-        self._product(Y, W, stream)
-        o = N.p24_distill_topk(self.logits, top_idx, top_logp, labels, temperature, tail, dkl, dce,
-                               out={**given, "dlogits": self.logits}, stream=stream)
-        N.p24_transpose(W, self.W_T, stream=stream)
-        o["dY"] = N.p24_gemm_nt(self.logits, self.W_T, given.get("dY"), stream=stream)
-        o["dW"] = N.p24_gemm_tn(self.logits, Y, given.get("dW"), stream=stream)
+            self._product(Y, W)
+            o = N.p24_distill_topk(self.logits, top_idx, top_logp, labels, temperature, tail, dkl, dce,
+                                   out={**given, "dlogits": self.logits})
+            N.p24_transpose(W, self.W_T)
+            o["dY"] = N.p24_gemm_nt(self.logits, self.W_T, given.get("dY"))
+            o["dW"] = N.p24_gemm_tn(self.logits, Y, given.get("dW"))
         return o
 
 
@@ -95,17 +100,18 @@ class DistillStep:
                                (W_down, (d, ffn), "W_down"), (b_down, (d,), "b_down"),
                                (W_head, (self.head.V, d), "W_head")):
             _shape(t, shape, name)
-        N.prune24_compress_both(W_up, self.up, self.up_T, stream=stream)
-        N.prune24_compress_both(W_down, self.down, self.down_T, stream=stream)
-        H = N.spmm24_fwd(X, self.up, b_up, relu=True, stream=stream)
-        Y = N.spmm24_fwd(H, self.down, b_down, stream=stream)
-        o = self.head.step(Y, W_head, top_idx, top_logp, dkl, labels, dce, temperature, tail, stream=stream)
-        o["dW_head"] = o.pop("dW")
-        dY = o.pop("dY")
-        o["db_up"] = torch.empty(ffn, dtype=torch.float32, device=X.device)
-        dH = N.spmm24_bwd_dx(dY, self.down_T, gate=H, dbias=o["db_up"], stream=stream)
-        o["db_down"] = N.p24_colsum(dY, stream=stream)
-        o["dW_down"] = N.masked_dw_gemm(dY, H, self.down, stream=stream)
-        o["dX"] = N.spmm24_bwd_dx(dH, self.up_T, stream=stream)
-        o["dW_up"] = N.masked_dw_gemm(dH, X, self.up, stream=stream)
+        with N._on(stream):
+            N.prune24_compress_both(W_up, self.up, self.up_T)
+            N.prune24_compress_both(W_down, self.down, self.down_T)
+            H = N.spmm24_fwd(X, self.up, b_up, relu=True)
+            Y = N.spmm24_fwd(H, self.down, b_down)
+            o = self.head.step(Y, W_head, top_idx, top_logp, dkl, labels, dce, temperature, tail)
+            o["dW_head"] = o.pop("dW")
+            dY = o.pop("dY")
+            o["db_up"] = torch.empty(ffn, dtype=torch.float32, device=X.device)
+            dH = N.spmm24_bwd_dx(dY, self.down_T, gate=H, dbias=o["db_up"])
+            o["db_down"] = N.p24_colsum(dY)
+            o["dW_down"] = N.masked_dw_gemm(dY, H, self.down)
+            o["dX"] = N.spmm24_bwd_dx(dH, self.up_T)
+            o["dW_up"] = N.masked_dw_gemm(dH, X, self.up)
         return o
