@@ -436,7 +436,8 @@ def p24_colsum(G: torch.Tensor, out: torch.Tensor | None = None, ws: torch.Tenso
     out = torch.empty(N, dtype=torch.float32, device=G.device) if out is None else out
     need = int(lib.p24_colsum_workspace_size(M, N))
     if ws is None:
-        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=G.device)
+        with _on(stream):  # dropped on return, with the kernels still queued: that stream's memory
+            ws = torch.empty(max(need, 16), dtype=torch.uint8, device=G.device)
     _check(lib.p24_colsum(G.data_ptr(), M, N, ldg, out.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
                           _stream(stream)), "p24_colsum")
     return out
@@ -532,7 +533,8 @@ def ffn24_step(X, W_up, b_up, W_down, b_down, dY, act24: bool = False, out: dict
     if vnm:
         a.vnm_V, a.vnm_M = int(vnm[0]), int(vnm[1])
     if workspace is None:
-        workspace = torch.empty(int(lib.ffn24_workspace_size_args(C.byref(a))), dtype=torch.uint8, device=dev)
+        with _on(stream):  # dropped on return, with the kernels still queued: that stream's memory
+            workspace = torch.empty(int(lib.ffn24_workspace_size_args(C.byref(a))), dtype=torch.uint8, device=dev)
     structs = {k: w[k].c() for k in STEP_WEIGHTS if w.get(k) is not None}  # alive for the call
     for k, st in structs.items():
         setattr(a, k, C.pointer(st))
