@@ -24,6 +24,7 @@
 #include <type_traits>
 
 #include "head_rows.cuh"
+#include "p24_chain.h"
 
 namespace p24 {
 namespace {
@@ -332,10 +333,13 @@ __global__ void __launch_bounds__(L::kThreads + 32, L::kCtas) distill_kernel(con
       const int par = r & 1;
       const uint32_t phase = (r >> 1) & 1;
       if (rank == 0) {
-        p24_wait(&hand.stats[par], phase, &ring_sh.abort, status);
+        if (!__all_sync(~0u, p24_wait(&hand.stats[par], phase, &ring_sh.abort, status))) break;
         store_loss(g, t, lists[par], hand.row[par]);
       }
-      p24_wait(&hand.freed[par], phase, &ring_sh.abort, status);
+      // Once a wait of this CTA has run out, a list may not have been used up: no other is chained to it.
+      const bool freed = p24_wait(&hand.freed[par], phase, &ring_sh.abort, status) &&
+                         *const_cast<volatile int*>(&ring_sh.abort) == 0;
+      if (!__all_sync(~0u, freed)) break;
       prepare(r + 2);
     }
   } else {
@@ -348,7 +352,8 @@ __global__ void __launch_bounds__(L::kThreads + 32, L::kCtas) distill_kernel(con
       const ListShared& sh = lists[par];
       const Marks& mk = marks[par];
       int* head = heads + par * stages * L::kWarps;
-      p24_wait(&hand.ready[par], (r >> 1) & 1, &ring_sh.abort, status);
+      // false where the wait ran out: nothing of the list is used then, it may be half written
+      const bool listed = __all_sync(~0u, p24_wait(&hand.ready[par], (r >> 1) & 1, &ring_sh.abort, status));
 
       // one pass over the row: sums (tail: off the list)
       Walk<false> w, w1;
@@ -370,13 +375,14 @@ __global__ void __launch_bounds__(L::kThreads + 32, L::kCtas) distill_kernel(con
         }
         if (tail) {
           // the listed elements become -inf in the stage: the sums off the list have their own maximum
-          int j = head[at * L::kWarps + warp];
+          const int j = listed ? head[at * L::kWarps + warp] : -1;
           if (j >= 0) {
             __syncwarp();
             if ((tid & 31) == 0) head[at * L::kWarps + warp] = -1;  // for the row after the next
-            for (; j >= 0; j = mk.next[j])
-              if ((tid & 31) == mk.lane[j])
-                *reinterpret_cast<T*>(reinterpret_cast<char*>(data - tid) + mk.byte[j]) = static_cast<T>(ninf());
+            chain_walk(j, mk.next, kTopMax, [&](int e) {
+              if ((tid & 31) == mk.lane[e])
+                *reinterpret_cast<T*>(reinterpret_cast<char*>(data - tid) + mk.byte[e]) = static_cast<T>(ninf());
+            });
             fence_proxy_async_smem();  // the next copy into this stage comes after these stores
             __syncwarp();
           }
@@ -408,7 +414,7 @@ __global__ void __launch_bounds__(L::kThreads + 32, L::kCtas) distill_kernel(con
         if (tid < p.edges) out[p.edge_pos(tid)] = static_cast<T>(rg.off.template one<kTwo>(edge_here));
         store_row<T, kTwo, R>(ring, out, aligned, p, stages, rg.off);
         walk_sync<NT>();
-        store_listed<T, kTwo, NT>(out, p, sh, K, rg);
+        if (listed) store_listed<T, kTwo, NT>(out, p, sh, K, rg);
       }
       __syncwarp();
       if ((tid & 31) == 0) mbar_arrive(&hand.freed[par]);
