@@ -522,9 +522,12 @@ int ffn24_step_traced(const p24_ffn_args* a, void* workspace, size_t ws_bytes, v
  * their ends element by element). Sums and statistics are fp32 and are added in a fixed
  * order: repeated calls are bit-identical.
  *
- * A logit of -inf is masked: probability 0, gradient 0. A row of nothing else has no
- * distribution: log probabilities -inf, entropy 0, losses +inf, gradients 0. A row with a
- * NaN or +inf gives NaN. Logits of the type's lowest finite value are ordinary numbers.
+ * A logit of -inf is masked: probability 0 and gradient 0, except what the row's token, label
+ * or list names: a masked token has logp -inf and gradient dlogp / tau, a masked label ce +inf
+ * and gradient -dce, a masked listed entry with q > 0 kl +inf and gradient -dkl q / tau. A row
+ * of nothing else has no distribution: log probabilities -inf, entropy 0, losses +inf,
+ * gradients 0. A row with a NaN or +inf gives NaN. Logits of the type's lowest finite value are
+ * ordinary numbers.
  *
  * A call's first launch of a kernel looks up how many of its CTAs the device holds; like
  * every first call it belongs before a stream capture.

@@ -99,3 +99,31 @@ def test_bucket_of_masked_logits(P, dtype, mask, tau, T, V, mode):  # noqa: F811
         bound = rel * np.abs(d) + 2.0 ** -126 + (2.0 ** -8 * np.abs(d) if dtype == BF else 0)
         bound[idx[t]] += (w[t] / tau + c[t]) * (e_s(V) + 64 * U)  # differences of terms of at most the weights
         close(o["dlogits"][t], d, bound, ("dlogits", t))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("tail", [False, True])
+def test_masked_token_label_and_listed_entry(P, dtype, tail):  # noqa: F811
+    """A logit of -inf that the row's token, label or list names: infinite losses, and its delta or q term
+    alone as its gradient. Values: one fp32 product or quotient and the output's rounding."""
+    V, tau = 1003, 2.0
+    z = torch.randn((3, V), device="cuda").to(dtype)
+    z[:, 17] = float("-inf")
+    tok = dev(np.full(3, 17), torch.int32)
+    w, c = dev(np.array([1.5, -0.5, 0.3]), F32), dev(np.array([0.7, 0.2, 1.1]), F32)
+    o = P.p24_token_logprobs(z, tok, temperature=tau)
+    assert (o["logp"] == float("-inf")).all()
+    D = P.p24_token_logprobs_bwd(z, tok, o["stats"], w, temperature=tau)
+    rel = 2.0 ** -8 if dtype == BF else 4 * U
+    close(D[:, 17], f64(w) / tau, rel * np.abs(f64(w)), "token")
+    assert torch.isfinite(D).all()
+    idx = dev(np.tile([3, 17], (3, 1)), torch.int32)
+    val = torch.log(dev(np.tile([0.5, 0.3], (3, 1)), F32))
+    q = 0.3 if tail else np.sqrt(0.3) / (np.sqrt(0.5) + np.sqrt(0.3))
+    s = P.p24_distill_topk(z, idx, val, tok, temperature=tau, tail=tail, dkl=w, dce=c)
+    assert (s["kl"] == float("inf")).all() and (s["ce"] == float("inf")).all()
+    back = P.p24_distill_topk_bwd(z, idx, val, s["stats"], w, tok, c, temperature=tau, tail=tail)
+    want = -f64(w) / tau * q - f64(c)
+    for d in (s["dlogits"], back):
+        close(d[:, 17], want, (rel + 16 * U) * (np.abs(f64(w)) + np.abs(f64(c))), "label and list")
+        assert torch.isfinite(d).all()
