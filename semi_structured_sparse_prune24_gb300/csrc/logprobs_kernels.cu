@@ -12,9 +12,11 @@
 //                       maximum reaches it can hold alternatives. Those parts (a thread's share
 //                       of one stage or a few) are read again, from L2, the elements that reach
 //                       the bound are listed, and each one's place is the number of listed ones
-//                       before it. Where the list overflows because many logits tie at the bound
-//                       (masked rows, constant rows) the ones above it are listed and the rest
-//                       taken in order of position; what is left goes through an exact selection.
+//                       before it. Where the list overflows because many logits tie at the bound,
+//                       the ones above it are listed and the rest taken in order of position, if the
+//                       bound shows the tied value: any negative one in bf16; in fp32 -inf, and the
+//                       lowest finite value in shares of up to kItems parts. Other ties go through
+//                       an exact selection, five walks over the share.
 //  logprobs_bwd_kernel  elementwise from the saved statistics.
 //
 // Bound: HBM, one read of the logits (and one write of the gradient). Measured on GB300, of the
@@ -22,7 +24,10 @@
 // the same rows with entropy 133 us, 0.92, of 1000 x 32003 fp32 42 us, 0.91; entropy and top 64 of
 // 8192 x 131072 409 us, 0.79 (the alternatives' searches are a fifth of the instructions, and the
 // walk waits for them; top 20 357 us, 0.90); one row of 32000 with 20 alternatives 7.0 us, of which
-// 2.4 us are the walk and the rest the alternatives' dependent steps.
+// 2.4 us are the walk and the rest the alternatives' dependent steps. The search is a fixed cost a
+// row, which shorter rows hide less: top 64 of 4096 x 50257 131 us, 0.47, top 20 101 us, 0.61, none 65;
+// top 5 of 8192 x 1001 51 us, 0.05, none 16. Exact selections: 16 x 50257 fp32 with 12 live entries
+// 36 us masked by -1e9, 11 by -inf; 1000 x 50257 621 and 48 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -49,7 +54,7 @@ __device__ __forceinline__ uint64_t entry(uint32_t key, int i) {
 __device__ __forceinline__ int entry_pos(uint64_t e) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(e)); }
 __device__ __forceinline__ uint32_t entry_key(uint64_t e) { return static_cast<uint32_t>(e >> 32); }
 
-// With alternatives (19 KB for them). Top 64 of 8192 x 131072: 409 us; 427 with 320 or 256 threads
+// With alternatives (20.5 KB for them). Top 64 of 8192 x 131072: 409 us; 427 with 320 or 256 threads
 // and 3 CTAs on an SM, 472 with 192 and 5, 465 with 256 and 2. Fewer threads have fewer maxima, so
 // more candidates; more threads pay more for each search.
 using Long = Layout<256, 4, 4, 2>;
@@ -612,6 +617,8 @@ cudaError_t launch_logprobs_as(const p24_logprobs_args& g, int* status, cudaStre
     using M = std::conditional_t<kTop, Short, ShortPlain>;
     return launch_rows(logprobs_kernel<T, kEntropy, kTop, M>, M::kThreads, g.T, 1, smem(M(), 1), s, g, status);
   }
+  // Without alternatives, 1000 vectors a CTA: 16 x 32000 2.9 us over 8 CTAs a row, 4.1 whole; 256 x 131072
+  // 11.6 over 2, 13.9 whole, 15.4 over 4; 450 x 32000 6.2 whole, 8.8 over 2.
   const int ranks = kTop ? top_split(g.T, vecs) : row_split(g.T, vecs, sm_count() * L::kCtas, kMaxRanks, 1000);
   if (kTop && g.T * ranks <= sm_count() * Few::kCtas)
     return launch_rows(logprobs_kernel<T, kEntropy, kTop, std::conditional_t<kTop, Few, L>>, Few::kThreads, g.T, ranks,

@@ -776,7 +776,9 @@ int hyb_sddmm(const p24_hybrid* h, const void* G, int64_t N, int64_t ldg, const 
 
 namespace {
 constexpr int64_t kMaxVocab = int64_t(1) << 30;      // positions in a row are 32-bit
-constexpr int64_t kMaxVocabTail = int64_t(1) << 19;  // the listed columns' mask is in shared memory
+// with the bucket, the heads of the chains of listed elements are in shared memory, one for each stage
+// and warp of two rows: 4 KB at this length, and their number grows with it
+constexpr int64_t kMaxVocabTail = int64_t(1) << 19;
 
 // [T, V] logits or their gradient: any row stride, aligned to the element
 int check_logits(const void* p, int32_t dtype, int64_t T, int64_t V, int64_t ld) {
