@@ -532,7 +532,7 @@ int ffn24_step_traced(const p24_ffn_args* a, void* workspace, size_t ws_bytes, v
  * A call's first launch of a kernel looks up how many of its CTAs the device holds; like
  * every first call it belongs before a stream capture.
  */
-typedef enum { P24_BF16 = 0, P24_F32 = 1 } p24_dtype;
+typedef enum { P24_BF16 = 0, P24_F32 = 1, P24_E4M3 = 2 } p24_dtype; /* P24_E4M3: only where a call says so */
 
 #define P24_TOPK_MAX 128 /* longest list of alternatives or of teacher entries per row */
 
@@ -637,6 +637,159 @@ typedef struct {
 
 int p24_distill_topk(const p24_distill_args* a, void* stream);
 int p24_distill_topk_bwd(const p24_distill_args* a, void* stream);
+
+/*
+ * What a pre-norm block and a training step have around the sparse FFN: the norm in front of
+ * it with the residual's addition, the embedding, and the norm over all gradients. Matrices are
+ * bf16 or fp32 as their dtype says, with any row stride that is at least the row and any
+ * alignment that is a multiple of the element; rows whose pieces of 8 columns lie on 16-byte
+ * boundaries (in a call: of all its tensors alike) move 16 bytes at a time, others in elements. Sums and statistics
+ * are fp32 or wider and are added in a fixed order: repeated calls are bit-identical. Inputs and
+ * outputs overlap only where a call says so.
+ *
+ * p24_rmsnorm -- root-mean-square norm of each row, after the residual's addition:
+ *   h = x + r, rounded to r's type, where there is a residual (else h is x)
+ *   rstd = 1 / sqrt(mean h^2 + eps),   y = h rstd w
+ *   x    : [T, d], x_dtype.   r, h : [T, d], r_dtype; both or neither. h may be r itself (the
+ *          stream is updated in place), or x where they have one type.
+ *   w    : [d], w_dtype, or NULL (all ones).
+ *   y    : [T, d], y_dtype; it may be x or r itself, where h is elsewhere and they have one type.
+ *          With P24_E4M3 codes of 8 bits (4 of exponent, 3 of fraction, largest 448), with
+ *   scale: fp32 [T, ceil(d / group)], row stride lds: the group's largest magnitude / 448 (1 for a group of
+ *          zeros, and no less than 2^-118); y = code * scale. Codes are rounded once, to nearest even.
+ *          group is 32, 64, 128 or 256 columns, or 0 for whole rows.
+ *   rstd : fp32 [T], or NULL. The backward reads it.
+ * A row with a NaN is NaN; of a row with an infinity the infinity gives NaN and the rest 0. Squares
+ * that fp32 does not hold are summed at another scale.
+ * 1 <= d <= P24_NORM_MAX_COLS (P24_EUNSUPPORTED beyond), 1e-12 <= eps <= 1e4.
+ *
+ * p24_rmsnorm_bwd -- from the norm's h and rstd and the gradient dy of y:
+ *   dx = dres + rstd (g - xh mean(g xh)),   g = dy w,  xh = h rstd;     dw = sum over rows of dy xh
+ *   dres : [T, d], r_dtype, or NULL: the gradient that reaches h directly (through the skip
+ *          connection). dx is then the gradient of x and of r alike.
+ *   dx   : [T, d], dx_dtype; it may be dy, dres or h itself where they have one type.
+ *   dw   : fp32 [d], or NULL (then ws may be too). With T = 0 it is zero.
+ *   ws   : device scratch of p24_rmsnorm_bwd_workspace_size(T, d) bytes, 16-byte aligned.
+ *
+ * p24_dequant8 -- y = code * scale, for readers that take no 8-bit operands (bf16 or fp32 y).
+ */
+#define P24_NORM_MAX_COLS 32768
+
+typedef struct {
+  int64_t T, d;
+  int32_t x_dtype, r_dtype, w_dtype, y_dtype;
+  float eps;
+  int32_t group;
+  const void* x;
+  int64_t ldx;
+  const void* r;
+  int64_t ldr;
+  const void* w;
+  void* h;
+  int64_t ldh;
+  void* y;
+  int64_t ldy;
+  float* scale;
+  int64_t lds;
+  float* rstd;
+} p24_rmsnorm_args;
+
+typedef struct {
+  int64_t T, d;
+  int32_t h_dtype, dy_dtype, r_dtype, dx_dtype, w_dtype, reserved; /* reserved: 0 */
+  const void* h;
+  int64_t ldh;
+  const void* dy;
+  int64_t lddy;
+  const void* dres;
+  int64_t ldres;
+  const void* w;
+  const float* rstd;
+  void* dx;
+  int64_t lddx;
+  float* dw;
+} p24_rmsnorm_bwd_args;
+
+typedef struct {
+  int64_t T, d;
+  int32_t y_dtype, group;
+  const void* q;
+  int64_t ldq;
+  const float* scale;
+  int64_t lds;
+  void* y;
+  int64_t ldy;
+} p24_dequant8_args;
+
+int p24_rmsnorm(const p24_rmsnorm_args* a, void* stream);
+size_t p24_rmsnorm_bwd_workspace_size(int64_t T, int64_t d);
+int p24_rmsnorm_bwd(const p24_rmsnorm_bwd_args* a, void* ws, size_t ws_bytes, void* stream);
+int p24_dequant8(const p24_dequant8_args* a, void* stream);
+
+/*
+ * p24_embed -- Y[t] = scale W[tokens[t]]: tokens int32 [T], W [V, d], Y [T, d]. A token outside
+ * 0..V-1 (padding) gives a row of zeros.
+ *
+ * p24_embed_bwd -- the table's gradient: dW[v] = scale * sum of dY[t] over tokens[t] = v, for every v in
+ * 0..V-1 (zeros where there is none), or with accumulate added to what dW holds, whose other rows are
+ * not touched (a head that shares the table has put its own gradient there). The sum is fp32, in the
+ * order of the positions within blocks of them, and rounded once. Padding counts nothing.
+ *   ws : device scratch of p24_embed_bwd_workspace_size(T, d) bytes, 16-byte aligned.
+ *
+ * V < 2^30, d <= P24_EMBED_MAX_COLS (P24_EUNSUPPORTED beyond); scale is finite.
+ */
+#define P24_EMBED_MAX_COLS 1048576
+
+typedef struct {
+  int64_t T, V, d;
+  int32_t w_dtype, y_dtype;
+  float scale;
+  const int32_t* tokens;
+  const void* W;
+  int64_t ldw;
+  void* Y;
+  int64_t ldy;
+} p24_embed_args;
+
+typedef struct {
+  int64_t T, V, d;
+  int32_t dy_dtype, dw_dtype;
+  float scale;
+  int32_t accumulate;
+  const int32_t* tokens;
+  const void* dY;
+  int64_t lddy;
+  void* dW;
+  int64_t lddw;
+} p24_embed_bwd_args;
+
+int p24_embed(const p24_embed_args* a, void* stream);
+size_t p24_embed_bwd_workspace_size(int64_t T, int64_t d);
+int p24_embed_bwd(const p24_embed_bwd_args* a, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * p24_grad_norm -- the norm over n tensors (contiguous, bf16 or fp32, any sizes, aligned to their
+ * element; an empty one counts nothing): norm[0] = sqrt(sum of g^2), fp32. Sums are fp64 over
+ * threads' fp32 sums of a few dozen elements, so that neither their number nor their size costs digits.
+ *
+ * p24_clip_grads -- the same, and g * min(1, max_norm / norm) goes to `out` (n tensors of the same
+ * sizes and types; each is the input itself or does not overlap any input), or with out = NULL to the
+ * gradients themselves. Where the norm is not finite the gradients stay as they are (out: a copy);
+ * the norm says so. norm may be NULL. max_norm > 0 and finite.
+ *
+ * The list `g` is a host array and is read before the call returns. ws: device scratch of
+ * p24_grad_norm_workspace_size(n) bytes, 16-byte aligned.
+ */
+typedef struct {
+  void* p;
+  int64_t n;     /* elements */
+  int64_t dtype; /* p24_dtype */
+} p24_tensor;
+
+size_t p24_grad_norm_workspace_size(int64_t n);
+int p24_grad_norm(const p24_tensor* g, int64_t n, float* norm, void* ws, size_t ws_bytes, void* stream);
+int p24_clip_grads(const p24_tensor* g, const p24_tensor* out, int64_t n, float max_norm, float* norm, void* ws,
+                   size_t ws_bytes, void* stream);
 
 /* Number of kernels this library has launched in this process (all devices). */
 uint64_t p24_launch_count(void);

@@ -8,6 +8,7 @@ if the shared library is missing, importing this module raises.
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes as C
 import os
@@ -25,7 +26,7 @@ P24_STEP_ACT24 = 0x1
 P24_STEP_KEEP_MASKS = 0x2
 P24_STEP_ADAPTERS = 0x4
 P24_STEP_VNM = 0x8
-P24_BF16, P24_F32 = 0, 1
+P24_BF16, P24_F32, P24_E4M3 = 0, 1, 2
 P24_TOPK_MAX = 128
 P24_DISTILL_TAIL = 0x1
 
@@ -76,6 +77,43 @@ class p24_distill_args(C.Structure):
                 ("dlogits", C.c_void_p), ("ldd", C.c_int64)]
 
 
+class p24_rmsnorm_args(C.Structure):
+    _fields_ = [("T", C.c_int64), ("d", C.c_int64), ("x_dtype", C.c_int32), ("r_dtype", C.c_int32),
+                ("w_dtype", C.c_int32), ("y_dtype", C.c_int32), ("eps", C.c_float), ("group", C.c_int32),
+                ("x", C.c_void_p), ("ldx", C.c_int64), ("r", C.c_void_p), ("ldr", C.c_int64), ("w", C.c_void_p),
+                ("h", C.c_void_p), ("ldh", C.c_int64), ("y", C.c_void_p), ("ldy", C.c_int64), ("scale", C.c_void_p),
+                ("lds", C.c_int64), ("rstd", C.c_void_p)]
+
+
+class p24_rmsnorm_bwd_args(C.Structure):
+    _fields_ = [("T", C.c_int64), ("d", C.c_int64), ("h_dtype", C.c_int32), ("dy_dtype", C.c_int32),
+                ("r_dtype", C.c_int32), ("dx_dtype", C.c_int32), ("w_dtype", C.c_int32), ("reserved", C.c_int32),
+                ("h", C.c_void_p), ("ldh", C.c_int64), ("dy", C.c_void_p), ("lddy", C.c_int64), ("dres", C.c_void_p),
+                ("ldres", C.c_int64), ("w", C.c_void_p), ("rstd", C.c_void_p), ("dx", C.c_void_p), ("lddx", C.c_int64),
+                ("dw", C.c_void_p)]
+
+
+class p24_dequant8_args(C.Structure):
+    _fields_ = [("T", C.c_int64), ("d", C.c_int64), ("y_dtype", C.c_int32), ("group", C.c_int32), ("q", C.c_void_p),
+                ("ldq", C.c_int64), ("scale", C.c_void_p), ("lds", C.c_int64), ("y", C.c_void_p), ("ldy", C.c_int64)]
+
+
+class p24_embed_args(C.Structure):
+    _fields_ = [("T", C.c_int64), ("V", C.c_int64), ("d", C.c_int64), ("w_dtype", C.c_int32), ("y_dtype", C.c_int32),
+                ("scale", C.c_float), ("tokens", C.c_void_p), ("W", C.c_void_p), ("ldw", C.c_int64), ("Y", C.c_void_p),
+                ("ldy", C.c_int64)]
+
+
+class p24_embed_bwd_args(C.Structure):
+    _fields_ = [("T", C.c_int64), ("V", C.c_int64), ("d", C.c_int64), ("dy_dtype", C.c_int32), ("dw_dtype", C.c_int32),
+                ("scale", C.c_float), ("accumulate", C.c_int32), ("tokens", C.c_void_p), ("dY", C.c_void_p),
+                ("lddy", C.c_int64), ("dW", C.c_void_p), ("lddw", C.c_int64)]
+
+
+class p24_tensor(C.Structure):
+    _fields_ = [("p", C.c_void_p), ("n", C.c_int64), ("dtype", C.c_int64)]
+
+
 def _load() -> C.CDLL:
     if not os.path.exists(_LIB_PATH):
         raise ImportError(f"libprune24 is not built ({_LIB_PATH} missing): run __graft_entry__.build() "
@@ -115,6 +153,16 @@ def _load() -> C.CDLL:
         "p24_token_logprobs_bwd": (i32, [C.POINTER(p24_logprobs_args), vp]),
         "p24_distill_topk": (i32, [C.POINTER(p24_distill_args), vp]),
         "p24_distill_topk_bwd": (i32, [C.POINTER(p24_distill_args), vp]),
+        "p24_rmsnorm": (i32, [C.POINTER(p24_rmsnorm_args), vp]),
+        "p24_rmsnorm_bwd_workspace_size": (sz, [i64, i64]),
+        "p24_rmsnorm_bwd": (i32, [C.POINTER(p24_rmsnorm_bwd_args), vp, sz, vp]),
+        "p24_dequant8": (i32, [C.POINTER(p24_dequant8_args), vp]),
+        "p24_embed": (i32, [C.POINTER(p24_embed_args), vp]),
+        "p24_embed_bwd_workspace_size": (sz, [i64, i64]),
+        "p24_embed_bwd": (i32, [C.POINTER(p24_embed_bwd_args), vp, sz, vp]),
+        "p24_grad_norm_workspace_size": (sz, [i64]),
+        "p24_grad_norm": (i32, [vp, i64, vp, vp, sz, vp]),
+        "p24_clip_grads": (i32, [vp, vp, i64, C.c_float, vp, vp, sz, vp]),
         "p24_launch_count": (C.c_uint64, []),
         "p24_query_status": (i32, [vp]),
         "p24_query_timeout": (i32, [vp, C.POINTER(i64), C.POINTER(i64)]),
@@ -776,3 +824,255 @@ def p24_distill_topk_bwd(logits: torch.Tensor, top_idx: torch.Tensor, top_val: t
                       lambda T: (None, None, _per_row(stats, (T, 4), torch.float32, "stats", logits.device)))
     _check(lib.p24_distill_topk_bwd(C.byref(a), _stream(stream)), "p24_distill_topk_bwd")
     return dlogits
+
+
+# ------------------------------------------------------------------ around the sparse FFN: norm, embedding, gradient norm
+_NORM_TYPES = {**_LOGIT_TYPES, torch.float8_e4m3fn: P24_E4M3}
+
+
+def _here(device) -> None:
+    """A call launches on the current device: its tensors have to be there."""
+    if device.type == "cuda" and device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _rows(t: torch.Tensor, name: str, shape: tuple | None = None, device=None, types: dict = _LOGIT_TYPES) -> tuple[int, int, int]:
+    """(pointer, row stride, dtype code) of a [T, d] matrix with any row stride."""
+    code = types.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be {' or '.join(str(k) for k in types)}, got {t.dtype}")
+    strides = t.stride()
+    if len(strides) != 2 or not t.is_cuda or (strides[1] != 1 and t.shape[1] > 1):
+        _mat(t, t.dtype, name)  # says what is wrong
+        raise ValueError(f"{name} must be contiguous along its last dimension")
+    if shape is not None and (t.shape != shape or t.device != device):
+        raise ValueError(f"{name} must be a {shape} tensor on {device}")
+    d = t.shape[1]
+    return t.data_ptr(), strides[0] if t.shape[0] > 1 else max(d, strides[0]), code
+
+
+def _vector(t: torch.Tensor | None, d: int, name: str, device) -> tuple[int | None, int]:
+    if t is None:
+        return None, P24_F32
+    code = _LOGIT_TYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    if t.shape != (d,) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {(d,)} tensor on {device}")
+    return t.data_ptr(), code
+
+
+def _scratch(given: torch.Tensor | None, need: int, device) -> tuple[torch.Tensor, int, int]:
+    """A call's scratch: the caller's, or one that is the current stream's memory when it is dropped."""
+    if given is None:
+        given = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    elif given.device != device or not given.is_contiguous():
+        raise ValueError(f"the workspace must be a contiguous tensor on {device}")
+    return given, given.data_ptr(), given.numel() * given.element_size()
+
+
+def p24_rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                eps: float = 1e-6, group: int | None = None, out: dict | None = None, stream=None) -> dict:
+    """Root-mean-square norm of the rows of x + residual: a dict of y [T, d], rstd [T] for the backward and, with a
+    residual, h = x + residual in the residual's type. x, residual: bf16 or fp32 [T, d]; weight: bf16 or fp32 [d].
+    y has x's type, or that of out["y"]. group (32, 64, 128 or 256 columns, or 0 for whole rows): y is 8 bits
+    (torch.float8_e4m3fn) and scale [T, groups] is in the result; y * scale are the values. out: tensors to write
+    to, under those names (h may be the residual itself). See include/prune24.h."""
+    if stream is not None:
+        with _on(stream):
+            return p24_rmsnorm(x, weight, residual, eps, group, out)
+    px, ldx, tx = _rows(x, "x")
+    shape, dev = x.shape, x.device
+    _here(dev)
+    T, d = shape
+    o, given = {}, {} if out is None else out
+    y = given.get("y")
+    if y is None:
+        y = torch.empty(shape, dtype=x.dtype if group is None else torch.float8_e4m3fn, device=dev)
+    py, ldy, ty = _rows(y, "y", shape, dev, _NORM_TYPES)
+    if (group is None) != (ty != P24_E4M3):
+        raise TypeError(f"y is 8 bits with a group and is not without one: group={group}, y {y.dtype}")
+    o["y"] = y
+    pr = ph = ps = None
+    ldr = ldh = lds = 0
+    tr = tx
+    if residual is not None:
+        pr, ldr, tr = _rows(residual, "residual", shape, dev)
+        h = given.get("h")
+        if h is None:
+            h = torch.empty(shape, dtype=residual.dtype, device=dev)
+        ph, ldh, th = _rows(h, "h", shape, dev)
+        if th != tr:
+            raise TypeError("h must have the residual's type")
+        o["h"] = h
+    if group is not None:
+        groups = -(-d // group) if group > 0 else 1
+        scale = given.get("scale")
+        if scale is None:
+            scale = torch.empty((T, groups), dtype=torch.float32, device=dev)
+        ps, lds, ts = _rows(scale, "scale", (T, groups), dev)
+        if ts != P24_F32:
+            raise TypeError("scale must be torch.float32")
+        o["scale"] = scale
+    pw, tw = _vector(weight, d, "weight", dev)
+    a = p24_rmsnorm_args(T, d, tx, tr, tw, ty, eps, group or 0, px, ldx, pr, ldr, pw, ph, ldh, py, ldy, ps, lds,
+                         _out(o, given, "rstd", (T,), torch.float32, dev))
+    _check(lib.p24_rmsnorm(C.byref(a), _stream(None)), "p24_rmsnorm")
+    return o
+
+
+def p24_rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor | None, rstd: torch.Tensor,
+                    dres: torch.Tensor | None = None, dweight: bool | None = None, out: dict | None = None,
+                    workspace: torch.Tensor | None = None, stream=None) -> dict:
+    """The gradient of p24_rmsnorm for the gradient dy of y, from its h (x where there was no residual) and rstd: a dict
+    of dx [T, d] (of x and the residual alike) and dweight (fp32 [d]; unless dweight=False, or without a weight). dres:
+    the gradient that reaches h directly; it is added. dx has h's type, or that of out["dx"], which may be dres, dy or
+    h itself."""
+    if stream is not None:
+        with _on(stream):
+            return p24_rmsnorm_bwd(dy, h, weight, rstd, dres, dweight, out, workspace)
+    ph, ldh, th = _rows(h, "h")
+    shape, dev = h.shape, h.device
+    _here(dev)
+    T, d = shape
+    pd, ldd, td = _rows(dy, "dy", shape, dev)
+    o, given = {}, {} if out is None else out
+    dx = given.get("dx")
+    if dx is None:
+        dx = torch.empty(shape, dtype=h.dtype, device=dev)
+    px, ldx, tx = _rows(dx, "dx", shape, dev)
+    o["dx"] = dx
+    pr, ldr, tr = (None, 0, tx) if dres is None else _rows(dres, "dres", shape, dev)
+    pw, tw = _vector(weight, d, "weight", dev)
+    pg = None
+    if dweight or (dweight is None and weight is not None):
+        pg = _out(o, given, "dweight", (d,), torch.float32, dev)
+    a = p24_rmsnorm_bwd_args(T, d, th, td, tr, tx, tw, 0, ph, ldh, pd, ldd, pr, ldr, pw,
+                             _per_row(rstd, (T,), torch.float32, "rstd", dev), px, ldx, pg)
+    ws, n = None, 0
+    if pg is not None:
+        workspace, ws, n = _scratch(workspace, lib.p24_rmsnorm_bwd_workspace_size(T, d), dev)
+    _check(lib.p24_rmsnorm_bwd(C.byref(a), ws, n, _stream(None)), "p24_rmsnorm_bwd")
+    return o
+
+
+def p24_dequant8(q: torch.Tensor, scale: torch.Tensor, group: int = 0, out: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """The values of p24_rmsnorm's 8-bit y and its scale: q * scale, bf16 (or out's type) [T, d]."""
+    if stream is not None:
+        with _on(stream):
+            return p24_dequant8(q, scale, group, out)
+    pq, ldq, tq = _rows(q, "q", types=_NORM_TYPES)
+    if tq != P24_E4M3:
+        raise TypeError(f"q must be torch.float8_e4m3fn, got {q.dtype}")
+    (T, d), dev = q.shape, q.device
+    _here(dev)
+    out = torch.empty((T, d), dtype=torch.bfloat16, device=dev) if out is None else out
+    py, ldy, ty = _rows(out, "out", q.shape, dev)
+    ps, lds, ts = _rows(scale, "scale", (T, -(-d // group) if group > 0 else 1), dev)
+    if ts != P24_F32:
+        raise TypeError("scale must be torch.float32")
+    a = p24_dequant8_args(T, d, ty, group, pq, ldq, ps, lds, py, ldy)
+    _check(lib.p24_dequant8(C.byref(a), _stream(None)), "p24_dequant8")
+    return out
+
+
+def p24_embed(tokens: torch.Tensor, W: torch.Tensor, scale: float = 1.0, out: torch.Tensor | None = None,
+              stream=None) -> torch.Tensor:
+    """Rows of the embedding table W [V, d] (bf16 or fp32), times scale: [T, d] of W's type, or out's. tokens: int32 [T];
+    one outside 0..V-1 gives zeros."""
+    if stream is not None:
+        with _on(stream):
+            return p24_embed(tokens, W, scale, out)
+    pw, ldw, tw = _rows(W, "W")
+    (V, d), dev = W.shape, W.device
+    _here(dev)
+    if tokens.dim() != 1:
+        raise ValueError("tokens must be 1-D")
+    T = tokens.shape[0]
+    pt = _per_row(tokens, (T,), torch.int32, "tokens", dev)
+    out = torch.empty((T, d), dtype=W.dtype, device=dev) if out is None else out
+    py, ldy, ty = _rows(out, "out", (T, d), dev)
+    a = p24_embed_args(T, V, d, tw, ty, scale, pt, pw, ldw, py, ldy)
+    _check(lib.p24_embed(C.byref(a), _stream(None)), "p24_embed")
+    return out
+
+
+def p24_embed_bwd(dY: torch.Tensor, tokens: torch.Tensor, V: int, scale: float = 1.0, dW: torch.Tensor | None = None,
+                  accumulate: bool = False, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The gradient of p24_embed's table: dW [V, d] (dY's type, or that of the tensor given), zero where no token is.
+    accumulate: added to dW, whose other rows are not touched (a head that shares the table)."""
+    if stream is not None:
+        with _on(stream):
+            return p24_embed_bwd(dY, tokens, V, scale, dW, accumulate, workspace)
+    py, ldy, ty = _rows(dY, "dY")
+    (T, d), dev = dY.shape, dY.device
+    _here(dev)
+    pt = _per_row(tokens, (T,), torch.int32, "tokens", dev)
+    if dW is None:
+        if accumulate:
+            raise ValueError("accumulate needs the dW to add to")
+        dW = torch.empty((V, d), dtype=dY.dtype, device=dev)
+    pw, ldw, tw = _rows(dW, "dW", (V, d), dev)
+    workspace, ws, n = _scratch(workspace, lib.p24_embed_bwd_workspace_size(T, d), dev)
+    a = p24_embed_bwd_args(T, V, d, ty, tw, scale, 1 if accumulate else 0, pt, py, ldy, pw, ldw)
+    _check(lib.p24_embed_bwd(C.byref(a), ws, n, _stream(None)), "p24_embed_bwd")
+    return dW
+
+
+def _tensor_list(ts, device, name: str) -> array.array:
+    """A list of tensors as p24_tensor[]."""
+    v = []
+    types = _LOGIT_TYPES
+    for t in ts:
+        code = types.get(t.dtype)
+        if code is None:
+            raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+        if t.device != device or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous tensors on {device}")
+        v += (t.data_ptr(), t.numel(), code)
+    return array.array("q", v)
+
+
+def _list_call(grads, norm, workspace):
+    if not grads:
+        raise ValueError("an empty list has no device to run on")
+    dev = grads[0].device
+    if dev.type != "cuda":
+        raise ValueError("the gradients must be CUDA tensors (libprune24 has no CPU path)")
+    _here(dev)
+    g = _tensor_list(grads, dev, "gradients")
+    if norm is None:
+        norm = torch.empty(1, dtype=torch.float32, device=dev)
+    elif norm.shape != (1,):
+        raise ValueError("norm must have one element")
+    pn = _per_row(norm, (1,), torch.float32, "norm", dev)
+    return g, norm, pn, _scratch(workspace, lib.p24_grad_norm_workspace_size(len(grads)), dev)
+
+
+def p24_grad_norm(grads, norm: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The norm over all elements of a list of gradients (bf16 and fp32 tensors of any shapes): fp32 [1]."""
+    if stream is not None:
+        with _on(stream):
+            return p24_grad_norm(grads, norm, workspace)
+    g, norm, pn, (workspace, ws, n) = _list_call(grads, norm, workspace)
+    _check(lib.p24_grad_norm(g.buffer_info()[0], len(grads), pn, ws, n, _stream(None)), "p24_grad_norm")
+    return norm
+
+
+def p24_clip_grads(grads, max_norm: float, out=None, norm: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Scales a list of gradients to a norm of at most max_norm, in place or into the tensors of `out` (same sizes and
+    types), and returns the norm they had (fp32 [1]). Where it is not finite they stay as they are."""
+    if stream is not None:
+        with _on(stream):
+            return p24_clip_grads(grads, max_norm, out, norm, workspace)
+    g, norm, pn, (workspace, ws, n) = _list_call(grads, norm, workspace)
+    to = None
+    if out is not None:
+        if len(out) != len(grads):
+            raise ValueError(f"{len(grads)} gradients, and {len(out)} tensors to write to")
+        o = _tensor_list(out, grads[0].device, "out")
+        to = o.buffer_info()[0]
+    _check(lib.p24_clip_grads(g.buffer_info()[0], to, len(grads), max_norm, pn, ws, n, _stream(None)), "p24_clip_grads")
+    return norm

@@ -867,6 +867,173 @@ int p24_distill_topk_bwd(const p24_distill_args* a, void* stream) {
   return cuda_status(launch_distill_bwd(*a, st, as_stream(stream)));
 }
 
+namespace {
+// [T, d], any row stride, aligned to the element; null with no rows
+int check_rows(const void* p, int32_t dtype, int64_t T, int64_t d, int64_t ld, bool codes = false) {
+  if (dtype != P24_BF16 && dtype != P24_F32 && !(codes && dtype == P24_E4M3)) return P24_EINVAL;
+  if (T == 0) return P24_OK;
+  if (!p || ld < d || ld > kMaxDim) return P24_EINVAL;
+  const unsigned size = dtype == P24_BF16 ? 2 : dtype == P24_F32 ? 4 : 1;
+  return reinterpret_cast<uintptr_t>(p) & (size - 1) ? P24_EALIGN : P24_OK;
+}
+int check_sizes(int64_t T, int64_t d, int64_t most) {
+  if (T < 0 || T > kMaxDim || d < 1) return P24_EINVAL;
+  return d > most ? P24_EUNSUPPORTED : P24_OK;
+}
+// [d], or null
+int check_weight(const void* w, int32_t dtype) {
+  if (!w) return P24_OK;
+  if (dtype != P24_BF16 && dtype != P24_F32) return P24_EINVAL;
+  return reinterpret_cast<uintptr_t>(w) & (dtype == P24_BF16 ? 1u : 3u) ? P24_EALIGN : P24_OK;
+}
+int check_ws(const void* ws, size_t bytes, size_t need) {
+  if (!ws) return P24_EINVAL;
+  if (!aligned16(ws)) return P24_EALIGN;
+  return bytes < need ? P24_ENOSPACE : P24_OK;
+}
+bool good_group(int32_t g) { return g == 0 || g == 32 || g == 64 || g == 128 || g == 256; }
+// An output that is an input's own memory has its type and stride.
+bool same_or_apart(const void* out, int64_t ldo, int32_t dto, const void* in, int64_t ldi, int32_t dti) {
+  return out != in || (ldo == ldi && dto == dti);
+}
+}  // namespace
+
+int p24_rmsnorm(const p24_rmsnorm_args* a, void* stream) {
+  if (!a) return P24_EINVAL;
+  P24_TRY(check_sizes(a->T, a->d, P24_NORM_MAX_COLS));
+  if (!(a->eps >= 1e-12f && a->eps <= 1e4f)) return P24_EINVAL;
+  P24_TRY(check_rows(a->x, a->x_dtype, a->T, a->d, a->ldx));
+  P24_TRY(check_rows(a->y, a->y_dtype, a->T, a->d, a->ldy, true));
+  P24_TRY(check_weight(a->w, a->w_dtype));
+  if (!a->r != !a->h) return P24_EINVAL;
+  if (a->r) {
+    P24_TRY(check_rows(a->r, a->r_dtype, a->T, a->d, a->ldr));
+    P24_TRY(check_rows(a->h, a->r_dtype, a->T, a->d, a->ldh));
+    if (a->h == a->y && a->T > 0) return P24_EINVAL;
+    if (!same_or_apart(a->h, a->ldh, a->r_dtype, a->r, a->ldr, a->r_dtype) ||
+        !same_or_apart(a->h, a->ldh, a->r_dtype, a->x, a->ldx, a->x_dtype) ||
+        !same_or_apart(a->y, a->ldy, a->y_dtype, a->r, a->ldr, a->r_dtype))
+      return P24_EINVAL;
+  }
+  if (a->T > 0 && !same_or_apart(a->y, a->ldy, a->y_dtype, a->x, a->ldx, a->x_dtype)) return P24_EINVAL;
+  if (a->y_dtype == P24_E4M3) {
+    if (!good_group(a->group)) return P24_EINVAL;
+    const int64_t groups = a->group ? (a->d + a->group - 1) / a->group : 1;
+    if (a->T > 0 && (!a->scale || a->lds < groups)) return P24_EINVAL;
+  }
+  if (a->T == 0) return P24_OK;
+  if (!all_aligned4({a->scale, a->rstd})) return P24_EALIGN;
+  return cuda_status(launch_rmsnorm(*a, as_stream(stream)));
+}
+
+size_t p24_rmsnorm_bwd_workspace_size(int64_t T, int64_t d) {
+  if (T <= 0 || d < 1 || T > kMaxDim || d > P24_NORM_MAX_COLS) return 0;
+  return round_up(static_cast<size_t>(rmsnorm_bwd_parts(T, d)) * sizeof(float), 16);
+}
+
+int p24_rmsnorm_bwd(const p24_rmsnorm_bwd_args* a, void* ws, size_t ws_bytes, void* stream) {
+  if (!a || a->reserved != 0) return P24_EINVAL;
+  P24_TRY(check_sizes(a->T, a->d, P24_NORM_MAX_COLS));
+  P24_TRY(check_rows(a->h, a->h_dtype, a->T, a->d, a->ldh));
+  P24_TRY(check_rows(a->dy, a->dy_dtype, a->T, a->d, a->lddy));
+  P24_TRY(check_rows(a->dx, a->dx_dtype, a->T, a->d, a->lddx));
+  if (a->dres) P24_TRY(check_rows(a->dres, a->r_dtype, a->T, a->d, a->ldres));
+  P24_TRY(check_weight(a->w, a->w_dtype));
+  if (!all_aligned4({a->rstd, a->dw})) return P24_EALIGN;
+  if (a->T == 0)
+    return a->dw ? cuda_status(cudaMemsetAsync(a->dw, 0, static_cast<size_t>(a->d) * sizeof(float), as_stream(stream))) : P24_OK;
+  if (!a->rstd) return P24_EINVAL;
+  if (!same_or_apart(a->dx, a->lddx, a->dx_dtype, a->h, a->ldh, a->h_dtype) ||
+      !same_or_apart(a->dx, a->lddx, a->dx_dtype, a->dy, a->lddy, a->dy_dtype) ||
+      !same_or_apart(a->dx, a->lddx, a->dx_dtype, a->dres, a->ldres, a->r_dtype))
+    return P24_EINVAL;
+  if (a->dw) P24_TRY(check_ws(ws, ws_bytes, p24_rmsnorm_bwd_workspace_size(a->T, a->d)));
+  return cuda_status(launch_rmsnorm_bwd(*a, static_cast<float*>(ws), as_stream(stream)));
+}
+
+int p24_dequant8(const p24_dequant8_args* a, void* stream) {
+  if (!a) return P24_EINVAL;
+  P24_TRY(check_sizes(a->T, a->d, P24_NORM_MAX_COLS));
+  P24_TRY(check_rows(a->q, P24_E4M3, a->T, a->d, a->ldq, true));
+  P24_TRY(check_rows(a->y, a->y_dtype, a->T, a->d, a->ldy));
+  if (!good_group(a->group)) return P24_EINVAL;
+  if (a->T == 0) return P24_OK;
+  if (!a->scale || a->lds < (a->group ? (a->d + a->group - 1) / a->group : 1)) return P24_EINVAL;
+  if (!all_aligned4({a->scale})) return P24_EALIGN;
+  return cuda_status(launch_dequant8(*a, as_stream(stream)));
+}
+
+namespace {
+int check_embed(int64_t T, int64_t V, int64_t d, float scale, const int32_t* tokens) {
+  P24_TRY(check_sizes(T, d, P24_EMBED_MAX_COLS));
+  if (V < 1 || !(scale - scale == 0.f)) return P24_EINVAL;
+  if (V >= kMaxVocab) return P24_EUNSUPPORTED;
+  if (T > 0 && !tokens) return P24_EINVAL;
+  return all_aligned4({tokens}) ? P24_OK : P24_EALIGN;
+}
+}  // namespace
+
+int p24_embed(const p24_embed_args* a, void* stream) {
+  if (!a) return P24_EINVAL;
+  P24_TRY(check_embed(a->T, a->V, a->d, a->scale, a->tokens));
+  P24_TRY(check_rows(a->W, a->w_dtype, a->T, a->d, a->ldw));
+  P24_TRY(check_rows(a->Y, a->y_dtype, a->T, a->d, a->ldy));
+  if (a->T == 0) return P24_OK;
+  if (a->Y == a->W) return P24_EINVAL;
+  return cuda_status(launch_embed(*a, as_stream(stream)));
+}
+
+size_t p24_embed_bwd_workspace_size(int64_t T, int64_t d) {
+  if (T <= 0 || d < 1 || T > kMaxDim || d > P24_EMBED_MAX_COLS) return 0;
+  return embed_bwd_workspace(T, d);
+}
+
+int p24_embed_bwd(const p24_embed_bwd_args* a, void* ws, size_t ws_bytes, void* stream) {
+  if (!a || (a->accumulate != 0 && a->accumulate != 1)) return P24_EINVAL;
+  P24_TRY(check_embed(a->T, a->V, a->d, a->scale, a->tokens));
+  P24_TRY(check_rows(a->dY, a->dy_dtype, a->T, a->d, a->lddy));
+  P24_TRY(check_rows(a->dW, a->dw_dtype, 1, a->d, a->lddw));
+  if (a->dY == a->dW) return P24_EINVAL;
+  if (a->T == 0 && a->accumulate) return P24_OK;
+  if (a->T > 0) P24_TRY(check_ws(ws, ws_bytes, p24_embed_bwd_workspace_size(a->T, a->d)));
+  return cuda_status(launch_embed_bwd(*a, ws, as_stream(stream)));
+}
+
+namespace {
+int check_list(const p24_tensor* g, const p24_tensor* out, int64_t n) {
+  constexpr int64_t kMostElements = int64_t(1) << 42;  // chunks of them are counted in 32 bits
+  if (n < 0 || n > kMaxDim || (n > 0 && !g)) return P24_EINVAL;
+  int64_t all = 0;
+  for (int64_t i = 0; i < n; ++i) {
+    if (g[i].n < 0 || (g[i].dtype != P24_BF16 && g[i].dtype != P24_F32) || (g[i].n > 0 && !g[i].p)) return P24_EINVAL;
+    const unsigned odd = g[i].dtype == P24_BF16 ? 1 : 3;
+    if (out && (out[i].n != g[i].n || out[i].dtype != g[i].dtype || (g[i].n > 0 && !out[i].p))) return P24_EINVAL;
+    if ((reinterpret_cast<uintptr_t>(g[i].p) | (out ? reinterpret_cast<uintptr_t>(out[i].p) : 0)) & odd) return P24_EALIGN;
+    if (g[i].n > kMostElements || (all += g[i].n) > kMostElements) return P24_EUNSUPPORTED;
+  }
+  return P24_OK;
+}
+}  // namespace
+
+size_t p24_grad_norm_workspace_size(int64_t n) { return n < 0 || n > kMaxDim ? 0 : round_up(grad_norm_workspace(n), 16); }
+
+int p24_grad_norm(const p24_tensor* g, int64_t n, float* norm, void* ws, size_t ws_bytes, void* stream) {
+  P24_TRY(check_list(g, nullptr, n));
+  if (!norm) return P24_EINVAL;
+  if (!all_aligned4({norm})) return P24_EALIGN;
+  P24_TRY(check_ws(ws, ws_bytes, p24_grad_norm_workspace_size(n)));
+  return cuda_status(launch_grad_norm(g, nullptr, n, false, 0.f, norm, ws, as_stream(stream)));
+}
+
+int p24_clip_grads(const p24_tensor* g, const p24_tensor* out, int64_t n, float max_norm, float* norm, void* ws, size_t ws_bytes,
+                   void* stream) {
+  P24_TRY(check_list(g, out, n));
+  if (!(max_norm > 0.f && max_norm - max_norm == 0.f)) return P24_EINVAL;
+  if (!all_aligned4({norm})) return P24_EALIGN;
+  P24_TRY(check_ws(ws, ws_bytes, p24_grad_norm_workspace_size(n)));
+  return cuda_status(launch_grad_norm(g, out, n, true, max_norm, norm, ws, as_stream(stream)));
+}
+
 int p24_selftest_timeout(int64_t limit_ns, void* stream) {
   if (limit_ns <= 0 || limit_ns > 10000000000LL) return P24_EINVAL;
   int* st = device_status_ptr();

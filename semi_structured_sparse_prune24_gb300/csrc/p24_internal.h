@@ -108,6 +108,20 @@ cudaError_t launch_logprobs_bwd(const p24_logprobs_args& g, int* status, cudaStr
 cudaError_t launch_distill(const p24_distill_args& g, int* status, cudaStream_t s);  // loss; with dlogits also the gradient
 cudaError_t launch_distill_bwd(const p24_distill_args& g, int* status, cudaStream_t s);
 
+// ---- rows of hidden states, embedding, gradient norm (norm_kernels.cu, embed_kernels.cu, gradnorm_kernels.cu);
+// arguments checked by the caller, T > 0 (embed_bwd: T >= 0)
+cudaError_t launch_rmsnorm(const p24_rmsnorm_args& g, cudaStream_t s);
+int64_t rmsnorm_bwd_parts(int64_t T, int64_t d);  // floats of scratch for the weight's gradient
+cudaError_t launch_rmsnorm_bwd(const p24_rmsnorm_bwd_args& g, float* parts, cudaStream_t s);
+cudaError_t launch_dequant8(const p24_dequant8_args& g, cudaStream_t s);
+cudaError_t launch_embed(const p24_embed_args& g, cudaStream_t s);
+size_t embed_bwd_workspace(int64_t T, int64_t d);
+cudaError_t launch_embed_bwd(const p24_embed_bwd_args& g, void* ws, cudaStream_t s);
+size_t grad_norm_workspace(int64_t n);
+// out: where the scaled gradients go, or null (in place); scale: whether they are
+cudaError_t launch_grad_norm(const p24_tensor* g, const p24_tensor* out, int64_t n, bool scale, float max_norm, float* norm,
+                             void* ws, cudaStream_t s);
+
 // A 2-D tensor map over a row-major matrix, for the HBM-bound kernels' TMA staging:
 // `inner` columns of `outer` rows, boxes of box_inner x box_outer; swizzle128 lays each
 // 128-byte box row out with the 128B swizzle (box_inner x element size must be 128).

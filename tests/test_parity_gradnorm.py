@@ -1,0 +1,164 @@
+"""GPU parity of p24_grad_norm and p24_clip_grads against the fp64 oracle (oracle/block_oracle.py).
+
+Tolerances, u = 2^-24: a thread adds the squares of at most 128 elements in fp32 (130u relative on a sum of positive
+terms), the rest is fp64; on the norm half of it, and its rounding: 70u. A scaled gradient: 70u, the quotient,
+the product, and the output's rounding: (73u + half a step) |g|."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import block_oracle as BO
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+BF, F32 = torch.bfloat16, torch.float32
+TINY = {BF: 2.0 ** -134, F32: 2.0 ** -150}
+
+
+@pytest.fixture(scope="module")
+def P():
+    import semi_structured_sparse_prune24_gb300 as P
+    yield P
+    assert P.p24_query_status() == 0
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def check(P, grads, max_norm, out=None):
+    before = [f64(t) for t in grads]
+    n, want = BO.clip(before, max_norm)
+    norm = P.p24_grad_norm(grads)
+    got = P.p24_clip_grads(grads, max_norm, out=out)
+    assert torch.equal(norm, got)
+    assert abs(float(got) - n) <= 70 * U * n
+    for k, (t, w) in enumerate(zip(grads if out is None else out, want)):
+        if n <= max_norm * (1 - 100 * U):
+            assert np.array_equal(f64(t), before[k])
+        e = torch.finfo(t.dtype).eps / 2
+        assert (np.abs(f64(t) - w) <= (73 * U + e) * np.abs(w) + TINY[t.dtype]).all(), k
+        if out is not None and t.data_ptr() != grads[k].data_ptr():
+            assert np.array_equal(f64(grads[k]), before[k])
+
+
+SETS = {
+    "one element": [(1, F32, 0)],
+    "a vector": [(768, F32, 0)],
+    "odd sizes and starts": [(1, BF, 1), (7, BF, 3), (8, BF, 0), (0, F32, 0), (1001, BF, 5), (4099, F32, 1), (17, F32, 3), (30000, BF, 7)],
+    "chunk ends": [(16384, BF, 0), (16385, BF, 0), (8192, F32, 0), (8191, F32, 0), (16391, BF, 1), (8195, F32, 1), (3 * 16384 + 2, BF, 2)],
+    "17 tensors": [(100 + k, BF if k % 3 else F32, k % 4) for k in range(17)],
+    "129 tensors": [(1 + 31 * k, BF if k % 2 else F32, 0) for k in range(129)],
+    "2000 tensors": [(1 + k % 50, BF if k % 5 else F32, k % 2) for k in range(2000)],
+    "a matrix": [(3000 * 1001, BF, 0), (0, BF, 0), (1001, F32, 0)],
+}
+
+
+def make(spec, seed, sigma=1e-2):
+    rng = np.random.default_rng(seed)
+    ts = []
+    for n, dt, off in spec:
+        full = torch.full((n + off + 8,), float("nan"), dtype=dt, device="cuda")
+        full[off:off + n] = torch.as_tensor(rng.normal(size=n) * sigma, device="cuda").to(dt)
+        ts.append(full[off:off + n])
+    return ts
+
+
+@pytest.mark.parametrize("name", SETS)
+@pytest.mark.parametrize("max_norm", [1e-3, 1e6])
+def test_clip_in_place(P, name, max_norm):
+    check(P, make(SETS[name], 1), max_norm)
+
+
+@pytest.mark.parametrize("name", SETS)
+@pytest.mark.parametrize("max_norm", [1e-3, 1e6])
+def test_clip_into_other_tensors(P, name, max_norm):
+    out = make([(n, dt, (off + 1) % 4) for n, dt, off in SETS[name]], 2)
+    grads = make(SETS[name], 1)
+    check(P, grads, max_norm, out)
+    mixed = [g if k % 2 else o for k, (g, o) in enumerate(zip(grads, out))]
+    check(P, grads, max_norm, mixed)
+
+
+@pytest.mark.parametrize("sigma", [1e-30, 1e-20, 1e15, 1e25, 1e36])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_sizes_whose_squares_leave_fp32(P, sigma, dt):
+    check(P, make([(20000, dt, 1), (5, dt, 0)], 3, sigma), sigma)
+
+
+def test_small_beside_large(P):
+    a, b = make([(20000, F32, 0)], 4, 1e-25) + make([(3, F32, 1)], 5, 1e-24)
+    check(P, [a, b], 1e-26)
+    a[7] = 1e20
+    check(P, [a, b], 1e20)
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("at", [0, 5, 9999])
+def test_a_norm_that_is_not_finite_scales_nothing(P, bad, at):
+    grads = make([(10000, BF, 1), (33, F32, 0)], 6)
+    grads[0][at] = bad
+    before = [t.clone() for t in grads]
+    out = [torch.zeros_like(t) for t in grads]
+    n = P.p24_clip_grads(grads, 1e-3, out=out)
+    assert not np.isfinite(float(n)) and np.isnan(float(n)) == np.isnan(bad)
+    P.p24_clip_grads(grads, 1e-3)
+    for t, o, b in zip(grads, out, before):
+        assert torch.equal(t.nan_to_num(7), b.nan_to_num(7)) and torch.equal(o.nan_to_num(7), b.nan_to_num(7))
+
+
+def test_zeros_and_empty_tensors(P):
+    z = torch.zeros(5000, device="cuda")
+    assert float(P.p24_clip_grads([z, torch.empty(0, device="cuda")], 1.0)) == 0 and bool((z == 0).all())
+    assert float(P.p24_grad_norm([torch.empty(0, dtype=BF, device="cuda")])) == 0
+    assert float(P.p24_clip_grads([torch.empty((0, 4), device="cuda")], 1.0)) == 0
+
+
+def test_shapes_do_not_matter(P):
+    g = torch.randn((30, 41), device="cuda")
+    assert torch.equal(P.p24_grad_norm([g]), P.p24_grad_norm([g.view(-1)]))
+    with pytest.raises(ValueError):
+        P.p24_grad_norm([g.t()])
+
+
+def test_a_model(P):
+    """Tens of millions of elements in full, against torch in fp64, twice the same."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    grads = [torch.empty(n, device="cuda", dtype=dt).normal_(0, 1e-3, generator=g)
+             for n, dt in ((30_000_001, BF), (12345, F32), (17_000_000, F32), (1, BF))]
+    n = float(torch.stack([t.double().square().sum() for t in grads]).sum().sqrt())
+    out = [torch.empty_like(t) for t in grads]
+    norm = P.p24_clip_grads(grads, 1.0, out=out)
+    assert abs(float(norm) - n) <= 70 * U * n and torch.equal(norm, P.p24_grad_norm(grads))
+    for t, o in zip(grads, out):
+        w = t.double() / n
+        e = torch.finfo(t.dtype).eps / 2
+        assert bool(((o.double() - w).abs() <= (73 * U + e) * w.abs() + TINY[t.dtype]).all())
+    again = [torch.empty_like(t) for t in grads]
+    P.p24_clip_grads(grads, 1.0, out=again)
+    assert all(torch.equal(a, b) for a, b in zip(out, again))
+
+
+def test_scratch_norm_and_another_stream(P):
+    grads = make(SETS["17 tensors"], 7)
+    want = P.p24_grad_norm(grads)
+    ws = torch.full((int(P.lib.p24_grad_norm_workspace_size(17)),), 255, dtype=torch.uint8, device="cuda")
+    n = torch.empty(1, device="cuda")
+    assert P.p24_grad_norm(grads, norm=n, workspace=ws) is n and torch.equal(n, want)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = P.p24_clip_grads(grads, 1e-3, stream=s)
+    s.synchronize()
+    assert torch.equal(got, want)
+
+
+def test_refusals_of_the_binding(P):
+    g = [torch.ones(5, device="cuda")]
+    for call, err in ((lambda: P.p24_grad_norm([]), ValueError), (lambda: P.p24_grad_norm([g[0].double()]), TypeError),
+                      (lambda: P.p24_clip_grads(g, 0.0), P.P24Error), (lambda: P.p24_clip_grads(g, float("inf")), P.P24Error),
+                      (lambda: P.p24_clip_grads(g, 1.0, out=[]), ValueError),
+                      (lambda: P.p24_clip_grads(g, 1.0, out=[torch.ones(4, device="cuda")]), P.P24Error),
+                      (lambda: P.p24_grad_norm(g, norm=torch.ones(2, device="cuda")), ValueError),
+                      (lambda: P.p24_grad_norm(g, workspace=torch.empty(8, dtype=torch.uint8, device="cuda")), P.P24Error)):
+        with pytest.raises(err):
+            call()
