@@ -6,6 +6,16 @@
 //
 // Everything between loads and stores is fp32, the sums in a fixed order; each output is rounded once.
 // The bound is memory: a row is read and written once.
+//
+// A unit (a CTA, or a warp for rows of up to 512 columns) takes rows unit, unit + units, ... A row is its interior,
+// from a boundary of 8 elements to another, and at most 7 edge columns before and after it. The interior is cut into
+// pieces of E columns, thread i has pieces i, i + NT, ...; edge columns are single threads'. E is 8 where all
+// matrices are bf16, else 4: then 16 bytes of fp32 and 8 of bf16 are neighbouring threads' neighbours (with pieces of
+// 8 columns a warp's access to fp32 touched each sector twice: norm of 16384 x 8192 fp32 428 us against 322).
+// The interiors of the rows ahead come by bulk copies into a ring of S rows in the unit's shared memory, and go on
+// arriving through a row's reduction and its stores. Copies by each thread into slots of its own (cp.async) took
+// 65 more of 260 instructions a warp and piece, and in rows that start 16 bytes off a sector 1.6 times the L2
+// reads: the gradient of 16384 x 8191 252 us against 200.
 #include <algorithm>
 
 #include "stream_rows.cuh"
@@ -13,444 +23,933 @@
 namespace p24 {
 namespace {
 
-constexpr int kWarpPieces = 128;  // rows of up to so many pieces: a warp each
-
-// What the row's lead tensor says about phases: row t's is (first + t step) mod 8.
+// What the rows' lead tensor says about phases: row t starts (first + t step) mod 8 elements past a boundary. Units
+// are as many as a multiple of 8 (or no fewer than rows), so that all rows of a unit have one phase.
 struct Phase {
   int first, step;
   __device__ __forceinline__ int of(int64_t t) const { return static_cast<int>((first + t * step) & 7); }
 };
 
-// The weights of columns [c, c + 8); 1 without weights.
-__device__ __forceinline__ void weights8(const void* w, int32_t dtype, int c, int d, bool vec, float (&v)[8]) {
-  if (!w) {
+// A matrix that rows come from or go to, bf16 or fp32 (f32: 0 or 1).
+struct Matrix {
+  uint8_t* p;
+  int64_t ld;  // bytes
+  int f32;
+  __device__ __forceinline__ Matrix() {}
+  __device__ __forceinline__ Matrix(const void* q, int64_t elements, int32_t dtype)
+      : p(static_cast<uint8_t*>(const_cast<void*>(q))), ld(elements << (1 + (dtype == P24_F32))), f32(dtype == P24_F32) {}
+  __device__ __forceinline__ uint8_t* row(int64_t t) const { return p + t * ld; }
+};
+
+// E columns of a row as fp32 pairs.
+template <int E>
+struct Vals {
+  Two p[E / 2];
+};
+template <int E>
+__device__ __forceinline__ void to_array(const Vals<E>& a, float (&v)[E]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 1.f;
-  } else if (dtype == P24_BF16) {
-    unpack8(load8(static_cast<const bf16*>(w), c, d, vec), v);
+  for (int k = 0; k < E / 2; ++k) apart(a.p[k], v[2 * k], v[2 * k + 1]);
+}
+template <int E>
+__device__ __forceinline__ Vals<E> filled(float x) {
+  Vals<E> a;
+#pragma unroll
+  for (int k = 0; k < E / 2; ++k) a.p[k] = both(x);
+  return a;
+}
+template <int E>
+__device__ __forceinline__ float sum_of(const Two& t) {
+  float a, b;
+  apart(t, a, b);
+  return a + b;
+}
+__device__ __forceinline__ Two pair_of(uint32_t w) { return two(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+__device__ __forceinline__ float rounded_bf16(float x) { return to_float(static_cast<bf16>(x)); }
+
+// A piece: of 8 bf16 (16 bytes), of 4 bf16 (8 bytes), of 4 fp32 (16 bytes).
+__device__ __forceinline__ Vals<8> vals_of(const uint4& q) {
+  Vals<8> a;
+  a.p[0] = pair_of(q.x), a.p[1] = pair_of(q.y), a.p[2] = pair_of(q.z), a.p[3] = pair_of(q.w);
+  return a;
+}
+__device__ __forceinline__ Vals<4> vals_of(const uint2& q) {
+  Vals<4> a;
+  a.p[0] = pair_of(q.x), a.p[1] = pair_of(q.y);
+  return a;
+}
+__device__ __forceinline__ Vals<4> vals_of_f32(const uint4& q) {
+  Vals<4> a;
+  a.p[0] = two(__uint_as_float(q.x), __uint_as_float(q.y)), a.p[1] = two(__uint_as_float(q.z), __uint_as_float(q.w));
+  return a;
+}
+__device__ __forceinline__ float element(const uint8_t* row, int f32, int c) {
+  return f32 ? reinterpret_cast<const float*>(row)[c] : to_float(reinterpret_cast<const bf16*>(row)[c]);
+}
+__device__ __forceinline__ void put_element(uint8_t* row, int f32, int c, float x) {
+  if (f32) reinterpret_cast<float*>(row)[c] = x;
+  else reinterpret_cast<bf16*>(row)[c] = static_cast<bf16>(x);
+}
+// Columns [c, c + E) of a row; `vec`: in one access.
+template <int E>
+__device__ __forceinline__ Vals<E> load_vals(const uint8_t* row, int f32, int c, bool vec) {
+  if (vec) {
+    if constexpr (E == 8) {
+      if (!f32) return vals_of(*reinterpret_cast<const uint4*>(row + 2 * c));
+      const Vals<4> a = vals_of_f32(*reinterpret_cast<const uint4*>(row + 4 * c)), b = vals_of_f32(*reinterpret_cast<const uint4*>(row + 4 * c + 16));
+      return Vals<8>{{a.p[0], a.p[1], b.p[0], b.p[1]}};
+    } else if (f32) return vals_of_f32(*reinterpret_cast<const uint4*>(row + 4 * c));
+    else return vals_of(*reinterpret_cast<const uint2*>(row + 2 * c));
+  }
+  Vals<E> a;
+#pragma unroll
+  for (int k = 0; k < E / 2; ++k) a.p[k] = two(element(row, f32, c + 2 * k), element(row, f32, c + 2 * k + 1));
+  return a;
+}
+template <int E>
+__device__ __forceinline__ void store_vals(uint8_t* row, int f32, int c, bool vec, const Vals<E>& a) {
+  float v[E];
+  to_array(a, v);
+  if (vec) {
+    if constexpr (E == 8) {
+      *reinterpret_cast<uint4*>(row + 2 * c) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    } else if (f32) {
+      *reinterpret_cast<float4*>(row + 4 * c) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+      *reinterpret_cast<uint2*>(row + 2 * c) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    }
   } else {
-    unpack8(load8(static_cast<const float*>(w), c, d, vec), v);
+#pragma unroll
+    for (int k = 0; k < E; ++k) put_element(row, f32, c + k, v[k]);
   }
 }
 
-__device__ __forceinline__ uint2 e4m3x8(const float (&v)[8]) {
-  uint32_t h[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    h[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-  return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+__device__ __forceinline__ void bulk_copy(uint32_t to, const void* from, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to), "l"(from),
+               "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
-__device__ __forceinline__ void store_e4m3(uint8_t* row, int c, int d, bool vec, const float (&v)[8]) {
-  const uint2 q = e4m3x8(v);
-  if (vec && c >= 0 && c + 8 <= d) {
-    *reinterpret_cast<uint2*>(row + c) = q;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i >= 0 && c + i < d) row[c + i] = static_cast<uint8_t>((i < 4 ? q.x >> (8 * i) : q.y >> (8 * (i - 4))) & 255u);
-  }
+__device__ __forceinline__ void copy4(uint32_t to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+// One of the arrivals that `bar` counts, once this thread's copy4s so far are there.
+__device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ uint32_t shared4(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 shared16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 shared8(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
 }
 
+// How a row is split over a unit's threads, the same for all rows of the unit.
+template <int E, bool kAligned>
+struct Split {
+  int NT, tid, d, c0, n, edges, edge;  // c0: the interior's first column; n pieces; this thread's edge column, if any
+  __device__ __forceinline__ void start(int phase) {
+    c0 = kAligned ? 0 : min(-phase & 7, d);
+    n = (d - c0) / 8 * (8 / E);
+    edges = kAligned ? 0 : d - n * E;
+    edge = tid < c0 ? tid : n * E + tid;
+  }
+  __device__ __forceinline__ bool has(int i) const { return i * NT + tid < n; }
+  __device__ __forceinline__ int column(int i) const { return c0 + E * (i * NT + tid); }
+  __device__ __forceinline__ bool has_edge() const { return !kAligned && tid < edges; }
+  // Whether the pieces of a matrix lie on boundaries of their own size.
+  __device__ __forceinline__ bool fits(const Matrix& m, int64_t t) const {
+    return kAligned || (reinterpret_cast<uintptr_t>(m.row(t) + (c0 << (m.f32 + 1))) & (E * 2 * (m.f32 + 1) - 1)) == 0;
+  }
+};
+
+constexpr int kMostRows = 4;  // of a ring
+
+constexpr int kMostEdges = 16;  // 14 are
+
+// What comes beside the interiors of a ring's rows.
+template <int M>
+struct Beside {
+  uint64_t full[kMostRows];  // a row has arrived
+  uint32_t edge[kMostRows][M][kMostEdges];
+  float rstd[kMostRows];
+  int abort;
+};
+
+// A unit's rows of M matrices: through a ring of S rows (kRing), or read where they are used. Edge columns, and the
+// row's rstd where it is an input, come by copies of 4 bytes, as far ahead as the interiors: loads into registers
+// one row ahead were waited for in every row (the gradient of 16384 x 8192 166 us against 158). The word of a bf16
+// column has a neighbour in it; where that lies outside the matrix the column is loaded by itself.
+template <int M, int NV, int E, bool kAligned, bool kRing>
+struct Pieces {
+  Split<E, kAligned> sp;
+  Matrix in[M];
+  int m, row_bytes, S;  // matrices; of a row in the ring; rows of it
+  uint32_t base;        // the ring
+  int64_t T;
+  Beside<M>* sh;
+  const float* rstd;    // or null
+  int* status;
+  int high;             // a bf16 edge column is the upper half of its word
+  bool vec[M];
+  int stage, parity;    // the row in use
+
+  __device__ __forceinline__ int f32(int a) const { return E == 8 ? 0 : in[a].f32; }
+  __device__ __forceinline__ int at(int a) const {  // matrix a's offset in a row of the ring
+    int k = 0;
+#pragma unroll
+    for (int i = 0; i < M; ++i)
+      if (i < a && i < m) k += sp.NT * NV * E * 2 << f32(i);
+    return k;
+  }
+  // All threads of the unit; the caller's barrier comes after it and before the first fill.
+  __device__ __forceinline__ void start(int64_t t, int phase, const void* smem) {
+    sp.start(phase);
+    row_bytes = at(M);
+    base = smem_u32(smem);
+    stage = parity = 0;
+    if (!kRing) {
+#pragma unroll
+      for (int a = 0; a < M; ++a) vec[a] = a < m && sp.fits(in[a], t);
+    } else if (sp.tid == 0) {
+      sh->abort = 0;
+      for (int k = 0; k < S; ++k) mbar_init(&sh->full[k], 1 + feeders());
+      fence_barrier_init();
+      fence_proxy_async_smem();
+    }
+    high = (phase + sp.edge) & 1;
+  }
+  __device__ __forceinline__ int feeders() const { return max(sp.edges, 1); }
+  // Threads below feeders(): row t, if there is one, into `to`, which no thread reads any more.
+  __device__ __forceinline__ void fill(int64_t t, int to) const {
+    if (t >= T || sp.tid >= feeders()) return;
+    if (sp.tid == 0) {
+      uint32_t bytes = 0;
+#pragma unroll
+      for (int a = 0; a < M; ++a)
+        if (a < m) bytes += sp.n * E * 2 << f32(a);
+      mbar_arrive_expect_tx(&sh->full[to], bytes);
+      if (sp.n > 0) {
+#pragma unroll
+        for (int a = 0; a < M; ++a)
+          if (a < m) bulk_copy(base + to * row_bytes + at(a), in[a].row(t) + (sp.c0 << (f32(a) + 1)), sp.n * E * 2 << f32(a), &sh->full[to]);
+      }
+      if (rstd) copy4(smem_u32(&sh->rstd[to]), rstd + t);
+    }
+    if (sp.has_edge()) {
+#pragma unroll
+      for (int a = 0; a < M; ++a) {
+        if (a >= m) continue;
+        const uint8_t* row = in[a].row(t);
+        const bool alone = high ? sp.edge == 0 && t == 0 : sp.edge == sp.d - 1 && t == T - 1;
+        uint32_t* slot = &sh->edge[to][a][sp.tid];
+        if (f32(a)) copy4(smem_u32(slot), row + 4 * sp.edge);
+        else if (!alone) copy4(smem_u32(slot), row + 2 * (sp.edge - high));
+        else *slot = reinterpret_cast<const uint16_t*>(row)[sp.edge] << (16 * high);
+      }
+    }
+    arrive_after_copies(&sh->full[to]);
+  }
+  __device__ __forceinline__ void wait() const { p24_wait(&sh->full[stage], parity, &sh->abort, status); }
+  __device__ __forceinline__ void advance() {
+    if (++stage == S) stage = 0, parity ^= 1;
+  }
+  // After an expired wait: the last of the unit's rows may still be on their way here.
+  __device__ __forceinline__ void drain(int64_t rows) const {
+    if (*reinterpret_cast<volatile int*>(&sh->abort) == 0) return;
+    for (int64_t i = rows > S ? rows - S : 0; i < rows; ++i) p24_wait_quiet(&sh->full[i % S], (i / S) & 1);
+  }
+  __device__ __forceinline__ Vals<E> get(int a, int i, int64_t t) const {
+    if (!kRing) return load_vals<E>(in[a].row(t), f32(a), sp.column(i), vec[a]);
+    const uint32_t from = base + stage * row_bytes + at(a) + ((i * sp.NT + sp.tid) * E * 2 << f32(a));
+    if constexpr (E == 8) return vals_of(shared16(from));
+    else if (f32(a)) return vals_of_f32(shared16(from));
+    else return vals_of(shared8(from));
+  }
+  // This thread's edge column of the row in use.
+  __device__ __forceinline__ float edge(int a, int64_t t) const {
+    if (!kRing) return element(in[a].row(t), f32(a), sp.edge);
+    const uint32_t w = shared4(smem_u32(&sh->edge[stage][a][sp.tid]));
+    return __uint_as_float(f32(a) || high ? (f32(a) ? w : w & 0xffff0000u) : w << 16);
+  }
+};
+
+// The weights of a thread's columns: in registers, or in shared memory where it has 16 columns, or read each time.
+template <int NV, int E>
+struct Weights {
+  static constexpr int kHow = NV * E <= 8 ? 0 : NV * E <= 16 ? 1 : 2;
+  const uint8_t* w;
+  int f32;
+  bool vec;
+  uint32_t sh;
+  Vals<E> r[kHow == 0 ? NV : 1];
+  float edge;
+
+  template <typename S>
+  __device__ __forceinline__ Vals<E> read(const S& sp, int i) const {
+    return w ? load_vals<E>(w, f32, sp.column(i), vec) : filled<E>(1.f);
+  }
+  // smem: the unit's place for them (16 bytes of each thread side by side)
+  template <typename S>
+  __device__ __forceinline__ void start(const S& sp, const void* weight, int32_t dtype, const void* smem) {
+    w = static_cast<const uint8_t*>(weight), f32 = dtype == P24_F32;
+    vec = w && (reinterpret_cast<uintptr_t>(w + (sp.c0 << (f32 + 1))) & (E == 4 && !f32 ? 7 : 15)) == 0;
+    sh = smem_u32(smem) + 16 * sp.tid;
+    edge = sp.has_edge() && w ? element(w, f32, sp.edge) : 1.f;
+    if (kHow == 2) return;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (!sp.has(i)) continue;
+      const Vals<E> v = read(sp, i);
+      if (kHow == 0) {
+        r[i] = v;
+      } else {
+        float x[E];
+        to_array(v, x);
+#pragma unroll
+        for (int k = 0; k < E; k += 4)
+          asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(sh + (i * E + k) / 4 * 16 * sp.NT), "f"(x[k]), "f"(x[k + 1]),
+                       "f"(x[k + 2]), "f"(x[k + 3])
+                       : "memory");
+      }
+    }
+  }
+  template <typename S>
+  __device__ __forceinline__ Vals<E> get(const S& sp, int i) const {
+    if (kHow == 0) return r[i];
+    if (kHow == 2) return read(sp, i);
+    Vals<E> v;
+#pragma unroll
+    for (int k = 0; k < E; k += 4) {
+      const Vals<4> q = vals_of_f32(shared16(sh + (i * E + k) / 4 * 16 * sp.NT));
+      v.p[k / 2] = q.p[0], v.p[k / 2 + 1] = q.p[1];
+    }
+    return v;
+  }
+};
+
+// Column c of a row of sums in shared memory, one word in nine left out: the lanes of a warp, 8 columns apart,
+// meet no conflicts.
+__device__ __forceinline__ int padded(int c) { return c + (c >> 3); }
+
+// Codes of 8 bits.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3) |
+         static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3)) << 16;
+}
+// Of values times a factor, one for the first `cut` columns and another for the rest.
+template <int E>
+__device__ __forceinline__ void store_e4m3(uint8_t* row, int c, bool vec, const Vals<E>& a, float fa, float fb, int cut) {
+  float v[E];
+  to_array(a, v);
+  uint32_t q[E / 4];
+#pragma unroll
+  for (int k = 0; k < E; ++k) v[k] *= k < cut ? fa : fb;
+#pragma unroll
+  for (int k = 0; k < E / 4; ++k) q[k] = e4m3x4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+  if (vec) {
+    if constexpr (E == 8) *reinterpret_cast<uint2*>(row + c) = make_uint2(q[0], q[1]);
+    else *reinterpret_cast<uint32_t*>(row + c) = q[0];
+  } else {
+#pragma unroll
+    for (int k = 0; k < E; ++k) row[c + k] = static_cast<uint8_t>(q[k / 4] >> (8 * (k & 3)));
+  }
+}
 // A scale and what values are multiplied by, from the largest magnitude. The reciprocal is that of the
 // stored scale, so that code times scale is the nearest to the value that the code allows; below 2^-118
 // a scale's reciprocal leaves fp32's range, and the scale stays there.
 __device__ __forceinline__ float scale_of(float top) { return top == 0.f ? 1.f : max_nan(top * (1.f / 448.f), 0x1p-118f); }
+template <int E>
+__device__ __forceinline__ float top_of(const Vals<E>& a) {
+  float v[E], top = 0.f;
+  to_array(a, v);
+#pragma unroll
+  for (int k = 0; k < E; ++k) top = max_nan(top, fabsf(v[k]));
+  return top;
+}
 
-// kWarp: a warp takes a row, else the CTA. NV: pieces of a thread.
-template <typename Tx, typename Tr, bool kWarp, bool kAligned, int NV>
-__global__ void __launch_bounds__(kWarp ? 256 : 1024) rmsnorm_kernel(const p24_rmsnorm_args g, const Phase phase) {
-  __shared__ float part[4][32];
-  extern __shared__ float group_top[];  // 8 bits, phases: the groups' largest magnitudes
-  const int d = static_cast<int>(g.d), lane = threadIdx.x & 31;
-  const int tid = kWarp ? lane : threadIdx.x, NT = kWarp ? 32 : blockDim.x;
-  const int per = kWarp ? blockDim.x >> 5 : 1;
-  int64_t t = static_cast<int64_t>(blockIdx.x) * per + (kWarp ? threadIdx.x >> 5 : 0);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * per;
-  const bool quant = g.y_dtype == P24_E4M3;
-  const int groups = quant ? (d + g.group - 1) / g.group : 0;
-  float* tops = group_top + (kWarp ? (threadIdx.x >> 5) * groups : 0);
-  auto add = [&](float x, int k) { return kWarp ? warp_add(x) : cta_add(x, part[k]); };
-  auto join = [&] {
-    if (kWarp) __syncwarp(); else __syncthreads();
-  };
+// How a launch is laid out: S rows of a unit's ring; bytes of a unit's ring, and of what it has behind it.
+struct Plan {
+  Phase phase;
+  int S, ring_bytes, unit_bytes;
+};
+
+// Sum or maximum over a unit; `k`: which of the reductions of a row, `odd`: the row's parity.
+template <bool kWarp>
+struct Reduce {
+  float (*part)[3][32];
+  __device__ __forceinline__ float add(float x, int odd, int k) const { return kWarp ? warp_add(x) : cta_add(x, part[odd][k]); }
+  __device__ __forceinline__ float max(float x, int odd, int k) const { return kWarp ? lanes_max(x) : cta_max(x, part[odd][k]); }
+  __device__ __forceinline__ void sync() const {
+    if (kWarp) __syncwarp();
+    else __syncthreads();
+  }
+};
+
+template <bool kWarp, bool kAligned, bool kRing, int E, int C>
+__global__ void __launch_bounds__(kWarp ? 256 : 1024, kWarp ? (C > 8 ? 3 : 4) : 1) rmsnorm_kernel(const p24_rmsnorm_args g, const Plan plan, int* status) {
+  __shared__ float part[2][3][32];
+  __shared__ Beside<2> beside[kWarp ? 8 : 1];
+  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int NV = C / E;
+  const int lane = threadIdx.x & 31;
+  const int per = kWarp ? blockDim.x >> 5 : 1, unit = kWarp ? threadIdx.x >> 5 : 0;
+  const int64_t begin = static_cast<int64_t>(blockIdx.x) * per + unit, step = static_cast<int64_t>(gridDim.x) * per;
+  const bool quant = g.y_dtype == P24_E4M3, with_r = g.r != nullptr;
+  const Reduce<kWarp> reduce{part};
+  Pieces<2, NV, E, kAligned, kRing> row;
+  const Split<E, kAligned>& sp = row.sp;
+  row.sp.NT = kWarp ? 32 : blockDim.x, row.sp.tid = kWarp ? lane : threadIdx.x, row.sp.d = static_cast<int>(g.d);
+  row.in[0] = Matrix(g.x, g.ldx, g.x_dtype);
+  row.in[1] = Matrix(g.r, g.ldr, g.r_dtype);
+  row.m = with_r ? 2 : 1, row.S = plan.S, row.T = g.T, row.sh = &beside[unit], row.rstd = nullptr, row.status = status;
+  // a unit's shared memory: the ring, the weights, its groups' largest magnitudes
+  uint8_t* own = smem + unit * plan.unit_bytes;
+  row.start(begin, kAligned ? 0 : plan.phase.of(begin), own);
+  Weights<NV, E> w;
+  float* tops = reinterpret_cast<float*>(own + plan.ring_bytes + (w.kHow == 1 ? sp.NT * C * 4 : 0));
+  const int groups = quant ? (sp.d + g.group - 1) / g.group : 0;
+  const Matrix h_out(g.h, g.ldh, g.r_dtype), y_out(g.y, g.ldy, g.y_dtype);
+  const bool hv = sp.fits(h_out, begin), yv = sp.fits(y_out, begin);
+  const float inv_d = 1.f / static_cast<float>(sp.d);
+  if (kRing) reduce.sync();  // thread 0 has set the ring up
   pdl_wait();
   pdl_trigger();
-  for (; t < g.T; t += step) {
-    const int s = kAligned ? 0 : phase.of(t);
-    const int n = (d + s + 7) >> 3;
-    const Tx* x = static_cast<const Tx*>(g.x) + t * g.ldx;
-    const Tr* r = static_cast<const Tr*>(g.r) + (g.r ? t * g.ldr : 0);
-    const bool xv = kAligned || pieces_aligned(x, s), rv = kAligned || pieces_aligned(r, s);
-    Raw8<Tx> rx[NV];
-    Raw8<Tr> rr[NV];
+  if (kRing)
+    for (int k = 0; k < plan.S; ++k) row.fill(begin + k * step, k);
+  w.start(sp, g.w, g.w_dtype, own + plan.ring_bytes);
+  int odd = 0;
+  for (int64_t t = begin; t < g.T; t += step, odd ^= 1) {
+    Vals<E> h[NV];
+    Two sums = both(0.f);
+    float e = 0.f;
+    if (kRing) row.wait();
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int j = i * NT + tid;
-      if (j < n) rx[i] = load8(x, 8 * j - s, d, xv);
-    }
-    if (g.r) {
+      h[i] = filled<E>(0.f);
+      if (!sp.has(i)) continue;
+      h[i] = row.get(0, i, t);
+      if (with_r) {
+        const Vals<E> r = row.get(1, i, t);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int j = i * NT + tid;
-        if (j < n) rr[i] = load8(r, 8 * j - s, d, rv);
-      }
-    }
-    float h[NV][8], sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int j = i * NT + tid;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) h[i][k] = 0.f;
-      if (j < n) {
-        unpack8(rx[i], h[i]);
-        if (g.r) {
-          float b[8];
-          unpack8(rr[i], b);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) h[i][k] = to_float(static_cast<Tr>(h[i][k] + b[k]));
-          Tr* to = static_cast<Tr*>(g.h) + t * g.ldh;
-          store8(to, 8 * j - s, d, kAligned || pieces_aligned(to, s), h[i]);
+        for (int k = 0; k < E / 2; ++k) {
+          h[i].p[k] = h[i].p[k] + r.p[k];
+          if (!row.f32(1)) {  // rounded as it is stored
+            float x, y;
+            apart(h[i].p[k], x, y);
+            h[i].p[k] = pair_of(pack_bf16x2(x, y));
+          }
         }
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sum = fmaf(h[i][k], h[i][k], sum);
+      for (int k = 0; k < E / 2; ++k) sums = fma(h[i].p[k], h[i].p[k], sums);
     }
-    sum = add(sum, 0);
-    float rstd = rsqrtf(sum / static_cast<float>(d) + g.eps);
-    if (sum == __int_as_float(0x7f800000)) {  // squares beyond fp32 (or an infinity): at a scale of 2^-80
-      float small = 0.f;
+    if (sp.has_edge()) {
+      e = row.edge(0, t);
+      if (with_r) {
+        e += row.edge(1, t);
+        if (!row.f32(1)) e = rounded_bf16(e);
+        put_element(h_out.row(t), row.f32(1), sp.edge, e);
+      }
+    }
+    if (with_r) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (sp.has(i)) store_vals<E>(h_out.row(t), row.f32(1), sp.column(i), hv, h[i]);
+    }
+    const float total = reduce.add(fmaf(e, e, sum_of<E>(sums)), odd, 0);
+    // every thread has read its pieces: the reduction says so
+    if (kRing) {
+      row.fill(t + plan.S * step, row.stage);
+      row.advance();
+    }
+    float rstd = rsqrtf(total * inv_d + g.eps);
+    if (total == __int_as_float(0x7f800000)) {  // squares beyond fp32 (or an infinity): at a scale of 2^-80
+      sums = both(0.f);
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) small = fmaf(h[i][k] * 0x1p-80f, h[i][k] * 0x1p-80f, small);
-      small = add(small, 1);
-      rstd = 0x1p-80f * rsqrtf(small / static_cast<float>(d));
+        for (int k = 0; k < E / 2; ++k) {
+          const Two small = h[i].p[k] * both(0x1p-80f);
+          sums = fma(small, small, sums);
+        }
+      const float small = e * 0x1p-80f;
+      rstd = 0x1p-80f * rsqrtf(reduce.add(fmaf(small, small, sum_of<E>(sums)), odd, 1) * inv_d);
     }
-    if (g.rstd && tid == 0) g.rstd[t] = rstd;
+    if (g.rstd && sp.tid == 0) g.rstd[t] = rstd;
+    e = e * rstd * w.edge;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int j = i * NT + tid;
-      if (j < n) {
-        float w[8];
-        weights8(g.w, g.w_dtype, 8 * j - s, d, kAligned, w);
+      if (!sp.has(i)) continue;
+      const Vals<E> wi = w.get(sp, i);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) h[i][k] = h[i][k] * rstd * w[k];
-      }
+      for (int k = 0; k < E / 2; ++k) h[i].p[k] = h[i].p[k] * both(rstd) * wi.p[k];
     }
     if (!quant) {
 #pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (sp.has(i)) store_vals<E>(y_out.row(t), E == 8 ? 0 : y_out.f32, sp.column(i), yv, h[i]);
+      if (sp.has_edge()) put_element(y_out.row(t), E == 8 ? 0 : y_out.f32, sp.edge, e);
+      continue;
+    }
+    uint8_t* y = static_cast<uint8_t*>(g.y) + t * g.ldy;
+    const bool qv = kAligned || (reinterpret_cast<uintptr_t>(y + sp.c0) & (E - 1)) == 0;
+    float* scales = g.scale + t * g.lds;
+    if (groups == 1) {
+      float top = fabsf(e);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) top = max_nan(top, top_of(h[i]));
+      const float sc = scale_of(reduce.max(top, odd, 2)), inv = 1.f / sc;
+      if (sp.tid == 0) scales[0] = sc;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (sp.has(i)) store_e4m3<E>(y, sp.column(i), qv, h[i], inv, inv, E);
+      if (sp.has_edge()) y[sp.edge] = static_cast<uint8_t>(e4m3x4(e * inv, 0.f, 0.f, 0.f));
+    } else if (kAligned && g.group <= 32 * E) {
+      // a group is some neighbouring lanes' pieces
+      const int lanes = g.group / E;
+#pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int j = i * NT + tid, c = 8 * j - s;
-        if (j >= n) continue;
-        if (g.y_dtype == P24_BF16) {
-          bf16* y = static_cast<bf16*>(g.y) + t * g.ldy;
-          store8(y, c, d, kAligned || pieces_aligned(y, s), h[i]);
-        } else {
-          float* y = static_cast<float*>(g.y) + t * g.ldy;
-          store8(y, c, d, kAligned || pieces_aligned(y, s), h[i]);
-        }
+        float top = top_of(h[i]);
+        for (int k = lanes >> 1; k; k >>= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, k));
+        const float sc = scale_of(top), inv = 1.f / sc;
+        if (!sp.has(i)) continue;
+        if ((lane & (lanes - 1)) == 0) scales[sp.column(i) / g.group] = sc;
+        store_e4m3<E>(y, sp.column(i), qv, h[i], inv, inv, E);
       }
     } else {
-      uint8_t* y = static_cast<uint8_t*>(g.y) + t * g.ldy;
-      const bool yv = kAligned || (reinterpret_cast<uintptr_t>(y + 8 - s) & 7u) == 0;
-      float* scales = g.scale + t * g.lds;
-      if (groups == 1) {
-        float top = 0.f;
+      // A piece meets at most two groups, from column `cut` of it on the second. Magnitudes are ordered as whole
+      // numbers, NaN last.
+      auto note = [&](int group, float top) { atomicMax(reinterpret_cast<int*>(&tops[group]), __float_as_int(top)); };
+      for (int i = sp.tid; i < groups; i += sp.NT) tops[i] = 0.f;
+      reduce.sync();
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+      for (int i = 0; i < NV; ++i) {
+        if (!sp.has(i)) continue;
+        const int c = sp.column(i), ga = c / g.group, gb = (c + E - 1) / g.group, cut = ga == gb ? E : gb * g.group - c;
+        float v[E], ta = 0.f, tb = 0.f;
+        to_array(h[i], v);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) top = max_nan(top, fabsf(h[i][k]));
-        const float sc = scale_of(kWarp ? lanes_max(top) : cta_max(top, part[2]));
-        if (tid == 0) scales[0] = sc;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int j = i * NT + tid;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) h[i][k] *= 1.f / sc;
-          if (j < n) store_e4m3(y, 8 * j - s, d, yv, h[i]);
-        }
-      } else {
-        // A piece of 8 columns meets at most two groups. Magnitudes are ordered as whole numbers, NaN last.
-        for (int i = tid; i < groups; i += NT) tops[i] = 0.f;
-        join();
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int j = i * NT + tid, c = 8 * j - s;
-          if (j >= n) continue;
-          const int a = max(c, 0) / g.group, b = min(c + 7, d - 1) / g.group;
-          float ta = 0.f, tb = 0.f;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float m = fabsf(h[i][k]);
-            if (c + k < b * g.group || a == b) ta = max_nan(ta, m); else tb = max_nan(tb, m);
-          }
-          atomicMax(reinterpret_cast<int*>(&tops[a]), __float_as_int(ta));
-          if (a != b) atomicMax(reinterpret_cast<int*>(&tops[b]), __float_as_int(tb));
-        }
-        join();
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int j = i * NT + tid, c = 8 * j - s;
-          if (j >= n) continue;
-          const int a = max(c, 0) / g.group, b = min(c + 7, d - 1) / g.group;
-          const float ia = 1.f / scale_of(tops[a]), ib = 1.f / scale_of(tops[b]);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) h[i][k] *= (c + k < b * g.group || a == b) ? ia : ib;
-          store_e4m3(y, c, d, yv, h[i]);
-        }
-        for (int i = tid; i < groups; i += NT) scales[i] = scale_of(tops[i]);
+        for (int k = 0; k < E; ++k)
+          if (k < cut) ta = max_nan(ta, fabsf(v[k]));
+          else tb = max_nan(tb, fabsf(v[k]));
+        note(ga, ta);
+        if (ga != gb) note(gb, tb);
       }
+      if (sp.has_edge()) note(sp.edge / g.group, max_nan(fabsf(e), 0.f));
+      reduce.sync();
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (!sp.has(i)) continue;
+        const int c = sp.column(i), ga = c / g.group, gb = (c + E - 1) / g.group;
+        store_e4m3<E>(y, c, qv, h[i], 1.f / scale_of(tops[ga]), 1.f / scale_of(tops[gb]), ga == gb ? E : gb * g.group - c);
+      }
+      if (sp.has_edge()) y[sp.edge] = static_cast<uint8_t>(e4m3x4(e * (1.f / scale_of(tops[sp.edge / g.group])), 0.f, 0.f, 0.f));
+      for (int i = sp.tid; i < groups; i += sp.NT) scales[i] = scale_of(tops[i]);
+      reduce.sync();  // before the next row's groups
     }
-    join();  // before the next row's reductions write again
   }
+  if (kRing && sp.tid == 0) row.drain(begin < g.T ? (g.T - begin + step - 1) / step : 0);
 }
 
-// The gradient. The weight's is summed over the rows of a CTA in registers where a thread's columns are
-// the same in every row (kAligned), else in shared memory, and goes to the CTA's row of `parts`.
-template <typename Th, typename Td, bool kAligned, int NV>
-__global__ void __launch_bounds__(1024) rmsnorm_bwd_kernel(const p24_rmsnorm_bwd_args g, const Phase phase, float* parts) {
-  __shared__ float part[2][32];
-  extern __shared__ float dw_sh[];
-  const int d = static_cast<int>(g.d), tid = threadIdx.x, NT = blockDim.x;
-  float acc[NV][8];
+// The gradient. The weight's is summed over a unit's rows in registers (a thread's columns are the same in all
+// of them), or where a thread has more than 16 in shared memory, then over a CTA's units, and goes to the CTA's row
+// of `parts`.
+template <bool kWarp, bool kAligned, bool kRing, int E, int C>
+__global__ void __launch_bounds__(kWarp ? 256 : 1024, kWarp ? 3 : 1) rmsnorm_bwd_kernel(const p24_rmsnorm_bwd_args g, const Plan plan, float* parts, int* status) {
+  __shared__ float part[2][3][32];
+  __shared__ Beside<3> beside[kWarp ? 8 : 1];
+  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int NV = C / E;
+  constexpr bool kHold = C <= 8;   // g and xh stay in registers through the reduction
+  constexpr bool kSums = C <= 16;  // and the sums
+  const int per = kWarp ? blockDim.x >> 5 : 1, unit = kWarp ? threadIdx.x >> 5 : 0;
+  const int64_t begin = static_cast<int64_t>(blockIdx.x) * per + unit, step = static_cast<int64_t>(gridDim.x) * per;
+  const bool with_r = g.dres != nullptr;
+  const Reduce<kWarp> reduce{part};
+  Pieces<3, NV, E, kAligned, kRing> row;
+  const Split<E, kAligned>& sp = row.sp;
+  row.sp.NT = kWarp ? 32 : blockDim.x, row.sp.tid = kWarp ? threadIdx.x & 31 : threadIdx.x, row.sp.d = static_cast<int>(g.d);
+  row.in[0] = Matrix(g.h, g.ldh, g.h_dtype);
+  row.in[1] = Matrix(g.dy, g.lddy, g.dy_dtype);
+  row.in[2] = Matrix(g.dres, g.ldres, g.r_dtype);
+  row.m = with_r ? 3 : 2, row.S = plan.S, row.T = g.T, row.sh = &beside[unit], row.rstd = g.rstd, row.status = status;
+  // a unit's shared memory: the ring, the weights; the sums take a warp's ring at its end, or are all there is
+  uint8_t* own = smem + unit * plan.unit_bytes;
+  row.start(begin, kAligned ? 0 : plan.phase.of(begin), own);
+  Weights<NV, E> w;
+  float* sums = reinterpret_cast<float*>(own);
+  const Matrix out(g.dx, g.lddx, g.dx_dtype);
+  const bool ov = sp.fits(out, begin);
+  const float inv_d = 1.f / static_cast<float>(sp.d);
+  Vals<E> acc[kSums ? NV : 1];
+  float acc_e = 0.f;
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int k = 0; k < 8; ++k) acc[i][k] = 0.f;
-  if (!kAligned && parts)
-    for (int c = tid; c < d; c += NT) dw_sh[c] = 0.f;
-  __syncthreads();
+  for (int i = 0; i < (kSums ? NV : 1); ++i) acc[i] = filled<E>(0.f);
+  if (!kSums && parts)
+    for (int c = sp.tid; c < padded(sp.d); c += sp.NT) sums[c] = 0.f;
+  if (kRing || !kSums) reduce.sync();  // thread 0 has set the ring up
   pdl_wait();
   pdl_trigger();
+  if (kRing)
+    for (int k = 0; k < plan.S; ++k) row.fill(begin + k * step, k);
+  w.start(sp, g.w, g.w_dtype, own + plan.ring_bytes);
   int odd = 0;
-  for (int64_t t = blockIdx.x; t < g.T; t += gridDim.x, odd ^= 1) {
-    const int s = kAligned ? 0 : phase.of(t);
-    const int n = (d + s + 7) >> 3;
-    const Th* h = static_cast<const Th*>(g.h) + t * g.ldh;
-    const Td* dy = static_cast<const Td*>(g.dy) + t * g.lddy;
-    const bool hv = kAligned || pieces_aligned(h, s), dv = kAligned || pieces_aligned(dy, s);
-    const float rstd = g.rstd[t];
-    Raw8<Th> rh[NV];
-    Raw8<Td> rd[NV];
+  for (int64_t t = begin; t < g.T; t += step, odd ^= 1) {
+    if (kRing) row.wait();
+    const float now = kRing ? beside[unit].rstd[row.stage] : g.rstd[t];
+    float eh = 0.f, eg = 0.f, er = 0.f;
+    if (sp.has_edge()) {
+      eh = row.edge(0, t) * now;
+      eg = row.edge(1, t);
+      if (with_r) er = row.edge(2, t);
+      acc_e = fmaf(eg, eh, acc_e);
+      eg *= w.edge;
+    }
+    Vals<E> xh[kHold ? NV : 1], v[kHold ? NV : 1];
+    Two dots = both(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int j = i * NT + tid;
-      if (j < n) rh[i] = load8(h, 8 * j - s, d, hv), rd[i] = load8(dy, 8 * j - s, d, dv);
+      const int u = kHold ? i : 0;
+      if (!sp.has(i)) continue;
+      xh[u] = row.get(0, i, t);
+      v[u] = row.get(1, i, t);
+      const Vals<E> wi = w.get(sp, i);
+      Vals<E> p;
+#pragma unroll
+      for (int k = 0; k < E / 2; ++k) {
+        xh[u].p[k] = xh[u].p[k] * both(now);
+        if (kSums) acc[kSums ? i : 0].p[k] = fma(v[u].p[k], xh[u].p[k], acc[kSums ? i : 0].p[k]);
+        else p.p[k] = v[u].p[k] * xh[u].p[k];
+        v[u].p[k] = v[u].p[k] * wi.p[k];
+        dots = fma(v[u].p[k], xh[u].p[k], dots);
+      }
+      if (!kSums && parts) {
+        float q[E];
+        to_array(p, q);
+#pragma unroll
+        for (int k = 0; k < E; ++k) sums[padded(sp.column(i) + k)] += q[k];
+      }
     }
-    float sum = 0.f;
+    const float mean = reduce.add(fmaf(eg, eh, sum_of<E>(dots)), odd, 0) * inv_d;
+    if (kRing && !kWarp && plan.S > 2 && t > begin)
+      row.fill(t + (plan.S - 1) * step, row.stage == 0 ? plan.S - 1 : row.stage - 1);  // the row before's place
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int j = i * NT + tid, c = 8 * j - s;
-      if (j >= n) continue;
-      float xh[8], v[8], w[8];
-      unpack8(rh[i], xh);
-      unpack8(rd[i], v);
-      weights8(g.w, g.w_dtype, c, d, kAligned, w);
+      const int u = kHold ? i : 0;
+      if (!sp.has(i)) continue;
+      if (!kHold) {
+        xh[u] = row.get(0, i, t);
+        v[u] = row.get(1, i, t);
+        const Vals<E> wi = w.get(sp, i);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float p = v[k] * (xh[k] * rstd);
-        sum = fmaf(p, w[k], sum);
-        if (kAligned) acc[i][k] += p;
-        else if (parts && c + k >= 0 && c + k < d) dw_sh[c + k] += p;
+        for (int k = 0; k < E / 2; ++k) xh[u].p[k] = xh[u].p[k] * both(now), v[u].p[k] = v[u].p[k] * wi.p[k];
       }
+      const Vals<E> r = with_r ? row.get(2, i, t) : filled<E>(0.f);
+#pragma unroll
+      for (int k = 0; k < E / 2; ++k) v[u].p[k] = fma(both(now), fma(xh[u].p[k], both(-mean), v[u].p[k]), r.p[k]);
+      store_vals<E>(out.row(t), E == 8 ? 0 : out.f32, sp.column(i), ov, v[u]);
     }
-    const float mean = cta_add(sum, part[odd]) / static_cast<float>(d);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int j = i * NT + tid, c = 8 * j - s;
-      if (j >= n) continue;
-      float xh[8], v[8], w[8];
-      unpack8(rh[i], xh);
-      unpack8(rd[i], v);
-      weights8(g.w, g.w_dtype, c, d, kAligned, w);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = rstd * (v[k] * w[k] - xh[k] * rstd * mean);
-      if (g.dres) {
-        if (g.r_dtype == P24_BF16) {
-          const bf16* r = static_cast<const bf16*>(g.dres) + t * g.ldres;
-          unpack8(load8(r, c, d, kAligned || pieces_aligned(r, s)), w);
-        } else {
-          const float* r = static_cast<const float*>(g.dres) + t * g.ldres;
-          unpack8(load8(r, c, d, kAligned || pieces_aligned(r, s)), w);
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] += w[k];
+    if (sp.has_edge()) put_element(out.row(t), E == 8 ? 0 : out.f32, sp.edge, fmaf(now, fmaf(eh, -mean, eg), er));
+    if (kRing) {
+      // A warp's lanes have read the row now, a CTA's threads when they meet in the next row's reduction; with a
+      // ring of one or two rows that would be too late (16384 x 8192 fp32, two rows: 347 us, like this 280).
+      if (kWarp || plan.S <= 2) {
+        reduce.sync();
+        row.fill(t + plan.S * step, row.stage);
       }
-      if (g.dx_dtype == P24_BF16) {
-        bf16* to = static_cast<bf16*>(g.dx) + t * g.lddx;
-        store8(to, c, d, kAligned || pieces_aligned(to, s), v);
-      } else {
-        float* to = static_cast<float*>(g.dx) + t * g.lddx;
-        store8(to, c, d, kAligned || pieces_aligned(to, s), v);
-      }
+      row.advance();
     }
-    // the next row's phase gives a column to another thread
-    if (!kAligned) __syncthreads();
   }
+  if (kRing && sp.tid == 0) row.drain(begin < g.T ? (g.T - begin + step - 1) / step : 0);
   if (!parts) return;
-  float* to = parts + static_cast<int64_t>(blockIdx.x) * d;
-  if (kAligned) {
+  float* to = parts + static_cast<int64_t>(blockIdx.x) * sp.d;
+  if (kSums && !kWarp) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = 8 * (i * NT + tid);
-      if (c < d) store8(to, c, d, (d & 3) == 0, acc[i]);
+      if (!sp.has(i)) continue;
+      float v[E];
+      to_array(acc[kSums ? i : 0], v);
+      float* at = to + sp.column(i);
+      if (kAligned) {
+#pragma unroll
+        for (int k = 0; k < E; k += 4) *reinterpret_cast<float4*>(at + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < E; ++k) at[k] = v[k];
+      }
     }
-  } else {
-    for (int c = tid; c < d; c += NT) to[c] = dw_sh[c];
+    if (sp.has_edge()) to[sp.edge] = acc_e;
+    return;
+  }
+  __syncthreads();  // the rings are done with
+  if (kSums) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (!sp.has(i)) continue;
+      float v[E];
+      to_array(acc[kSums ? i : 0], v);
+#pragma unroll
+      for (int k = 0; k < E; ++k) sums[padded(sp.column(i) + k)] = v[k];
+    }
+  }
+  if (sp.has_edge()) sums[padded(sp.edge)] = acc_e;
+  __syncthreads();
+  sums = reinterpret_cast<float*>(smem);
+  for (int c = threadIdx.x; c < sp.d; c += blockDim.x) {
+    float v = sums[padded(c)];
+    for (int u = 1; u < per; ++u) v += sums[u * (plan.unit_bytes / 4) + padded(c)];
+    to[c] = v;
   }
 }
 
-// Column sums of the CTAs' parts [G, d]: 32 columns of a CTA, 8 warps that take every eighth row.
-__global__ void __launch_bounds__(256) dweight_kernel(const float* parts, int G, int d, float* dw) {
-  __shared__ float sh[8][32];
+// Column sums of the CTAs' parts [G, d]: 32 columns of a CTA, 32 warps that take
+// every 32nd row each.
+__global__ void __launch_bounds__(1024) dweight_kernel(const float* parts, int G, int d, float* dw) {
+  __shared__ float sh[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   pdl_wait();
   pdl_trigger();
   float s = 0.f;
   if (c < d) {
 #pragma unroll 8
-    for (int i = warp; i < G; i += 8) s += parts[static_cast<int64_t>(i) * d + c];
+    for (int i = warp; i < G; i += 32) s += parts[static_cast<int64_t>(i) * d + c];
   }
   sh[warp][lane] = s;
   __syncthreads();
-  if (warp == 0 && c < d) {
-    s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s += sh[i][lane];
-    dw[c] = s;
-  }
+  // warp i adds up column i, in one order
+  s = warp_add(sh[lane][warp]);
+  if (lane == 0 && blockIdx.x * 32 + warp < d) dw[blockIdx.x * 32 + warp] = s;
 }
 
-// Values of 8-bit codes: a thread takes 8 columns.
-template <typename To>
+// Values of 8-bit codes. A CTA: blockDim.x pieces of 8 columns, blockDim.y rows, U of them for a thread.
+template <typename To, int U>
 __global__ void __launch_bounds__(256) dequant8_kernel(const p24_dequant8_args g, bool qv, bool yv) {
-  const int d = static_cast<int>(g.d), n = (d + 7) >> 3;
-  const int64_t all = g.T * n;
+  const int d = static_cast<int>(g.d), c = 8 * (blockIdx.y * blockDim.x + threadIdx.x);
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * U * blockDim.y + threadIdx.y;
   pdl_wait();
   pdl_trigger();
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < all; i += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t t = i / n;
-    const int c = static_cast<int>(i - t * n) * 8;
-    const uint8_t* q = static_cast<const uint8_t*>(g.q) + t * g.ldq;
-    uint2 b = make_uint2(0, 0);
+  if (c >= d) return;
+  uint2 b[U];
+  float sc[U];
+  const int group = c / g.group;  // groups are multiples of 8 columns, or the whole row
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t t = t0 + u * blockDim.y;
+    if (t >= g.T) break;
+    const uint8_t* q = static_cast<const uint8_t*>(g.q) + t * g.ldq + c;
+    b[u] = make_uint2(0, 0);
     if (qv && c + 8 <= d) {
-      b = *reinterpret_cast<const uint2*>(q + c);
+      b[u] = *reinterpret_cast<const uint2*>(q);
     } else {
+#pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (c + k < d) (k < 4 ? b.x : b.y) |= static_cast<uint32_t>(q[c + k]) << (8 * (k & 3));
+        if (c + k < d) (k < 4 ? b[u].x : b[u].y) |= static_cast<uint32_t>(q[k]) << (8 * (k & 3));
     }
-    const float sc = g.scale[t * g.lds + c / g.group];
+    sc[u] = g.scale[t * g.lds + group];
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t t = t0 + u * blockDim.y;
+    if (t >= g.T) break;
     float v[8];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>((k < 2 ? b.x : b.y) >> (16 * (k & 1))), __NV_E4M3);
+      const __half2_raw h =
+          __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>((k < 2 ? b[u].x : b[u].y) >> (16 * (k & 1))), __NV_E4M3);
       const float2 f = __half22float2(__half2(h));
-      v[2 * k] = f.x * sc;
-      v[2 * k + 1] = f.y * sc;
+      v[2 * k] = f.x * sc[u];
+      v[2 * k + 1] = f.y * sc[u];
     }
     store8(static_cast<To*>(g.y) + t * g.ldy, c, d, yv, v);
   }
 }
 
-template <typename Tx, typename Tr, bool kWarp, bool kAligned>
-cudaError_t launch_norm_as(const p24_rmsnorm_args& g, Phase ph, int pieces, cudaStream_t s) {
-  const int groups = g.y_dtype == P24_E4M3 ? static_cast<int>((g.d + g.group - 1) / g.group) : 0;
-  auto go = [&](auto kern, int nv) {
-    const int NT = kWarp ? 256 : ((pieces + nv - 1) / nv + 31) / 32 * 32;
-    const size_t smem = groups > 1 ? groups * sizeof(float) * (kWarp ? NT / 32 : 1) : 0;
-    const int64_t rows = kWarp ? (g.T + NT / 32 - 1) / (NT / 32) : g.T;
-    const cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>(std::min<int64_t>(rows, sm_count() * 16))), dim3(NT), smem, s, g, ph);
-    if (e == cudaSuccess) count_launch();
-    return e;
-  };
-  if (kWarp) {
-    if (pieces <= 32) return go(rmsnorm_kernel<Tx, Tr, true, kAligned, 1>, 1);
-    return go(rmsnorm_kernel<Tx, Tr, true, kAligned, 4>, 4);
-  }
-  if (pieces <= 1024 && (g.T <= 2 * sm_count() || pieces <= 256)) return go(rmsnorm_kernel<Tx, Tr, false, kAligned, 1>, 1);
-  if (pieces <= 1024) return go(rmsnorm_kernel<Tx, Tr, false, kAligned, 2>, 2);
-  return go(rmsnorm_kernel<Tx, Tr, false, kAligned, 5>, 5);
-}
-template <typename Tx, typename Tr>
-cudaError_t launch_norm_types(const p24_rmsnorm_args& g, Phase ph, bool aligned, cudaStream_t s) {
-  const int pieces = static_cast<int>((g.d + (aligned ? 0 : 7) + 7) / 8);
-  if (pieces <= kWarpPieces)
-    return aligned ? launch_norm_as<Tx, Tr, true, true>(g, ph, pieces, s) : launch_norm_as<Tx, Tr, true, false>(g, ph, pieces, s);
-  return aligned ? launch_norm_as<Tx, Tr, false, true>(g, ph, pieces, s) : launch_norm_as<Tx, Tr, false, false>(g, ph, pieces, s);
-}
+constexpr int kWarpColumns = 512;      // rows of up to so many: a warp each
+constexpr size_t kShared = 220 << 10;  // of an SM, for the CTAs' rings
 
-// The phase of the first bf16 tensor among these, which fp32 ones of the same layout agree with.
 struct Lead {
   const void* p;
   int64_t ld;
   int32_t dtype;
 };
+// The phases of the first bf16 (or 8-bit) matrix among these, which fp32 ones of the same layout agree with.
 Phase phase_of(std::initializer_list<Lead> all) {
   const Lead* lead = all.begin();
   for (const Lead& l : all)
-    if (l.p && l.dtype == P24_BF16) {
+    if (l.p && l.dtype != P24_F32) {
       lead = &l;
       break;
     }
   const uintptr_t at = reinterpret_cast<uintptr_t>(lead->p) / size_of(lead->dtype);
   return Phase{static_cast<int>(at & 7), static_cast<int>(lead->ld & 7)};
 }
+// Whether the interiors of a matrix begin on 16-byte boundaries (8 bits: of 8) in every row, at the phases of `ph`.
+bool in_phase(const Lead& l, int64_t T, Phase ph) {
+  const int m = l.dtype == P24_F32 ? 3 : 7;
+  return !l.p || (((reinterpret_cast<uintptr_t>(l.p) / size_of(l.dtype) - ph.first) & m) == 0 && (T == 1 || ((l.ld - ph.step) & m) == 0));
+}
 
-// CTAs of the gradient, each with a row of partial sums: 2 for each SM.
-int64_t bwd_ctas(int64_t T) { return std::min<int64_t>(T, 2 * sm_count()); }
+// What a launch comes to: threads of a CTA, units of it, the plan, shared memory.
+struct Shape {
+  int NT, per;
+  Plan plan;
+  size_t smem;
+};
+// A ring of 2 to 4 rows and as many CTAs as make 1024 threads on an SM, or fewer CTAs, or one row. col_bytes: of a
+// column in all matrices that are read; own: what a unit has besides its ring and (16 columns a thread) the weights;
+// ahead: how many bytes an SM should have in its rings, 0 for as many as fit. The forward writes as much as it reads
+// and is fastest with few (16384 x 8192 bf16, rows of 32 KB: 169 us with 2, 179 with 3, 185 with 4); the gradient
+// with all (253, 167, 157).
+Shape ring_shape(int d, int C, bool warp, int col_bytes, size_t own, Phase ph, size_t ahead) {
+  constexpr int kThreads = 1024;  // of an SM; the registers of a thread allow no more
+  Shape z{};
+  z.plan.phase = ph;
+  z.NT = warp ? 256 : ((d + C - 1) / C + 31) / 32 * 32;
+  z.per = warp ? z.NT / 32 : 1;
+  const size_t cols = static_cast<size_t>(warp ? 32 : z.NT) * C, row = cols * col_bytes;
+  own += C > 8 ? cols * sizeof(float) : 0;
+  for (int c = std::max(1, kThreads / z.NT); c >= 1; --c) {
+    const size_t room = (kShared / c - 2048) / z.per;  // an SM reserves 1 KB for each CTA, and a CTA has static arrays
+    const size_t most = ahead ? std::max<size_t>(2, std::min<size_t>(kMostRows, ahead / (c * z.per * row))) : kMostRows;
+    const int S = static_cast<int>(std::min<size_t>(most, room > own ? (room - own) / row : 0));
+    if (S < 2 && (c > 1 || S < 1)) continue;
+    z.plan.S = S, z.plan.ring_bytes = static_cast<int>(S * row), z.plan.unit_bytes = static_cast<int>(S * row + own);
+    z.smem = z.per * static_cast<size_t>(z.plan.unit_bytes);
+    break;
+  }
+  return z;  // S = 0: too wide
+}
+Shape direct_shape(int d, int C, size_t own, Phase ph) {
+  Shape z{};
+  z.plan.phase = ph, z.per = 1, z.smem = own;
+  z.NT = ((d + C - 1) / C + 31) / 32 * 32;
+  return z;
+}
 
-template <typename Th, typename Td, bool kAligned>
-cudaError_t launch_bwd_as(const p24_rmsnorm_bwd_args& g, Phase ph, float* parts, cudaStream_t s) {
-  const int pieces = static_cast<int>((g.d + (kAligned ? 0 : 7) + 7) / 8);
-  auto go = [&](auto kern, int nv) {
-    const int NT = ((pieces + nv - 1) / nv + 31) / 32 * 32;
-    const size_t smem = kAligned || !parts ? 0 : g.d * sizeof(float);
-    if (smem > 40 << 10) {
-      const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kern), cudaFuncAttributeMaxDynamicSharedMemorySize, 160 << 10);
-      if (e != cudaSuccess) return e;
-    }
-    const cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>(bwd_ctas(g.T))), dim3(NT), smem, s, g, ph, parts);
+// CTAs for T rows: as many as run at once, and units a multiple of 8 so that each has rows of one phase.
+template <typename K>
+cudaError_t grid_of(K kern, const Shape& z, int64_t T, int64_t most, int64_t* grid) {
+  int slots = 0;
+  const cudaError_t e = row_kernel_slots(reinterpret_cast<const void*>(kern), z.NT, 1, z.smem, &slots);
+  int64_t n = std::min<int64_t>(slots, most);
+  if (z.per == 1 && n > 8) n = n / 8 * 8;
+  *grid = std::min<int64_t>({(T + z.per - 1) / z.per, n, most});
+  return e;
+}
+
+
+// Columns of a thread. 8, but 16 where CTAs of d / 8 threads leave an SM's 1024 a quarter empty or more (d = 5001:
+// one of 640): all bf16 8192 x 5001 60 us against 70, its gradient 71 against 81. With fp32 8 are faster there too.
+int columns_of(int d, int E, bool few) {
+  if (d > 8192) return 16;
+  const int NT = (d + 255) / 256 * 32;
+  return E == 8 && !few && 1024 / NT * NT < 768 ? 16 : 8;
+}
+
+template <bool kAligned, int E>
+cudaError_t launch_norm(const p24_rmsnorm_args& g, Phase ph, bool ring, int* status, cudaStream_t s) {
+  const int d = static_cast<int>(g.d);
+  const int bytes = size_of(g.x_dtype) + (g.r ? size_of(g.r_dtype) : 0);
+  const size_t groups = g.y_dtype == P24_E4M3 ? (d + g.group - 1) / g.group : 0, own = (groups * sizeof(float) + 15) / 16 * 16;
+  auto go = [&](auto kern, const Shape& z) {
+    int64_t grid = 0;
+    cudaError_t e = grid_of(kern, z, g.T, INT64_MAX, &grid);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(z.NT), z.smem, s, g, z.plan, status);
     if (e == cudaSuccess) count_launch();
     return e;
   };
-  if (pieces <= 512) return go(rmsnorm_bwd_kernel<Th, Td, kAligned, 1>, 1);
-  if (pieces <= 2048) return go(rmsnorm_bwd_kernel<Th, Td, kAligned, 2>, 2);
-  return go(rmsnorm_bwd_kernel<Th, Td, kAligned, 5>, 5);
+  if (ring && d <= kWarpColumns) {
+    if (d <= 256) return go(rmsnorm_kernel<true, kAligned, true, E, 8>, ring_shape(d, 8, true, bytes, own, ph, 80 << 10));
+    return go(rmsnorm_kernel<true, kAligned, true, E, 16>, ring_shape(d, 16, true, bytes, own, ph, 80 << 10));
+  }
+  const bool few = g.T <= 2 * sm_count();
+  const int C = columns_of(d, E, few);
+  const Shape z = ring_shape(d, C, false, bytes, own, ph, 80 << 10);
+  if (ring && d <= 16384 && z.plan.S > 0)
+    return C == 8 ? go(rmsnorm_kernel<false, kAligned, true, E, 8>, z) : go(rmsnorm_kernel<false, kAligned, true, E, 16>, z);
+  return go(rmsnorm_kernel<false, false, false, 4, 32>, direct_shape(d, 32, own, ph));
 }
-template <typename Th, typename Td>
-cudaError_t launch_bwd_types(const p24_rmsnorm_bwd_args& g, Phase ph, bool aligned, float* parts, cudaStream_t s) {
-  return aligned ? launch_bwd_as<Th, Td, true>(g, ph, parts, s) : launch_bwd_as<Th, Td, false>(g, ph, parts, s);
+
+// CTAs of the gradient, at most; each has a row of partial sums, and 8 rows or so of the batch for it.
+int64_t bwd_ctas(int64_t T) { return std::min<int64_t>(T, std::max<int64_t>(2 * sm_count(), std::min<int64_t>(16 * sm_count(), T / 8))); }
+
+template <bool kAligned, int E>
+cudaError_t launch_bwd(const p24_rmsnorm_bwd_args& g, Phase ph, bool ring, float* parts, int* status, cudaStream_t s, int64_t* used) {
+  const int d = static_cast<int>(g.d);
+  const int bytes = size_of(g.h_dtype) + size_of(g.dy_dtype) + (g.dres ? size_of(g.r_dtype) : 0);
+  auto go = [&](auto kern, const Shape& z) {
+    cudaError_t e = grid_of(kern, z, g.T, bwd_ctas(g.T) + 7, used);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(kern, dim3(static_cast<unsigned>(*used)), dim3(z.NT), z.smem, s, g, z.plan, parts, status);
+    if (e == cudaSuccess) count_launch();
+    return e;
+  };
+  if (ring && d <= kWarpColumns) {
+    if (d <= 256) return go(rmsnorm_bwd_kernel<true, kAligned, true, E, 8>, ring_shape(d, 8, true, bytes, 0, ph, 0));
+    return go(rmsnorm_bwd_kernel<true, kAligned, true, E, 16>, ring_shape(d, 16, true, bytes, 0, ph, 0));
+  }
+  const bool few = g.T <= 2 * sm_count();
+  const int C = columns_of(d, E, few);
+  const Shape z = ring_shape(d, C, false, bytes, 0, ph, 0);
+  if (ring && d <= 16384 && z.plan.S > 0)
+    return C == 8 ? go(rmsnorm_bwd_kernel<false, kAligned, true, E, 8>, z) : go(rmsnorm_bwd_kernel<false, kAligned, true, E, 16>, z);
+  const size_t sums = ((d + d / 8 + 1) * sizeof(float) + 15) / 16 * 16;
+  return go(rmsnorm_bwd_kernel<false, false, false, 4, 32>, direct_shape(d, 32, sums, ph));
+}
+
+// Pieces of 8 columns where nothing is fp32; aligned: no edges, and all on their boundaries in every row.
+struct Layout {
+  bool wide, aligned, ring;
+  Phase ph;
+};
+// in: what the ring reads (the first n); all: with the outputs.
+Layout layout_of(std::initializer_list<Lead> all, size_t n, int64_t T, int64_t d, const void* w) {
+  Layout l{true, false, true, phase_of(all)};
+  for (const Lead& m : all)
+    if (m.p && m.dtype == P24_F32) l.wide = false;
+  l.aligned = d % 8 == 0 && on16(w) && l.ph.first == 0 && (T == 1 || l.ph.step == 0);
+  size_t i = 0;
+  for (const Lead& m : all) {
+    const bool in = in_phase(m, T, l.ph);
+    l.aligned = l.aligned && in;
+    if (i++ < n) l.ring = l.ring && in;
+  }
+  return l;
 }
 
 }  // namespace
 
 int64_t rmsnorm_bwd_parts(int64_t T, int64_t d) { return bwd_ctas(T) * d; }
 
-cudaError_t launch_rmsnorm(const p24_rmsnorm_args& a, cudaStream_t s) {
+cudaError_t launch_rmsnorm(const p24_rmsnorm_args& a, int* status, cudaStream_t s) {
   p24_rmsnorm_args g = a;
   if (!g.r) g.r_dtype = g.x_dtype, g.h = nullptr;
   if (g.y_dtype == P24_E4M3 && (g.group == 0 || g.group > g.d)) g.group = static_cast<int32_t>(g.d);
-  const bool aligned = rows_aligned(g.x, g.ldx, g.x_dtype) && rows_aligned(g.r, g.ldr, g.r_dtype) && on16(g.w) &&
-                       rows_aligned(g.h, g.ldh, g.r_dtype) && rows_aligned(g.y, g.ldy, g.y_dtype);
-  const Phase ph = phase_of({{g.x, g.ldx, g.x_dtype}, {g.y, g.ldy, g.y_dtype}, {g.r, g.ldr, g.r_dtype}});
-  if (g.x_dtype == P24_BF16)
-    return g.r_dtype == P24_BF16 ? launch_norm_types<bf16, bf16>(g, ph, aligned, s) : launch_norm_types<bf16, float>(g, ph, aligned, s);
-  return g.r_dtype == P24_BF16 ? launch_norm_types<float, bf16>(g, ph, aligned, s) : launch_norm_types<float, float>(g, ph, aligned, s);
+  const Layout l = layout_of({{g.x, g.ldx, g.x_dtype}, {g.r, g.ldr, g.r_dtype}, {g.h, g.ldh, g.r_dtype}, {g.y, g.ldy, g.y_dtype}}, 2, g.T, g.d, g.w);
+  if (l.wide) return l.aligned ? launch_norm<true, 8>(g, l.ph, l.ring, status, s) : launch_norm<false, 8>(g, l.ph, l.ring, status, s);
+  return l.aligned ? launch_norm<true, 4>(g, l.ph, l.ring, status, s) : launch_norm<false, 4>(g, l.ph, l.ring, status, s);
 }
 
-cudaError_t launch_rmsnorm_bwd(const p24_rmsnorm_bwd_args& g, float* parts, cudaStream_t s) {
-  const bool aligned = rows_aligned(g.h, g.ldh, g.h_dtype) && rows_aligned(g.dy, g.lddy, g.dy_dtype) && on16(g.w) &&
-                       rows_aligned(g.dres, g.ldres, g.r_dtype) && rows_aligned(g.dx, g.lddx, g.dx_dtype);
-  const Phase ph = phase_of({{g.h, g.ldh, g.h_dtype}, {g.dy, g.lddy, g.dy_dtype}, {g.dx, g.lddx, g.dx_dtype}, {g.dres, g.ldres, g.r_dtype}});
+cudaError_t launch_rmsnorm_bwd(const p24_rmsnorm_bwd_args& g, float* parts, int* status, cudaStream_t s) {
+  const Layout l = layout_of({{g.h, g.ldh, g.h_dtype}, {g.dy, g.lddy, g.dy_dtype}, {g.dres, g.ldres, g.r_dtype}, {g.dx, g.lddx, g.dx_dtype}}, 3, g.T, g.d, g.w);
+  int64_t used = 0;
   float* to = g.dw ? parts : nullptr;
   cudaError_t e;
-  if (g.h_dtype == P24_BF16)
-    e = g.dy_dtype == P24_BF16 ? launch_bwd_types<bf16, bf16>(g, ph, aligned, to, s) : launch_bwd_types<bf16, float>(g, ph, aligned, to, s);
-  else
-    e = g.dy_dtype == P24_BF16 ? launch_bwd_types<float, bf16>(g, ph, aligned, to, s) : launch_bwd_types<float, float>(g, ph, aligned, to, s);
+  if (l.wide) e = l.aligned ? launch_bwd<true, 8>(g, l.ph, l.ring, to, status, s, &used) : launch_bwd<false, 8>(g, l.ph, l.ring, to, status, s, &used);
+  else e = l.aligned ? launch_bwd<true, 4>(g, l.ph, l.ring, to, status, s, &used) : launch_bwd<false, 4>(g, l.ph, l.ring, to, status, s, &used);
   if (e != cudaSuccess || !g.dw) return e;
   const int d = static_cast<int>(g.d);
-  e = launch_pdl(dweight_kernel, dim3((d + 31) / 32), dim3(256), 0, s, static_cast<const float*>(parts), static_cast<int>(bwd_ctas(g.T)), d, g.dw);
+  e = launch_pdl(dweight_kernel, dim3((d + 31) / 32), dim3(1024), 0, s, static_cast<const float*>(parts), static_cast<int>(used), d, g.dw);
   if (e == cudaSuccess) count_launch();
   return e;
 }
@@ -459,12 +958,20 @@ cudaError_t launch_dequant8(const p24_dequant8_args& a, cudaStream_t s) {
   p24_dequant8_args g = a;
   if (g.group == 0 || g.group > g.d) g.group = static_cast<int32_t>(g.d);
   const bool qv = rows_aligned(g.q, g.ldq, P24_E4M3), yv = rows_aligned(g.y, g.ldy, g.y_dtype);
-  const int64_t blocks = std::min<int64_t>((g.T * ((g.d + 7) / 8) + 255) / 256, sm_count() * 64);
-  const cudaError_t e = g.y_dtype == P24_BF16
-                            ? launch_pdl(dequant8_kernel<bf16>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, g, qv, yv)
-                            : launch_pdl(dequant8_kernel<float>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, g, qv, yv);
-  if (e == cudaSuccess) count_launch();
-  return e;
+  const int64_t n = (g.d + 7) / 8;
+  dim3 block(32);
+  while (block.x < 256 && block.x < n) block.x *= 2;
+  block.y = 256 / block.x;
+  const unsigned chunks = static_cast<unsigned>((n + block.x - 1) / block.x);
+  auto go = [&](auto kern, int u) {
+    const int64_t rows = static_cast<int64_t>(u) * block.y;
+    const cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>((g.T + rows - 1) / rows), chunks), block, 0, s, g, qv, yv);
+    if (e == cudaSuccess) count_launch();
+    return e;
+  };
+  const bool many = g.T * n >= 256 * 8 * 4 * sm_count();
+  if (g.y_dtype == P24_BF16) return many ? go(dequant8_kernel<bf16, 4>, 4) : go(dequant8_kernel<bf16, 1>, 1);
+  return many ? go(dequant8_kernel<float, 4>, 4) : go(dequant8_kernel<float, 1>, 1);
 }
 
 }  // namespace p24

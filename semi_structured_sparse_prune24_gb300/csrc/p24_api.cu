@@ -923,7 +923,9 @@ int p24_rmsnorm(const p24_rmsnorm_args* a, void* stream) {
   }
   if (a->T == 0) return P24_OK;
   if (!all_aligned4({a->scale, a->rstd})) return P24_EALIGN;
-  return cuda_status(launch_rmsnorm(*a, as_stream(stream)));
+  int* st = device_status_ptr();
+  if (!st) return P24_ECUDA;
+  return cuda_status(launch_rmsnorm(*a, st, as_stream(stream)));
 }
 
 size_t p24_rmsnorm_bwd_workspace_size(int64_t T, int64_t d) {
@@ -948,7 +950,9 @@ int p24_rmsnorm_bwd(const p24_rmsnorm_bwd_args* a, void* ws, size_t ws_bytes, vo
       !same_or_apart(a->dx, a->lddx, a->dx_dtype, a->dres, a->ldres, a->r_dtype))
     return P24_EINVAL;
   if (a->dw) P24_TRY(check_ws(ws, ws_bytes, p24_rmsnorm_bwd_workspace_size(a->T, a->d)));
-  return cuda_status(launch_rmsnorm_bwd(*a, static_cast<float*>(ws), as_stream(stream)));
+  int* st = device_status_ptr();
+  if (!st) return P24_ECUDA;
+  return cuda_status(launch_rmsnorm_bwd(*a, static_cast<float*>(ws), st, as_stream(stream)));
 }
 
 int p24_dequant8(const p24_dequant8_args* a, void* stream) {

@@ -110,9 +110,9 @@ cudaError_t launch_distill_bwd(const p24_distill_args& g, int* status, cudaStrea
 
 // ---- rows of hidden states, embedding, gradient norm (norm_kernels.cu, embed_kernels.cu, gradnorm_kernels.cu);
 // arguments checked by the caller, T > 0 (embed_bwd: T >= 0)
-cudaError_t launch_rmsnorm(const p24_rmsnorm_args& g, cudaStream_t s);
+cudaError_t launch_rmsnorm(const p24_rmsnorm_args& g, int* status, cudaStream_t s);
 int64_t rmsnorm_bwd_parts(int64_t T, int64_t d);  // floats of scratch for the weight's gradient
-cudaError_t launch_rmsnorm_bwd(const p24_rmsnorm_bwd_args& g, float* parts, cudaStream_t s);
+cudaError_t launch_rmsnorm_bwd(const p24_rmsnorm_bwd_args& g, float* parts, int* status, cudaStream_t s);
 cudaError_t launch_dequant8(const p24_dequant8_args& g, cudaStream_t s);
 cudaError_t launch_embed(const p24_embed_args& g, cudaStream_t s);
 size_t embed_bwd_workspace(int64_t T, int64_t d);

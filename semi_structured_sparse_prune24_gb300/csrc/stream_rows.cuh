@@ -24,6 +24,32 @@ using bf16 = __nv_bfloat16;
 __device__ __forceinline__ float to_float(bf16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_float(float x) { return x; }
 
+// Two fp32 operations in one instruction.
+struct Two {
+  unsigned long long v;
+};
+__device__ __forceinline__ Two two(float x, float y) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ Two both(float x) { return two(x, x); }
+__device__ __forceinline__ void apart(Two p, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p.v)); }
+__device__ __forceinline__ Two operator+(Two p, Two q) {
+  Two r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(p.v), "l"(q.v));
+  return r;
+}
+__device__ __forceinline__ Two operator*(Two p, Two q) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(p.v), "l"(q.v));
+  return r;
+}
+__device__ __forceinline__ Two fma(Two p, Two q, Two s) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(p.v), "l"(q.v), "l"(s.v));
+  return r;
+}
 // Eight elements as they lie in memory.
 template <typename T>
 struct Raw8 {
