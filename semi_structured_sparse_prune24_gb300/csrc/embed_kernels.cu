@@ -17,41 +17,87 @@
 namespace p24 {
 namespace {
 
+// A thread's 8 columns of a row: neighbours, moved 16 bytes at a time, where every row of a matrix lies on 16-byte
+// boundaries (kVec), else every blockDim.x-th one, moved element by element, so that a warp's access still covers
+// whole sectors (16384 x 767 bf16 looked up with 8 neighbours an element at a time 36 us, like this XXX).
+template <bool kVec>
+struct Columns {
+  int c, step, n;  // the first, from one to the next, how many of the 8 there are
+  __device__ __forceinline__ Columns(int chunk, int tid, int width, int d) {
+    c = chunk * width * 8 + (kVec ? 8 * tid : tid);
+    step = kVec ? 1 : width;
+    n = c >= d ? 0 : min(8, (d - c + step - 1) / step);
+  }
+};
+// A thread's elements as they lie in memory.
+template <bool kVec, typename T>
+struct Loaded {
+  Raw8<T> r;
+};
+template <typename T>
+struct Loaded<false, T> {
+  T e[8];
+};
+template <bool kVec, typename T>
+__device__ __forceinline__ Loaded<kVec, T> load_columns(const T* row, const Columns<kVec>& k) {
+  Loaded<kVec, T> x;
+  if constexpr (kVec) {
+    x.r = load8(row, k.c, k.c + k.n, true);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x.e[i] = i < k.n ? row[k.c + i * k.step] : static_cast<T>(0.f);
+  }
+  return x;
+}
+template <bool kVec, typename T>
+__device__ __forceinline__ void values(const Loaded<kVec, T>& x, float (&v)[8]) {
+  if constexpr (kVec) {
+    unpack8(x.r, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = to_float(x.e[i]);
+  }
+}
+template <bool kVec, typename T>
+__device__ __forceinline__ void store_columns(T* row, const Columns<kVec>& k, const float (&v)[8]) {
+  if (kVec && k.n == 8) {
+    store8(row, k.c, k.c + 8, true, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < k.n) row[k.c + i * k.step] = static_cast<T>(v[i]);
+  }
+}
+
 // ---------------------------------------------------------------- lookup
-// A CTA: blockDim.x pieces of 8 columns, blockDim.y rows, U of them for a thread.
-template <typename Tw, typename To, int U>
-__global__ void __launch_bounds__(256) embed_kernel(const p24_embed_args g, bool wv, bool yv) {
-  const int d = static_cast<int>(g.d), c = 8 * (blockIdx.y * blockDim.x + threadIdx.x);
+// A CTA: blockDim.x threads with 8 columns each, blockDim.y rows, U of them for a thread.
+template <typename Tw, typename To, int U, bool kVec>
+__global__ void __launch_bounds__(256) embed_kernel(const p24_embed_args g) {
+  const Columns<kVec> k(blockIdx.y, threadIdx.x, blockDim.x, static_cast<int>(g.d));
   const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * U) * blockDim.y + threadIdx.y;
   pdl_wait();
   pdl_trigger();
-  if (c >= d) return;
+  if (k.n == 0) return;
   int tok[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int64_t t = t0 + u * blockDim.y;
     tok[u] = t < g.T ? g.tokens[t] : -1;
   }
-  Raw8<Tw> r[U];
+  Loaded<kVec, Tw> r[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    if (tok[u] >= 0 && tok[u] < g.V) {
-      r[u] = load8(static_cast<const Tw*>(g.W) + static_cast<int64_t>(tok[u]) * g.ldw, c, d, wv);
-    } else {
-#pragma unroll
-      for (unsigned i = 0; i < sizeof(Tw) / 2; ++i) r[u].q[i] = make_uint4(0, 0, 0, 0);
-    }
-  }
+  for (int u = 0; u < U; ++u)
+    if (tok[u] >= 0 && tok[u] < g.V) r[u] = load_columns(static_cast<const Tw*>(g.W) + static_cast<int64_t>(tok[u]) * g.ldw, k);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int64_t t = t0 + u * blockDim.y;
     if (t >= g.T) break;
     float v[8];
-    unpack8(r[u], v);
     const bool in = tok[u] >= 0 && tok[u] < g.V;
+    if (in) values(r[u], v);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = in ? v[k] * g.scale : 0.f;  // a scale of infinity times a 0 that is not there
-    store8(static_cast<To*>(g.Y) + t * g.ldy, c, d, yv, v);
+    for (int i = 0; i < 8; ++i) v[i] = in ? v[i] * g.scale : 0.f;
+    store_columns(static_cast<To*>(g.Y) + t * g.ldy, k, v);
   }
 }
 
@@ -208,38 +254,43 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const p24_embe
 
 // ---------------------------------------------------------------- sums
 constexpr int kBlockMost = 64;  // sorted positions of a block, at most
+constexpr int kJoinThreads = 512;
 
 struct SumArgs {
   p24_embed_bwd_args g;
   const int2* sorted;
-  float* parts;  // [blocks, 2, dpad]: a block's part of the run that enters it, and of the one that leaves it
-  int64_t dpad;
+  float* parts;  // [blocks, 2, wide]: a block's part of the run that enters it, and of the one that leaves it
+  int64_t wide;  // 8 for each thread of a row's chunks
   int length;    // of a block
-  bool dyv, dwv;
 };
 
-template <typename To>
-__device__ __forceinline__ void put_row(const p24_embed_bwd_args& g, int v, int c, int d, bool vec, float (&s)[8]) {
-  To* to = static_cast<To*>(g.dW) + static_cast<int64_t>(v) * g.lddw;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) s[k] *= g.scale;
-  if (g.accumulate) {
-    float old[8];
-    unpack8(load8(static_cast<const To*>(to), c, d, vec), old);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) s[k] += old[k];
-  }
-  store8(to, c, d, vec, s);
+// A thread's 8 sums among the parts.
+__device__ __forceinline__ float* part_of(const SumArgs& a, int64_t block, int which, int width) {
+  return a.parts + (2 * block + which) * a.wide + (static_cast<int64_t>(blockIdx.y) * width + threadIdx.x) * 8;
 }
 
-template <typename Td, typename To, int U>
+template <bool kVec, typename To>
+__device__ __forceinline__ void put_row(const p24_embed_bwd_args& g, int v, const Columns<kVec>& k, float (&s)[8]) {
+  To* to = static_cast<To*>(g.dW) + static_cast<int64_t>(v) * g.lddw;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[i] *= g.scale;
+  if (g.accumulate) {
+    float old[8];
+    values(load_columns(static_cast<const To*>(to), k), old);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] += old[i];
+  }
+  store_columns(to, k, s);
+}
+
+template <typename Td, typename To, int U, bool kVec>
 __global__ void __launch_bounds__(256) embed_sum_kernel(const SumArgs a) {
   __shared__ int2 e[kBlockMost + 2];  // the block's, with its neighbours around it
   const p24_embed_bwd_args& g = a.g;
-  const int d = static_cast<int>(g.d), V = static_cast<int>(g.V);
+  const int V = static_cast<int>(g.V);
   const int64_t p0 = static_cast<int64_t>(blockIdx.x) * a.length;
   const int n = static_cast<int>(min(static_cast<int64_t>(a.length), g.T - p0));
-  const int c = 8 * (blockIdx.y * blockDim.x + threadIdx.x);
+  const Columns<kVec> k(blockIdx.y, threadIdx.x, blockDim.x, static_cast<int>(g.d));
   pdl_wait();
   pdl_trigger();
   for (int i = threadIdx.x; i < n + 2; i += blockDim.x) {
@@ -247,71 +298,87 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const SumArgs a) {
     e[i] = p >= 0 && p < g.T ? a.sorted[p] : make_int2(-1, -1);
   }
   __syncthreads();
-  if (c >= d) return;
+  if (k.n == 0) return;
   const Td* dy = static_cast<const Td*>(g.dY);
   float s[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) s[k] = 0.f;
+  for (int i = 0; i < 8; ++i) s[i] = 0.f;
   int start = 1;
-  for (int i0 = 1; i0 <= n; i0 += U) {
-    Raw8<Td> r[U];
+  for (int i0 = 1; i0 <= n && e[i0].x < V; i0 += U) {
+    Loaded<kVec, Td> r[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (i0 + u <= n && e[i0 + u].x < V) r[u] = load8(dy + static_cast<int64_t>(e[i0 + u].y) * g.lddy, c, d, a.dyv);
+      if (i0 + u <= n && e[i0 + u].x < V) r[u] = load_columns(dy + static_cast<int64_t>(e[i0 + u].y) * g.lddy, k);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u;
       if (i > n || e[i].x >= V) break;
       float v[8];
-      unpack8(r[u], v);
+      values(r[u], v);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) s[k] += v[k];
+      for (int j = 0; j < 8; ++j) s[j] += v[j];
       if (i < n && e[i + 1].x == e[i].x) continue;
       // a run ends, or the block does
       const bool enters = start == 1 && e[0].x == e[1].x, leaves = i == n && e[n + 1].x == e[n].x;
       if (!enters && !leaves) {
-        put_row<To>(g, e[i].x, c, d, a.dwv, s);
+        put_row<kVec, To>(g, e[i].x, k, s);
       } else {
-        float* to = a.parts + (2 * static_cast<int64_t>(blockIdx.x) + (enters ? 0 : 1)) * a.dpad + c;
+        float* to = part_of(a, blockIdx.x, enters ? 0 : 1, blockDim.x);
         reinterpret_cast<float4*>(to)[0] = make_float4(s[0], s[1], s[2], s[3]);
         reinterpret_cast<float4*>(to)[1] = make_float4(s[4], s[5], s[6], s[7]);
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) s[k] = 0.f;
+      for (int j = 0; j < 8; ++j) s[j] = 0.f;
       start = i + 1;
     }
   }
 }
 
-// For each run that crosses blocks, at the first border that it crosses: its parts.
-template <typename To>
-__global__ void __launch_bounds__(256) embed_join_kernel(const SumArgs a) {
+// For each run that crosses blocks, at the first border that it crosses: its parts, added up by blockDim.y groups of
+// threads that take neighbouring ones, and then group by group.
+template <typename To, bool kVec>
+__global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(const SumArgs a) {
+  __shared__ float groups[kJoinThreads][8];
   const p24_embed_bwd_args& g = a.g;
-  const int d = static_cast<int>(g.d);
   const int64_t blocks = (g.T + a.length - 1) / a.length;
-  const int c = 8 * (blockIdx.y * blockDim.x + threadIdx.x);
+  const Columns<kVec> k(blockIdx.y, threadIdx.x, blockDim.x, static_cast<int>(g.d));
+  const int me = threadIdx.y * blockDim.x + threadIdx.x;
   pdl_wait();
   pdl_trigger();
-  if (c >= d) return;
   for (int64_t b = blockIdx.x; b + 1 < blocks; b += gridDim.x) {
     const int64_t end = (b + 1) * a.length;
-    const int v = a.sorted[end - 1].x;
-    if (v >= g.V || a.sorted[end].x != v) continue;
-    if (b > 0 && a.sorted[end - a.length].x == v && a.sorted[end - a.length - 1].x == v) continue;  // it came from before
-    const float* p = a.parts + (2 * b + 1) * a.dpad + c;
-    float s[8];
-    const float4 x = reinterpret_cast<const float4*>(p)[0], y = reinterpret_cast<const float4*>(p)[1];
-    s[0] = x.x, s[1] = x.y, s[2] = x.z, s[3] = x.w, s[4] = y.x, s[5] = y.y, s[6] = y.z, s[7] = y.w;
-    // how far it goes: blocks whose first position has the token
-    int64_t last = b + 1;
-    while (last + 1 < blocks && a.sorted[(last + 1) * a.length].x == v) ++last;
-#pragma unroll 4
-    for (int64_t q = b + 1; q <= last; ++q) {
-      const float* part = a.parts + 2 * q * a.dpad + c;
-      const float4 u = reinterpret_cast<const float4*>(part)[0], w = reinterpret_cast<const float4*>(part)[1];
-      s[0] += u.x, s[1] += u.y, s[2] += u.z, s[3] += u.w, s[4] += w.x, s[5] += w.y, s[6] += w.z, s[7] += w.w;
+    const int v = a.sorted[end - 1].x, next = a.sorted[end].x;
+    const int first = a.sorted[end - a.length].x, before = b > 0 ? a.sorted[end - a.length - 1].x : -1;
+    if (v >= g.V || next != v || (first == v && before == v)) continue;  // no run crosses, or it came from before
+    // the blocks whose first position has the token
+    int64_t n = 0;
+    for (;;) {
+      const int64_t q = b + 1 + n + me;
+      const int more = __syncthreads_count(q < blocks && a.sorted[q * a.length].x == v);
+      n += more;
+      if (more < static_cast<int>(blockDim.x * blockDim.y)) break;
     }
-    put_row<To>(g, v, c, d, a.dwv, s);
+    const int64_t each = (n + 1 + blockDim.y - 1) / blockDim.y;  // with the part that leaves block b, which is the first
+    const int64_t lo = threadIdx.y * each, hi = min(n + 1, lo + each);
+    float s[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] = 0.f;
+#pragma unroll 8
+    for (int64_t q = lo; q < hi; ++q) {
+      const float* p = part_of(a, b + q, q == 0 ? 1 : 0, blockDim.x);
+      const float4 x = reinterpret_cast<const float4*>(p)[0], y = reinterpret_cast<const float4*>(p)[1];
+      s[0] += x.x, s[1] += x.y, s[2] += x.z, s[3] += x.w, s[4] += y.x, s[5] += y.y, s[6] += y.z, s[7] += y.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) groups[me][i] = s[i];
+    __syncthreads();
+    if (threadIdx.y == 0 && k.n > 0) {
+      for (int y = 1; y < static_cast<int>(blockDim.y); ++y)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] += groups[y * blockDim.x + threadIdx.x][i];
+      put_row<kVec, To>(g, v, k, s);
+    }
+    __syncthreads();
   }
 }
 
@@ -322,52 +389,66 @@ int block_length(int64_t T, int64_t d) {
   while (n < kBlockMost && n < want) n *= 2;
   return n;
 }
-int64_t pad8(int64_t d) { return (d + 7) / 8 * 8; }
 int64_t sort_bytes(int64_t T) { return (T * 8 + 255) / 256 * 256; }
 
-dim3 piece_block(int64_t d, int most) {
+// Threads of a row, 8 columns each: a power of two up to `most`, and chunks of as many.
+struct RowThreads {
+  int x;
+  unsigned chunks;
+};
+RowThreads row_threads(int64_t d, int most) {
   const int64_t n = (d + 7) / 8;
-  int x = 32;
-  while (x < most && x < n) x *= 2;
-  return dim3(x);
+  RowThreads r{32, 1};
+  while (r.x < most && r.x < n) r.x *= 2;
+  r.chunks = static_cast<unsigned>((n + r.x - 1) / r.x);
+  return r;
+}
+constexpr int kSumThreads = 128;
+int64_t wide_of(int64_t d) {
+  const RowThreads r = row_threads(d, kSumThreads);
+  return static_cast<int64_t>(r.x) * r.chunks * 8;
 }
 
-template <typename Td, typename To>
-cudaError_t launch_sums(const SumArgs& a, cudaStream_t s) {
-  const dim3 block = piece_block(a.g.d, 128);
+template <typename Td, typename To, bool kVec>
+cudaError_t launch_sums_as(const SumArgs& a, cudaStream_t s) {
+  const RowThreads r = row_threads(a.g.d, kSumThreads);
   const int64_t blocks = (a.g.T + a.length - 1) / a.length;
-  const unsigned chunks = static_cast<unsigned>(((a.g.d + 7) / 8 + block.x - 1) / block.x);
-  cudaError_t e = launch_pdl(embed_sum_kernel<Td, To, 4>, dim3(static_cast<unsigned>(blocks), chunks), block, 0, s, a);
+  cudaError_t e = launch_pdl(embed_sum_kernel<Td, To, 4, kVec>, dim3(static_cast<unsigned>(blocks), r.chunks), dim3(r.x), 0, s, a);
   if (e != cudaSuccess) return e;
   count_launch();
   if (blocks == 1) return e;
-  e = launch_pdl(embed_join_kernel<To>, dim3(static_cast<unsigned>(std::min<int64_t>(blocks - 1, 65535)), chunks), block, 0, s, a);
+  e = launch_pdl(embed_join_kernel<To, kVec>, dim3(static_cast<unsigned>(std::min<int64_t>(blocks - 1, 65535)), r.chunks),
+                 dim3(r.x, kJoinThreads / r.x), 0, s, a);
   if (e == cudaSuccess) count_launch();
   return e;
+}
+template <typename Td, typename To>
+cudaError_t launch_sums(const SumArgs& a, cudaStream_t s) {
+  const bool vec = rows_aligned(a.g.dY, a.g.lddy, a.g.dy_dtype) && rows_aligned(a.g.dW, a.g.lddw, a.g.dw_dtype);
+  return vec ? launch_sums_as<Td, To, true>(a, s) : launch_sums_as<Td, To, false>(a, s);
 }
 
 template <typename Tw, typename To>
 cudaError_t launch_embed_as(const p24_embed_args& g, cudaStream_t s) {
-  const bool wv = rows_aligned(g.W, g.ldw, g.w_dtype), yv = rows_aligned(g.Y, g.ldy, g.y_dtype);
-  dim3 block = piece_block(g.d, 256);
-  block.y = 256 / block.x;
-  const int64_t n = (g.d + 7) / 8;
-  const unsigned chunks = static_cast<unsigned>((n + block.x - 1) / block.x);
+  const bool vec = rows_aligned(g.W, g.ldw, g.w_dtype) && rows_aligned(g.Y, g.ldy, g.y_dtype);
+  const RowThreads r = row_threads(g.d, 256);
+  const dim3 block(r.x, 256 / r.x);
   auto go = [&](auto kern, int u) {
     const int64_t rows = static_cast<int64_t>(u) * block.y;
-    const cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>((g.T + rows - 1) / rows), chunks), block, 0, s, g, wv, yv);
+    const cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>((g.T + rows - 1) / rows), r.chunks), block, 0, s, g);
     if (e == cudaSuccess) count_launch();
     return e;
   };
-  if (g.T * n >= 256 * 8 * 4 * sm_count()) return go(embed_kernel<Tw, To, 4>, 4);
-  return go(embed_kernel<Tw, To, 1>, 1);
+  // 4 rows a thread where that leaves 8 CTAs for each SM
+  if (g.T * r.x * r.chunks >= 256 * 8 * 4 * sm_count()) return vec ? go(embed_kernel<Tw, To, 4, true>, 4) : go(embed_kernel<Tw, To, 4, false>, 4);
+  return vec ? go(embed_kernel<Tw, To, 1, true>, 1) : go(embed_kernel<Tw, To, 1, false>, 1);
 }
 
 }  // namespace
 
 size_t embed_bwd_workspace(int64_t T, int64_t d) {
   const int64_t blocks = (T + block_length(T, d) - 1) / block_length(T, d);
-  return static_cast<size_t>(2 * sort_bytes(T) + 2 * blocks * pad8(d) * sizeof(float));
+  return static_cast<size_t>(2 * sort_bytes(T) + 2 * blocks * wide_of(d) * sizeof(float));
 }
 
 cudaError_t launch_embed(const p24_embed_args& g, cudaStream_t s) {
@@ -376,8 +457,7 @@ cudaError_t launch_embed(const p24_embed_args& g, cudaStream_t s) {
 }
 
 cudaError_t launch_embed_bwd(const p24_embed_bwd_args& g, void* ws, cudaStream_t s) {
-  SumArgs a{g, nullptr, nullptr, pad8(g.d), block_length(g.T, g.d), rows_aligned(g.dY, g.lddy, g.dy_dtype),
-            rows_aligned(g.dW, g.lddw, g.dw_dtype)};
+  SumArgs a{g, nullptr, nullptr, wide_of(g.d), block_length(g.T, g.d)};
   int2* first = static_cast<int2*>(ws);
   int2* second = reinterpret_cast<int2*>(static_cast<uint8_t*>(ws) + sort_bytes(g.T));
   a.sorted = first;

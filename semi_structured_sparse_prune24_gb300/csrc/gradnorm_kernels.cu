@@ -3,11 +3,13 @@
 //
 //   norm = sqrt(sum over all tensors and elements of g^2);   g <- g min(1, max_norm / norm)
 //
-// The tensors are cut into chunks of 32 KB; CTA b of a fixed grid takes chunks b, b + grid, ... A thread
-// squares and adds the elements of a chunk in fp32 and the chunks' sums in fp64, so neither the number
-// of elements nor their size (squares outside fp32 are summed again in fp64) costs digits, and every sum
-// has a fixed order. The scaling pass goes through the chunks from the end, where the first pass left
-// off: what still is in L2 is read from there.
+// The tensors are cut into chunks of 4 to 32 KB, and each CTA of a fixed grid takes a stretch of them. A thread
+// squares and adds the elements of a chunk in fp32, and chunks, threads and CTAs are added as pairs of fp32 numbers,
+// a sum and what its rounding left (Knuth's two-sum): the number of elements costs no digits. Chunks whose sum
+// lies outside 2^-100 .. 2^100 are squared and added again in fp64, so neither does their size. (All of it in
+// fp64 beyond the chunks took 45 us for 72 tensors of 4.8 MB: an SM adds two a clock.) Every sum has a fixed
+// order. The scaling pass walks the stretches backwards: what the first pass read last is read
+// from L2.
 #include <algorithm>
 
 #include "stream_rows.cuh"
@@ -15,45 +17,60 @@
 namespace p24 {
 namespace {
 
-constexpr int kThreads = 256, kUnroll = 8;
-constexpr int64_t kChunk = kThreads * kUnroll;  // 16-byte vectors
+constexpr int kThreads = 256, kUnroll = 8, kCtas = 4;  // of an SM
+constexpr int64_t kChunk = kThreads * kUnroll;  // 16-byte vectors, at most
+constexpr int kMostTable = 850;   // tensors of a launch: its parameters are up to 32 764 bytes
+constexpr int kMostCtas = 1024;
 
 // The list goes with the launch: no copy to the device, and a captured graph keeps its own.
+struct Entry {
+  const uint8_t* p;
+  uint8_t* to;
+  int64_t n;      // elements
+  int32_t chunk;  // the first one
+  int32_t f32;
+};
 template <int N>
 struct Table {
-  const void* p[N];
-  void* to[N];
-  int64_t n[N];
-  int32_t chunk[N + 1];  // the first chunk of each tensor; past the last: all chunks
-  uint8_t dtype[N];
-  int32_t count;
+  Entry e[N + 1];               // the last has the number of chunks
+  uint16_t first[kMostCtas];    // the tensor that a CTA's stretch begins in
+  int32_t vecs;                 // 16-byte vectors of a chunk
+  int32_t chunks, ctas;
 };
+
+static_assert(sizeof(Table<kMostTable>) + 64 <= 32764, "a launch's parameters");
 
 struct Piece {  // a chunk of a tensor
   const uint8_t* p;
   uint8_t* to;
-  int64_t n, vec0, vecs;  // elements; the chunk's first vector and how many it has
+  int64_t n, vec0;        // elements of the tensor; the chunk's first vector
+  int vecs;               // and how many it has
   int head, tail, f32;    // elements before the tensor's first 16-byte boundary and after its last one
   bool first;             // takes those
 };
 
+// Chunk c, of tensor `at` or one near it. (Looked up from a CTA's first tensor on: a search from the list's
+// beginning went through the launch's constants one miss at a time, 13 us for 72 tensors of 600 KB in all.)
 template <int N>
-__device__ __forceinline__ Piece piece_of(const Table<N>& t, int chunk, int& at) {
-  while (chunk < t.chunk[at]) --at;
-  while (chunk >= t.chunk[at + 1]) ++at;
+__device__ __forceinline__ Piece piece_of(const Table<N>& t, int c, int& at) {
+  while (c < t.e[at].chunk) --at;
+  while (c >= t.e[at + 1].chunk) ++at;
+  const Entry& e = t.e[at];
   Piece r;
-  r.p = static_cast<const uint8_t*>(t.p[at]);
-  r.to = static_cast<uint8_t*>(t.to[at]);
-  r.n = t.n[at];
-  r.f32 = t.dtype[at] == P24_F32;
+  r.p = e.p, r.to = e.to, r.n = e.n, r.f32 = e.f32;
   const int shift = r.f32 ? 2 : 1;
   r.head = static_cast<int>(min(r.n, static_cast<int64_t>(((16 - (reinterpret_cast<uintptr_t>(r.p) & 15u)) & 15u) >> shift)));
   const int64_t all = (r.n - r.head) << shift >> 4;
   r.tail = static_cast<int>(r.n - r.head - (all << 4 >> shift));
-  r.vec0 = (chunk - t.chunk[at]) * kChunk;
-  r.vecs = min(all - r.vec0, kChunk);
+  r.vec0 = static_cast<int64_t>(c - e.chunk) * t.vecs;
+  r.vecs = static_cast<int>(min(all - r.vec0, static_cast<int64_t>(t.vecs)));
   r.first = r.vec0 == 0;
   return r;
+}
+// CTA b's stretch of the chunks.
+template <int N>
+__device__ __forceinline__ int stretch(const Table<N>& t, int b) {
+  return static_cast<int>(static_cast<int64_t>(t.chunks) * b / t.ctas);
 }
 
 __device__ __forceinline__ float element(const Piece& r, int64_t i) {
@@ -72,26 +89,64 @@ __device__ __forceinline__ void words8(const uint4& q, bool f32, float (&v)[8]) 
   }
 }
 
-// The sum over a CTA in thread 0, in a fixed order.
-__device__ __forceinline__ double cta_sum(double x, double* sh) {
+// A sum and what its rounding left.
+struct Pair {
+  float hi, lo;
+};
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return Pair{s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Pair add(const Pair& a, const Pair& b) {
+  const Pair s = two_sum(a.hi, b.hi);
+  return two_sum(s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)));
+}
+
+// What a CTA, or all of them, come to: the sum of the chunks in range, and of the others.
+struct Sum {
+  Pair in;
+  double out;
+};
+struct SumShared {
+  Pair in[kThreads / 32];
+  double out[kThreads / 32];
+};
+// Over the CTA, in every thread.
+__device__ __forceinline__ Sum cta_sum(Sum x, SumShared& sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // a bit pattern other than 0: a number, or NaN
+  const bool rare = __syncthreads_or(__double_as_longlong(x.out) != 0);
 #pragma unroll
-  for (int i = 16; i; i >>= 1) x += __shfl_xor_sync(~0u, x, i);
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
+  for (int i = 16; i; i >>= 1) x.in = add(x.in, Pair{__shfl_xor_sync(~0u, x.in.hi, i), __shfl_xor_sync(~0u, x.in.lo, i)});
+  if (lane == 0) sh.in[warp] = x.in;
+  if (rare) {
+#pragma unroll 1
+    for (int i = 16; i; i >>= 1) x.out += __shfl_xor_sync(~0u, x.out, i);
+    if (lane == 0) sh.out[warp] = x.out;
+  }
   __syncthreads();
-  x = 0;
+  Sum y{sh.in[0], 0.0};
 #pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) x += sh[i];
-  return x;
+  for (int i = 1; i < kThreads / 32; ++i) y.in = add(y.in, sh.in[i]);
+  if (rare)
+#pragma unroll 1
+    for (int i = 0; i < kThreads / 32; ++i) y.out += sh.out[i];
+  return y;
+}
+__device__ __forceinline__ float root(const Sum& s) {
+  if (__double_as_longlong(s.out) == 0) return sqrtf(__fadd_rn(s.in.hi, s.in.lo));
+  return static_cast<float>(sqrt(s.out + s.in.hi + s.in.lo));
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads) grad_squares_kernel(const __grid_constant__ Table<N> t, double* sums) {
-  __shared__ double sh[kThreads / 32];
+__global__ void __launch_bounds__(kThreads, kCtas) grad_squares_kernel(const __grid_constant__ Table<N> t, Sum* sums) {
+  __shared__ SumShared sh;
+  const int lo = stretch(t, blockIdx.x), hi = stretch(t, blockIdx.x + 1);
+  int at = t.first[blockIdx.x];
   pdl_wait();
   pdl_trigger();
-  double total = 0;
-  int at = 0;
-  for (int c = blockIdx.x; c < t.chunk[t.count]; c += gridDim.x) {
+  Sum total{Pair{0.f, 0.f}, 0.0};
+  for (int c = lo; c < hi; ++c) {
     const Piece r = piece_of(t, c, at);
     const uint4* q = reinterpret_cast<const uint4*>(r.p + (r.head << (r.f32 ? 2 : 1))) + r.vec0;
     uint4 x[kUnroll];
@@ -112,19 +167,23 @@ __global__ void __launch_bounds__(kThreads) grad_squares_kernel(const __grid_con
       for (int k = 0; k < 8; k += 2) s0 = fmaf(v[k], v[k], s0), s1 = fmaf(v[k + 1], v[k + 1], s1);
     }
     const float s = s0 + s1;
-    if (s >= 0x1p-100f && s < __int_as_float(0x7f800000)) {
-      total += s;
-    } else {  // zeros, or squares that fp32 does not hold
-      total += static_cast<double>(edge) * edge;
-#pragma unroll 1
-      for (int u = 0; u < kUnroll; ++u) {
-        const int i = u * kThreads + threadIdx.x;
-        float v[8];
-        words8(i < r.vecs ? q[i] : make_uint4(0, 0, 0, 0), r.f32, v);
+    if (s >= 0x1p-100f && s <= 0x1p100f) {
+      total.in = add(total.in, Pair{s, 0.f});
+      continue;
+    }
+    // only zeros, or squares that fp32 does not hold, or no numbers
+    uint32_t any = __float_as_uint(edge);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (v[k] != 0.f) total += static_cast<double>(v[k]) * v[k];
-      }
+    for (int u = 0; u < kUnroll; ++u) any |= x[u].x | x[u].y | x[u].z | x[u].w;
+    if ((any & (r.f32 ? 0x7fffffffu : 0x7fff7fffu)) == 0) continue;
+    total.out += static_cast<double>(edge) * edge;
+#pragma unroll 1
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = u * kThreads + threadIdx.x;
+      float v[8];
+      words8(i < r.vecs ? q[i] : make_uint4(0, 0, 0, 0), r.f32, v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) total.out += static_cast<double>(v[k]) * v[k];
     }
   }
   total = cta_sum(total, sh);
@@ -132,14 +191,19 @@ __global__ void __launch_bounds__(kThreads) grad_squares_kernel(const __grid_con
 }
 
 // The norm of `n` CTAs' sums, in every thread.
-__device__ __forceinline__ float norm_of(const double* sums, int n, double* sh) {
-  double x = 0;
-  for (int i = threadIdx.x; i < n; i += kThreads) x += sums[i];
-  return static_cast<float>(sqrt(cta_sum(x, sh)));
+__device__ __forceinline__ float norm_of(const Sum* sums, int n, SumShared& sh) {
+  Sum x{Pair{0.f, 0.f}, 0.0};
+#pragma unroll 4
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const Sum y = sums[i];
+    x.in = add(x.in, y.in);
+    if (__double_as_longlong(y.out) != 0) x.out += y.out;
+  }
+  return root(cta_sum(x, sh));
 }
 
-__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const double* sums, int n, float* norm) {
-  __shared__ double sh[kThreads / 32];
+__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const Sum* sums, int n, float* norm) {
+  __shared__ SumShared sh;
   pdl_wait();
   pdl_trigger();
   const float x = norm_of(sums, n, sh);
@@ -147,17 +211,18 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const double* sums,
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_constant__ Table<N> t, const double* sums, int n,
+__global__ void __launch_bounds__(kThreads, kCtas) grad_scale_kernel(const __grid_constant__ Table<N> t, const Sum* sums, int n,
                                                               float max_norm, float* norm) {
-  __shared__ double sh[kThreads / 32];
+  __shared__ SumShared sh;
+  const int lo = stretch(t, blockIdx.x), hi = stretch(t, blockIdx.x + 1);
+  int at = blockIdx.x + 1 < gridDim.x ? t.first[blockIdx.x + 1] : t.first[blockIdx.x];
   pdl_wait();
   pdl_trigger();
   const float x = norm_of(sums, n, sh);
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = x;
   const bool over = x > max_norm && x < __int_as_float(0x7f800000);  // a norm that is no number scales nothing
   const float f = over ? max_norm / x : 1.f;
-  int at = t.count - 1;
-  for (int c = t.chunk[t.count] - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x) {
+  for (int c = hi - 1; c >= lo; --c) {
     const Piece r = piece_of(t, c, at);
     if (!over && r.to == r.p) continue;
     const int shift = r.f32 ? 2 : 1;
@@ -203,56 +268,61 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_const
   }
 }
 
-constexpr int kMostTable = 900;
-int64_t grid_most() { return sm_count() * 6; }
+// As many as run at once: each has a stretch of the same length.
+int64_t grid_most() { return std::min<int64_t>(kMostCtas, sm_count() * kCtas); }
 
-int64_t chunks_of(const p24_tensor& t) {
+int64_t chunks_of(const p24_tensor& t, int64_t most) {
   const int64_t size = t.dtype == P24_F32 ? 4 : 2;
   const int64_t head = std::min<int64_t>(t.n, ((16 - (reinterpret_cast<uintptr_t>(t.p) & 15u)) & 15u) / size);
   const int64_t vecs = (t.n - head) * size / 16;
-  return t.n == 0 ? 0 : std::max<int64_t>(1, (vecs + kChunk - 1) / kChunk);
+  return t.n == 0 ? 0 : std::max<int64_t>(1, (vecs + most - 1) / most);
 }
 
-// Tensors [from, ...) of the list, as many as one launch takes.
+// Tensors [from, ...) of the list, as many as one launch takes; returns where the next one goes on.
 template <int N>
 int64_t fill_table(Table<N>& t, const p24_tensor* g, const p24_tensor* out, int64_t n, int64_t from) {
-  int64_t chunks = 0, i = from;
-  t.count = 0;
-  for (; i < n && t.count < N; ++i) {
-    const int64_t c = chunks_of(g[i]);
+  int64_t chunks = 0, bytes = 0, i = from;
+  int count = 0;
+  for (int64_t k = from; k < std::min<int64_t>(n, from + N); ++k) bytes += g[k].n * (g[k].dtype == P24_F32 ? 4 : 2);
+  // chunks as long as leaves each CTA some
+  int64_t vecs = kChunk;
+  while (vecs > kThreads && bytes < vecs * 16 * grid_most()) vecs /= 2;
+  t.vecs = static_cast<int32_t>(vecs);
+  for (; i < n && count < N; ++i) {
+    const int64_t c = chunks_of(g[i], vecs);
     if (c == 0) continue;
-    t.p[t.count] = g[i].p;
-    t.to[t.count] = out ? out[i].p : const_cast<void*>(static_cast<const void*>(g[i].p));
-    t.n[t.count] = g[i].n;
-    t.dtype[t.count] = static_cast<uint8_t>(g[i].dtype);
-    t.chunk[t.count++] = static_cast<int32_t>(chunks);
+    t.e[count++] = Entry{static_cast<const uint8_t*>(g[i].p), static_cast<uint8_t*>(out ? out[i].p : g[i].p), g[i].n,
+                         static_cast<int32_t>(chunks), g[i].dtype == P24_F32};
     chunks += c;
   }
-  t.chunk[t.count] = static_cast<int32_t>(chunks);
+  t.e[count].chunk = t.chunks = static_cast<int32_t>(chunks);
+  t.ctas = static_cast<int32_t>(std::min<int64_t>(chunks, grid_most()));
+  for (int b = 0, at = 0; b < t.ctas; ++b) {
+    while (chunks * b / t.ctas >= t.e[at + 1].chunk) ++at;
+    t.first[b] = static_cast<uint16_t>(at);
+  }
   return i;
 }
 
 template <int N>
-cudaError_t run_list(const p24_tensor* g, const p24_tensor* out, int64_t n, bool scale, float max_norm, float* norm, double* sums,
+cudaError_t run_list(const p24_tensor* g, const p24_tensor* out, int64_t n, bool scale, float max_norm, float* norm, Sum* sums,
                      cudaStream_t s) {
   Table<N> t;
   int64_t used = 0;
   cudaError_t e;
   for (int64_t i = 0; i < n;) {
     i = fill_table(t, g, nullptr, n, i);
-    if (t.count == 0) continue;
-    const int64_t grid = std::min<int64_t>(t.chunk[t.count], grid_most());
-    e = launch_pdl(grad_squares_kernel<N>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, t, sums + used);
+    if (t.chunks == 0) continue;
+    e = launch_pdl(grad_squares_kernel<N>, dim3(static_cast<unsigned>(t.ctas)), dim3(kThreads), 0, s, t, sums + used);
     if (e != cudaSuccess) return e;
     count_launch();
-    used += grid;
+    used += t.ctas;
   }
   if (scale && used > 0) {
     for (int64_t i = 0; i < n;) {
       i = fill_table(t, g, out, n, i);
-      if (t.count == 0) continue;
-      const int64_t grid = std::min<int64_t>(t.chunk[t.count], grid_most());
-      e = launch_pdl(grad_scale_kernel<N>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, t, static_cast<const double*>(sums),
+      if (t.chunks == 0) continue;
+      e = launch_pdl(grad_scale_kernel<N>, dim3(static_cast<unsigned>(t.ctas)), dim3(kThreads), 0, s, t, static_cast<const Sum*>(sums),
                      static_cast<int>(used), max_norm, norm);
       if (e != cudaSuccess) return e;
       count_launch();
@@ -260,7 +330,7 @@ cudaError_t run_list(const p24_tensor* g, const p24_tensor* out, int64_t n, bool
     return cudaSuccess;
   }
   if (!norm) return cudaSuccess;  // an empty list, and no norm asked for
-  e = launch_pdl(grad_norm_kernel, dim3(1), dim3(kThreads), 0, s, static_cast<const double*>(sums), static_cast<int>(used), norm);
+  e = launch_pdl(grad_norm_kernel, dim3(1), dim3(kThreads), 0, s, static_cast<const Sum*>(sums), static_cast<int>(used), norm);
   if (e == cudaSuccess) count_launch();
   return e;
 }
@@ -269,12 +339,12 @@ cudaError_t run_list(const p24_tensor* g, const p24_tensor* out, int64_t n, bool
 
 // A sum for each CTA of the launches that a list of n tensors takes.
 size_t grad_norm_workspace(int64_t n) {
-  return static_cast<size_t>(std::max<int64_t>(1, (n + kMostTable - 1) / kMostTable) * grid_most()) * sizeof(double);
+  return static_cast<size_t>(std::max<int64_t>(1, (n + kMostTable - 1) / kMostTable) * grid_most()) * sizeof(Sum);
 }
 
 cudaError_t launch_grad_norm(const p24_tensor* g, const p24_tensor* out, int64_t n, bool scale, float max_norm, float* norm,
                              void* ws, cudaStream_t s) {
-  double* sums = static_cast<double*>(ws);
+  Sum* sums = static_cast<Sum*>(ws);
   if (n <= 16) return run_list<16>(g, out, n, scale, max_norm, norm, sums, s);
   if (n <= 128) return run_list<128>(g, out, n, scale, max_norm, norm, sums, s);
   return run_list<kMostTable>(g, out, n, scale, max_norm, norm, sums, s);
