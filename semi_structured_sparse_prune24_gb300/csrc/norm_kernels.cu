@@ -417,6 +417,7 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024, kWarp ? (C > 8 ? 3 : 4) : 
   Weights<NV, E> w;
   float* tops = reinterpret_cast<float*>(own + plan.ring_bytes + (w.kHow == 1 ? sp.NT * C * 4 : 0));
   const int groups = quant ? (sp.d + g.group - 1) / g.group : 0;
+  const int shift = groups > 1 ? 31 - __clz(g.group) : 30;  // several groups are of a power of two
   const Matrix h_out(g.h, g.ldh, g.r_dtype), y_out(g.y, g.ldy, g.y_dtype);
   const bool hv = sp.fits(h_out, begin), yv = sp.fits(y_out, begin);
   const float inv_d = 1.f / static_cast<float>(sp.d);
@@ -522,7 +523,7 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024, kWarp ? (C > 8 ? 3 : 4) : 
         for (int k = lanes >> 1; k; k >>= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, k));
         const float sc = scale_of(top), inv = 1.f / sc;
         if (!sp.has(i)) continue;
-        if ((lane & (lanes - 1)) == 0) scales[sp.column(i) / g.group] = sc;
+        if ((lane & (lanes - 1)) == 0) scales[sp.column(i) >> shift] = sc;
         store_e4m3<E>(y, sp.column(i), qv, h[i], inv, inv, E);
       }
     } else {
@@ -534,7 +535,7 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024, kWarp ? (C > 8 ? 3 : 4) : 
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if (!sp.has(i)) continue;
-        const int c = sp.column(i), ga = c / g.group, gb = (c + E - 1) / g.group, cut = ga == gb ? E : gb * g.group - c;
+        const int c = sp.column(i), ga = c >> shift, gb = (c + E - 1) >> shift, cut = ga == gb ? E : (gb << shift) - c;
         float v[E], ta = 0.f, tb = 0.f;
         to_array(h[i], v);
 #pragma unroll
@@ -544,15 +545,15 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024, kWarp ? (C > 8 ? 3 : 4) : 
         note(ga, ta);
         if (ga != gb) note(gb, tb);
       }
-      if (sp.has_edge()) note(sp.edge / g.group, max_nan(fabsf(e), 0.f));
+      if (sp.has_edge()) note(sp.edge >> shift, max_nan(fabsf(e), 0.f));
       reduce.sync();
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if (!sp.has(i)) continue;
-        const int c = sp.column(i), ga = c / g.group, gb = (c + E - 1) / g.group;
-        store_e4m3<E>(y, c, qv, h[i], 1.f / scale_of(tops[ga]), 1.f / scale_of(tops[gb]), ga == gb ? E : gb * g.group - c);
+        const int c = sp.column(i), ga = c >> shift, gb = (c + E - 1) >> shift;
+        store_e4m3<E>(y, c, qv, h[i], 1.f / scale_of(tops[ga]), 1.f / scale_of(tops[gb]), ga == gb ? E : (gb << shift) - c);
       }
-      if (sp.has_edge()) y[sp.edge] = static_cast<uint8_t>(e4m3x4(e * (1.f / scale_of(tops[sp.edge / g.group])), 0.f, 0.f, 0.f));
+      if (sp.has_edge()) y[sp.edge] = static_cast<uint8_t>(e4m3x4(e * (1.f / scale_of(tops[sp.edge >> shift])), 0.f, 0.f, 0.f));
       for (int i = sp.tid; i < groups; i += sp.NT) scales[i] = scale_of(tops[i]);
       reduce.sync();  // before the next row's groups
     }
@@ -730,31 +731,32 @@ __global__ void __launch_bounds__(1024) dweight_kernel(const float* parts, int G
   if (lane == 0 && blockIdx.x * 32 + warp < d) dw[blockIdx.x * 32 + warp] = s;
 }
 
-// Values of 8-bit codes. A CTA: blockDim.x pieces of 8 columns, blockDim.y rows, U of them for a thread.
-template <typename To, int U>
-__global__ void __launch_bounds__(256) dequant8_kernel(const p24_dequant8_args g, bool qv, bool yv) {
-  const int d = static_cast<int>(g.d), c = 8 * (blockIdx.y * blockDim.x + threadIdx.x);
+// Values of 8-bit codes. A CTA: blockDim.x threads with 8 columns each, blockDim.y rows, U of them for a thread.
+template <typename To, int U, bool kVec>
+__global__ void __launch_bounds__(256) dequant8_kernel(const p24_dequant8_args g, int shift) {
+  const Columns<kVec> k(blockIdx.y, threadIdx.x, blockDim.x, static_cast<int>(g.d));
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * U * blockDim.y + threadIdx.y;
   pdl_wait();
   pdl_trigger();
-  if (c >= d) return;
+  if (k.n == 0) return;
   uint2 b[U];
-  float sc[U];
-  const int group = c / g.group;  // groups are multiples of 8 columns, or the whole row
+  float sc[U][kVec ? 1 : 8];  // groups are multiples of 8 columns (shift: of how many), or the whole row
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int64_t t = t0 + u * blockDim.y;
     if (t >= g.T) break;
-    const uint8_t* q = static_cast<const uint8_t*>(g.q) + t * g.ldq + c;
+    const uint8_t* q = static_cast<const uint8_t*>(g.q) + t * g.ldq + k.c;
+    const float* scale = g.scale + t * g.lds;
     b[u] = make_uint2(0, 0);
-    if (qv && c + 8 <= d) {
+    if (kVec && k.n == 8) {
       b[u] = *reinterpret_cast<const uint2*>(q);
     } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (c + k < d) (k < 4 ? b[u].x : b[u].y) |= static_cast<uint32_t>(q[k]) << (8 * (k & 3));
+      for (int i = 0; i < 8; ++i)
+        if (i < k.n) (i < 4 ? b[u].x : b[u].y) |= static_cast<uint32_t>(q[i * k.step]) << (8 * (i & 3));
     }
-    sc[u] = g.scale[t * g.lds + group];
+#pragma unroll
+    for (int i = 0; i < (kVec ? 1 : 8); ++i) sc[u][i] = i < k.n ? scale[(k.c + i * k.step) >> shift] : 0.f;
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -762,14 +764,14 @@ __global__ void __launch_bounds__(256) dequant8_kernel(const p24_dequant8_args g
     if (t >= g.T) break;
     float v[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int i = 0; i < 4; ++i) {
       const __half2_raw h =
-          __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>((k < 2 ? b[u].x : b[u].y) >> (16 * (k & 1))), __NV_E4M3);
+          __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>((i < 2 ? b[u].x : b[u].y) >> (16 * (i & 1))), __NV_E4M3);
       const float2 f = __half22float2(__half2(h));
-      v[2 * k] = f.x * sc[u];
-      v[2 * k + 1] = f.y * sc[u];
+      v[2 * i] = f.x * sc[u][kVec ? 0 : 2 * i];
+      v[2 * i + 1] = f.y * sc[u][kVec ? 0 : 2 * i + 1];
     }
-    store8(static_cast<To*>(g.y) + t * g.ldy, c, d, yv, v);
+    store_columns(static_cast<To*>(g.y) + t * g.ldy, k, v);
   }
 }
 
@@ -957,21 +959,23 @@ cudaError_t launch_rmsnorm_bwd(const p24_rmsnorm_bwd_args& g, float* parts, int*
 cudaError_t launch_dequant8(const p24_dequant8_args& a, cudaStream_t s) {
   p24_dequant8_args g = a;
   if (g.group == 0 || g.group > g.d) g.group = static_cast<int32_t>(g.d);
-  const bool qv = rows_aligned(g.q, g.ldq, P24_E4M3), yv = rows_aligned(g.y, g.ldy, g.y_dtype);
-  const int64_t n = (g.d + 7) / 8;
-  dim3 block(32);
-  while (block.x < 256 && block.x < n) block.x *= 2;
-  block.y = 256 / block.x;
-  const unsigned chunks = static_cast<unsigned>((n + block.x - 1) / block.x);
+  const bool vec = rows_aligned(g.q, g.ldq, P24_E4M3) && rows_aligned(g.y, g.ldy, g.y_dtype);
+  const RowThreads r = row_threads(g.d, 256);
+  const dim3 block(r.x, 256 / r.x);
+  int shift = 30;
+  if (g.group < g.d)
+    for (shift = 5; (1 << shift) < g.group;) ++shift;
   auto go = [&](auto kern, int u) {
     const int64_t rows = static_cast<int64_t>(u) * block.y;
-    const cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>((g.T + rows - 1) / rows), chunks), block, 0, s, g, qv, yv);
+    const cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>((g.T + rows - 1) / rows), r.chunks), block, 0, s, g, shift);
     if (e == cudaSuccess) count_launch();
     return e;
   };
-  const bool many = g.T * n >= 256 * 8 * 4 * sm_count();
-  if (g.y_dtype == P24_BF16) return many ? go(dequant8_kernel<bf16, 4>, 4) : go(dequant8_kernel<bf16, 1>, 1);
-  return many ? go(dequant8_kernel<float, 4>, 4) : go(dequant8_kernel<float, 1>, 1);
+  // 4 rows a thread where that leaves 8 CTAs for each SM
+  const bool many = vec && g.T * r.x * r.chunks >= 256 * 8 * 4 * sm_count();
+  if (g.y_dtype == P24_BF16)
+    return many ? go(dequant8_kernel<bf16, 4, true>, 4) : vec ? go(dequant8_kernel<bf16, 1, true>, 1) : go(dequant8_kernel<bf16, 1, false>, 1);
+  return many ? go(dequant8_kernel<float, 4, true>, 4) : vec ? go(dequant8_kernel<float, 1, true>, 1) : go(dequant8_kernel<float, 1, false>, 1);
 }
 
 }  // namespace p24

@@ -143,7 +143,8 @@ def test_binding_refuses_host_tensors(N):
 
 
 def test_binding_refuses_another_device(N, monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    N._here(torch.device("cuda", 0))
+    monkeypatch.setattr(N, "_current_device", lambda: 0)
+    monkeypatch.setattr(N, "_raw_stream", lambda i: 77)
+    assert N._here(torch.device("cuda", 0)) == 77
     with pytest.raises(ValueError, match="cuda:1"):
         N._here(torch.device("cuda", 1))
