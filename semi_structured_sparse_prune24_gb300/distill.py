@@ -6,7 +6,9 @@ tokens and their log probabilities, as p24_token_logprobs finds them. DistillHea
 holds the student's head (the unembedding): logits, loss and gradients, one pass
 over the logits and in place, so that one [M, V] buffer is all it needs.
 DistillStep runs a whole step of a student whose last layer is a 2:4 FFN: prune,
-forward, head, loss and backward, on the library's calls.
+forward, head, loss and backward, on the library's calls. StudentStep runs one from
+tokens to clipped gradients: embedding, a pre-norm 2:4 FFN with its residual, a norm
+in front of the head, and the backward of all of it.
 
 A call with stream=s is the call under torch.cuda.stream(s): what it allocates, intermediates that
 are dropped when it returns among them, is that stream's memory.
@@ -101,17 +103,75 @@ class DistillStep:
                                (W_head, (self.head.V, d), "W_head")):
             _shape(t, shape, name)
         with N._on(stream):
-            N.prune24_compress_both(W_up, self.up, self.up_T)
-            N.prune24_compress_both(W_down, self.down, self.down_T)
-            H = N.spmm24_fwd(X, self.up, b_up, relu=True)
-            Y = N.spmm24_fwd(H, self.down, b_down)
+            H, Y = self._forward(X, W_up, b_up, W_down, b_down)
             o = self.head.step(Y, W_head, top_idx, top_logp, dkl, labels, dce, temperature, tail)
             o["dW_head"] = o.pop("dW")
-            dY = o.pop("dY")
-            o["db_up"] = torch.empty(ffn, dtype=torch.float32, device=X.device)
-            dH = N.spmm24_bwd_dx(dY, self.down_T, gate=H, dbias=o["db_up"])
-            o["db_down"] = N.p24_colsum(dY)
-            o["dW_down"] = N.masked_dw_gemm(dY, H, self.down)
-            o["dX"] = N.spmm24_bwd_dx(dH, self.up_T)
-            o["dW_up"] = N.masked_dw_gemm(dH, X, self.up)
+            self._backward(o, o.pop("dY"), X, H)
         return o
+
+    def _forward(self, X, W_up, b_up, W_down, b_down):
+        N.prune24_compress_both(W_up, self.up, self.up_T)
+        N.prune24_compress_both(W_down, self.down, self.down_T)
+        H = N.spmm24_fwd(X, self.up, b_up, relu=True)
+        return H, N.spmm24_fwd(H, self.down, b_down)
+
+    def _backward(self, o: dict, dY, X, H) -> None:
+        """The FFN's gradients for that of its output, put into o."""
+        o["db_up"] = torch.empty(self.ffn, dtype=torch.float32, device=X.device)
+        dH = N.spmm24_bwd_dx(dY, self.down_T, gate=H, dbias=o["db_up"])
+        o["db_down"] = N.p24_colsum(dY)
+        o["dW_down"] = N.masked_dw_gemm(dY, H, self.down)
+        o["dX"] = N.spmm24_bwd_dx(dH, self.up_T)
+        o["dW_up"] = N.masked_dw_gemm(dH, X, self.up)
+
+
+class StudentStep:
+    """One training step of a student from its tokens, against a teacher's list:
+
+        x = scale E[tokens],  h = x + FFN(norm(x; w_in)),  logits = norm(h; w_out) W_head^T
+
+    with a 2:4 FFN as in DistillStep, and its gradients scaled to a norm of at most max_norm. Weights come in a dict
+    (bf16 E [V, d], W_up, W_down, W_head [V, d]; fp32 w_in, w_out [d], b_up, b_down), their gradients go out under
+    "d" + their names. Without a W_head the head's weights are E (tied), and E has both gradients."""
+
+    MATRICES = ("E", "W_up", "W_down", "W_head")
+
+    def __init__(self, M: int, d: int, ffn: int, V: int, scale: float = 1.0, eps: float = 1e-6, device="cuda"):
+        self.layer = DistillStep(M, d, ffn, V, device)
+        self.scale, self.eps = scale, eps
+
+    def run(self, tokens, weights: dict, top_idx, top_logp, dkl, labels=None, dce=None, temperature: float = 1.0,
+            tail: bool = True, max_norm: float | None = 1.0, stream=None) -> dict:
+        """Returns kl (and ce) per token, the gradients, and with max_norm their norm before they were scaled.
+        tokens: int32 [M]; one outside 0..V-1 is padding."""
+        w, head = weights, self.layer.head
+        M, d, ffn, V = head.M, head.d, self.layer.ffn, head.V
+        tied = w.get("W_head") is None
+        _shape(tokens, (M,), "tokens")
+        for name, shape in (("E", (V, d)), ("w_in", (d,)), ("W_up", (ffn, d)), ("b_up", (ffn,)), ("W_down", (d, ffn)),
+                            ("b_down", (d,)), ("w_out", (d,)), ("W_head", (V, d))):
+            _shape(w.get(name), shape, name)
+        with N._on(stream):
+            x = N.p24_embed(tokens, w["E"], self.scale)
+            a = N.p24_rmsnorm(x, w["w_in"], eps=self.eps)
+            H, Y = self.layer._forward(a["y"], w["W_up"], w.get("b_up"), w["W_down"], w.get("b_down"))
+            b = N.p24_rmsnorm(Y, w["w_out"], residual=x, eps=self.eps, out={"h": Y})
+            o = head.step(b["y"], w["E"] if tied else w["W_head"], top_idx, top_logp, dkl, labels, dce, temperature, tail)
+            back = N.p24_rmsnorm_bwd(o.pop("dY"), b["h"], w["w_out"], b["rstd"])
+            dh, o["dw_out"] = back["dx"], back["dweight"]
+            self.layer._backward(o, dh, a["y"], H)
+            back = N.p24_rmsnorm_bwd(o.pop("dX"), x, w["w_in"], a["rstd"], dres=dh, out={"dx": dh})
+            o["dw_in"] = back["dweight"]
+            dW = o.pop("dW")
+            if tied:
+                o["dE"] = N.p24_embed_bwd(back["dx"], tokens, V, self.scale, dW=dW, accumulate=True)
+            else:
+                o["dW_head"], o["dE"] = dW, N.p24_embed_bwd(back["dx"], tokens, V, self.scale)
+            if max_norm is not None:
+                o["norm"] = N.p24_clip_grads([o[k] for k in self.gradients(tied)], max_norm)
+        return o
+
+    @classmethod
+    def gradients(cls, tied: bool = False) -> list[str]:
+        """The names of run's gradients."""
+        return ["d" + n for n in cls.MATRICES if not (tied and n == "W_head")] + ["dw_in", "dw_out", "db_up", "db_down"]
