@@ -52,6 +52,7 @@ __global__ void __launch_bounds__(256) embed_kernel(const p24_embed_args g) {
 // ---------------------------------------------------------------- sort
 constexpr int kSortThreads = 1024, kSortWarps = 32, kDigit = 9, kBins = 1 << kDigit;
 constexpr int kSortCtas = 8;          // the portable cluster size
+constexpr int kHeld = 4;
 constexpr int kFillRows = 1 << 17;    // rows of the table that a CTA looks at together: a bit each
 
 struct SortShared {
@@ -70,7 +71,8 @@ __device__ __forceinline__ uint32_t load_cta(const uint32_t* p, int rank) {
   return v;
 }
 
-// (token, position), by token; a token outside 0..V-1 is V. `ctas`: those that sort, one cluster.
+// (token, position), by token; a token outside 0..V-1 is V. `ctas`: those that sort, one cluster, through a and b.
+// (16384 tokens over 5000: one CTA 46 us, a cluster of 8 14.)
 __device__ __forceinline__ void sort_tokens(const int32_t* tokens, int64_t T, int64_t V, int bits, int passes, int2* a, int2* b,
                                             int rank, int ctas, SortShared& sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -88,14 +90,26 @@ __device__ __forceinline__ void sort_tokens(const int32_t* tokens, int64_t T, in
       const int32_t v = tokens[i];
       return make_int2(v >= 0 && v < V ? v : static_cast<int>(V), static_cast<int>(i));
     };
+    int2 e[kHeld];  // some of a warp's elements, loaded together
+    auto load = [&](int64_t i0) {
+#pragma unroll
+      for (int u = 0; u < kHeld; ++u) {
+        const int64_t i = i0 + 32 * u + lane;
+        e[u] = i < hi ? key_of(i) : make_int2(-1, 0);
+      }
+    };
     for (int i = lane; i < bins; i += 32) sh.count[warp][i] = 0;
     __syncwarp();
-    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-      const int64_t i = i0 + lane;
-      const int digit = i < hi ? (key_of(i).x >> shift) & (bins - 1) : -1;
-      const unsigned peers = __match_any_sync(~0u, digit);
-      if (digit >= 0 && lane == __ffs(peers) - 1) sh.count[warp][digit] += __popc(peers);
-      __syncwarp();
+    for (int64_t i0 = lo; i0 < hi; i0 += 32 * kHeld) {
+      load(i0);
+#pragma unroll
+      for (int u = 0; u < kHeld; ++u) {
+        if (i0 + 32 * u >= hi) break;
+        const int digit = e[u].x < 0 ? -1 : (e[u].x >> shift) & (bins - 1);
+        const unsigned peers = __match_any_sync(~0u, digit);
+        if (digit >= 0 && lane == __ffs(peers) - 1) sh.count[warp][digit] += __popc(peers);
+        __syncwarp();
+      }
     }
     __syncthreads();
     uint32_t mine = 0;
@@ -134,19 +148,21 @@ __device__ __forceinline__ void sort_tokens(const int32_t* tokens, int64_t T, in
 #pragma unroll 8
       for (int w = 0; w < kSortWarps; ++w) sh.count[w][tid] += base;
     __syncthreads();
-    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-      const int64_t i = i0 + lane;
-      int2 e = make_int2(0, 0);
-      if (i < hi) e = key_of(i);
-      const int digit = i < hi ? (e.x >> shift) & (bins - 1) : -1;
-      const unsigned peers = __match_any_sync(~0u, digit);
-      const uint32_t at = digit >= 0 ? sh.count[warp][digit] : 0;
-      __syncwarp();
-      if (digit >= 0) {
-        if (lane == __ffs(peers) - 1) sh.count[warp][digit] = at + __popc(peers);
-        to[at + __popc(peers & ((1u << lane) - 1))] = e;
+    for (int64_t i0 = lo; i0 < hi; i0 += 32 * kHeld) {
+      if (span > 32 * kHeld) load(i0);  // else they are still here
+#pragma unroll
+      for (int u = 0; u < kHeld; ++u) {
+        if (i0 + 32 * u >= hi) break;
+        const int digit = e[u].x < 0 ? -1 : (e[u].x >> shift) & (bins - 1);
+        const unsigned peers = __match_any_sync(~0u, digit);
+        const uint32_t at = digit >= 0 ? sh.count[warp][digit] : 0;
+        __syncwarp();
+        if (digit >= 0) {
+          if (lane == __ffs(peers) - 1) sh.count[warp][digit] = at + __popc(peers);
+          to[at + __popc(peers & ((1u << lane) - 1))] = e[u];
+        }
+        __syncwarp();
       }
-      __syncwarp();
     }
     // the others' elements are there, and their totals read, before the next pass
     if (ctas > 1) cluster_barrier_all();
@@ -176,20 +192,22 @@ __device__ __forceinline__ void rank_tokens(const int32_t* tokens, int T, int64_
   to[place] = make_int2(mine, tid);
 }
 
-// `n` bytes of zeros, by a warp.
-__device__ __forceinline__ void zero_row(uint8_t* p, int64_t n, int unit) {
-  const int lane = threadIdx.x & 31;
+// `n` bytes of zeros, by `lanes` threads: what lies between 16-byte boundaries by bulk copies from `zeros` in shared memory
+// (16384 x 4096 over 131072, fp32: 385 us, with stores 398; 5000 x 5001 over 50257 205 and 227).
+constexpr int kZeros = 8192;
+__device__ __forceinline__ void zero_row(uint8_t* p, int64_t n, int unit, const uint8_t* zeros, int lane, int lanes) {
   const int64_t head = min(n, static_cast<int64_t>((16 - (reinterpret_cast<uintptr_t>(p) & 15u)) & 15u));
-  const int64_t vecs = (n - head) >> 4, tail = head + (vecs << 4);
+  const int64_t body = (n - head) & ~int64_t(15), tail = head + body;
   const int64_t ends = (head + n - tail) / unit;
-  if (lane < ends) {
-    const int64_t at = lane * unit < head ? lane * unit : tail + lane * unit - head;
+  for (int e = lane; e < ends; e += lanes) {
+    const int64_t at = e * unit < head ? e * unit : tail + e * unit - head;
     if (unit == 2) *reinterpret_cast<uint16_t*>(p + at) = 0;
     else *reinterpret_cast<uint32_t*>(p + at) = 0;
   }
-  uint4* q = reinterpret_cast<uint4*>(p + head);
-#pragma unroll 4
-  for (int64_t i = lane; i < vecs; i += 32) q[i] = make_uint4(0, 0, 0, 0);
+  for (int64_t i = static_cast<int64_t>(lane) * kZeros; i < body; i += static_cast<int64_t>(lanes) * kZeros)
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(p + head + i), "r"(smem_u32(zeros)),
+                 "r"(static_cast<uint32_t>(min(body - i, static_cast<int64_t>(kZeros))))
+                 : "memory");
 }
 
 // CTAs [0, ctas): the sort. The others: zeros for the table's rows without a token.
@@ -203,6 +221,9 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const p24_embe
     return;
   }
   uint32_t* used = reinterpret_cast<uint32_t*>(raw);
+  uint8_t* zeros = raw + kFillRows / 8;
+  for (int i = threadIdx.x; i < kZeros / 16; i += kSortThreads) reinterpret_cast<uint4*>(zeros)[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();  // the bulk copies read them; the barrier below comes before the first
   const int64_t fills = gridDim.x - ctas, f = blockIdx.x - ctas;
   const int64_t end = g.V * (f + 1) / fills;
   const int unit = g.dw_dtype == P24_BF16 ? 2 : 4;
@@ -217,10 +238,14 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const p24_embe
       if (v >= 0 && v < rows) atomicOr(&used[v >> 5], 1u << (v & 31));
     }
     __syncthreads();
-    for (int i = threadIdx.x >> 5; i < rows; i += kSortWarps)
+    // a warp a row, or a thread where that is one copy (8192 x 128 over 131072: 13 us against 21)
+    const bool alone = g.d * unit <= kZeros / 4;
+    const int lane = alone ? 0 : threadIdx.x & 31, lanes = alone ? 1 : 32;
+    for (int i = threadIdx.x / lanes; i < rows; i += kSortThreads / lanes)
       if (!(used[i >> 5] >> (i & 31) & 1))
-        zero_row(static_cast<uint8_t*>(g.dW) + (lo + i) * g.lddw * unit, g.d * unit, unit);
+        zero_row(static_cast<uint8_t*>(g.dW) + (lo + i) * g.lddw * unit, g.d * unit, unit, zeros, lane, lanes);
   }
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // ---------------------------------------------------------------- sums
@@ -424,17 +449,23 @@ cudaError_t launch_embed_bwd(const p24_embed_bwd_args& g, void* ws, cudaStream_t
   int total = 1;  // of the keys 0..V
   while (g.V >> total) ++total;
   const int passes = (total + kDigit - 1) / kDigit, bits = (total + passes - 1) / passes;
-  const int ctas = g.T <= 4096 ? 1 : kSortCtas;
+  // One CTA, or a cluster of 8: 1024 tokens 9 us and 12, 4096 17 and 12, 16384 46 and 14. But beside a cluster fewer
+  // CTAs fit to write the zeros, so where those take longer anyway one sorts: 16384 x 4096 over 131072, fp32, 398 us
+  // with the cluster, 372 without. (6 TB/s of zeros; 10 us and 2.4 ns a token.)
+  const double zeros_us = g.accumulate ? 0.0 : static_cast<double>(g.V) * g.d * size_of(g.dw_dtype) / 6e6;
+  const int ctas = g.T <= 1024 || 10.0 + 2.4e-3 * g.T < zeros_us ? 1 : kSortCtas;
   const void* kern = reinterpret_cast<const void*>(embed_sort_kernel);
   int slots = 0;
-  cudaError_t e = row_kernel_slots(kern, kSortThreads, ctas, sizeof(SortShared), &slots);
+  static_assert(sizeof(SortShared) % 16 == 0 && sizeof(SortShared) >= kFillRows / 8 + kZeros, "the fill's shared memory");
+  const size_t smem = sizeof(SortShared);
+  cudaError_t e = row_kernel_slots(kern, kSortThreads, ctas, smem, &slots);
   if (e != cudaSuccess) return e;
   // one cluster sorts; the others, as many as fit, write zeros
   const int64_t grid = (g.accumulate ? 1 : std::max<int64_t>(2, slots)) * ctas;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(kSortThreads);
-  cfg.dynamicSmemBytes = sizeof(SortShared);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
