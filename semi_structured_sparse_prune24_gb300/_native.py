@@ -8,11 +8,11 @@ if the shared library is missing, importing this module raises.
 """
 from __future__ import annotations
 
-import array
 import contextlib
 import ctypes as C
+import importlib.machinery
+import importlib.util
 import os
-import struct
 from dataclasses import dataclass
 
 import torch
@@ -154,13 +154,13 @@ def _load() -> C.CDLL:
         "p24_token_logprobs_bwd": (i32, [C.POINTER(p24_logprobs_args), vp]),
         "p24_distill_topk": (i32, [C.POINTER(p24_distill_args), vp]),
         "p24_distill_topk_bwd": (i32, [C.POINTER(p24_distill_args), vp]),
-        "p24_rmsnorm": (i32, [vp, vp]),
+        "p24_rmsnorm": (i32, [C.POINTER(p24_rmsnorm_args), vp]),
         "p24_rmsnorm_bwd_workspace_size": (sz, [i64, i64]),
-        "p24_rmsnorm_bwd": (i32, [vp, vp, sz, vp]),
-        "p24_dequant8": (i32, [vp, vp]),
-        "p24_embed": (i32, [vp, vp]),
+        "p24_rmsnorm_bwd": (i32, [C.POINTER(p24_rmsnorm_bwd_args), vp, sz, vp]),
+        "p24_dequant8": (i32, [C.POINTER(p24_dequant8_args), vp]),
+        "p24_embed": (i32, [C.POINTER(p24_embed_args), vp]),
         "p24_embed_bwd_workspace_size": (sz, [i64, i64]),
-        "p24_embed_bwd": (i32, [vp, vp, sz, vp]),
+        "p24_embed_bwd": (i32, [C.POINTER(p24_embed_bwd_args), vp, sz, vp]),
         "p24_grad_norm_workspace_size": (sz, [i64]),
         "p24_grad_norm": (i32, [vp, i64, vp, vp, sz, vp]),
         "p24_clip_grads": (i32, [vp, vp, i64, C.c_float, vp, vp, sz, vp]),
@@ -177,7 +177,19 @@ def _load() -> C.CDLL:
     return L
 
 
+def _load_marshal():
+    path = os.path.join(os.path.dirname(_LIB_PATH), "_p24_torch.so")
+    if not os.path.exists(path):
+        raise ImportError(f"the tensors' marshalling is not built ({path} missing): run __graft_entry__.build() "
+                          "or python semi_structured_sparse_prune24_gb300/build.py")
+    loader = importlib.machinery.ExtensionFileLoader("_p24_torch", path)
+    module = importlib.util.module_from_spec(importlib.machinery.ModuleSpec("_p24_torch", loader, origin=path))
+    loader.exec_module(module)
+    return module
+
+
 lib = _load()
+_marshal = _load_marshal()  # uses the library that has just been loaded
 
 
 def _check(code: int, where: str) -> None:
@@ -828,76 +840,8 @@ def p24_distill_topk_bwd(logits: torch.Tensor, top_idx: torch.Tensor, top_val: t
 
 
 # ------------------------------------------------------------------ around the sparse FFN: norm, embedding, gradient norm
-_NORM_TYPES = {**_LOGIT_TYPES, torch.float8_e4m3fn: P24_E4M3}
-
-
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-
-
-def _here(device) -> int:
-    """The stream a call launches on: the current device's current one. Its tensors have to be there."""
-    i = _current_device()
-    if device.index != i:
-        raise ValueError(f"the tensors are on {device}, the current device is cuda:{i}")
-    return _raw_stream(i) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
-
-
-def _packer(fields: str, args) -> "struct.Struct":
-    """Packs a call's arguments as the C structure `args` lies in memory: a third of the time that filling a
-    ctypes structure takes, 0.5 us of a call."""
-    s = struct.Struct(fields)
-    assert s.size == C.sizeof(args), args
-    return s
-
-
-_RMSNORM = _packer("qqiiiifiPqPqPPqPqPqP", p24_rmsnorm_args)
-_RMSNORM_BWD = _packer("qqiiiiiiPqPqPqPPPqP", p24_rmsnorm_bwd_args)
-_DEQUANT8 = _packer("qqiiPqPqPq", p24_dequant8_args)
-_EMBED = _packer("qqqiifPPqPq", p24_embed_args)
-_EMBED_BWD = _packer("qqqiifiPPqPq", p24_embed_bwd_args)
-
-
-def _rows(t: torch.Tensor, name: str, shape: tuple | None = None, device=None, types: dict = _LOGIT_TYPES) -> tuple[int, int, int]:
-    """(pointer, row stride, dtype code) of a [T, d] matrix with any row stride."""
-    code = types.get(t.dtype)
-    strides = t.stride()
-    if code is not None and len(strides) == 2 and strides[1] == 1 and t.is_cuda and (
-            shape is None or (t.shape == shape and t.device == device)):
-        ld, d = strides[0], t.shape[1]
-        return t.data_ptr(), ld if ld >= d else _row_stride(t), code
-    if code is None:
-        raise TypeError(f"{name} must be {' or '.join(str(k) for k in types)}, got {t.dtype}")
-    if len(strides) != 2 or not t.is_cuda or (strides[1] != 1 and t.shape[1] > 1):
-        _mat(t, t.dtype, name)  # says what is wrong
-        raise ValueError(f"{name} must be contiguous along its last dimension")
-    if shape is not None and (t.shape != shape or t.device != device):
-        raise ValueError(f"{name} must be a {tuple(shape)} tensor on {device}")
-    return t.data_ptr(), _row_stride(t), code
-
-
-def _row_stride(t: torch.Tensor) -> int:
-    """A matrix of one row, or of one column, may have any stride in torch."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
-
-
-def _vector(t: torch.Tensor | None, d: int, name: str, device) -> tuple[int, int]:
-    if t is None:
-        return 0, P24_F32
-    code = _LOGIT_TYPES.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
-    if t.shape != (d,) or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {(d,)} tensor on {device}")
-    return t.data_ptr(), code
-
-
-def _scratch(given: torch.Tensor | None, need: int, device) -> tuple[torch.Tensor, int, int]:
-    """A call's scratch: the caller's, or one that is the current stream's memory when it is dropped."""
-    if given is None:
-        given = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    elif given.device != device or not given.is_contiguous():
-        raise ValueError(f"the workspace must be a contiguous tensor on {device}")
-    return given, given.data_ptr(), given.numel() * given.element_size()
+# Their arguments are checked and marshalled by csrc/p24_torch.cpp, for a program makes many such calls on little data.
+_NONE: dict = {}
 
 
 def p24_rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torch.Tensor | None = None,
@@ -910,43 +854,15 @@ def p24_rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: t
     if stream is not None:
         with _on(stream):
             return p24_rmsnorm(x, weight, residual, eps, group, out)
-    px, ldx, tx = _rows(x, "x")
-    shape, dev = x.shape, x.device
-    at = _here(dev)
-    T, d = shape
-    o, given = {}, {} if out is None else out
-    y = given.get("y")
-    if y is None:
-        y = torch.empty(shape, dtype=x.dtype if group is None else torch.float8_e4m3fn, device=dev)
-    py, ldy, ty = _rows(y, "y", shape, dev, _NORM_TYPES)
-    if (group is None) != (ty != P24_E4M3):
-        raise TypeError(f"y is 8 bits with a group and is not without one: group={group}, y {y.dtype}")
-    o["y"] = y
-    pr = ph = ps = ldr = ldh = lds = 0
-    tr = tx
-    if residual is not None:
-        pr, ldr, tr = _rows(residual, "residual", shape, dev)
-        h = given.get("h")
-        if h is None:
-            h = torch.empty(shape, dtype=residual.dtype, device=dev)
-        ph, ldh, th = _rows(h, "h", shape, dev)
-        if th != tr:
-            raise TypeError("h must have the residual's type")
-        o["h"] = h
-    if group is not None:
-        groups = -(-d // group) if group > 0 else 1
-        scale = given.get("scale")
-        if scale is None:
-            scale = torch.empty((T, groups), dtype=torch.float32, device=dev)
-        ps, lds, ts = _rows(scale, "scale", (T, groups), dev)
-        if ts != P24_F32:
-            raise TypeError("scale must be torch.float32")
-        o["scale"] = scale
-    pw, tw = _vector(weight, d, "weight", dev)
-    rc = lib.p24_rmsnorm(_RMSNORM.pack(T, d, tx, tr, tw, ty, eps, group or 0, px, ldx, pr, ldr, pw, ph, ldh, py, ldy, ps, lds,
-                                       _out(o, given, "rstd", (T,), torch.float32, dev)), at)
+    get = _NONE.get if out is None else out.get
+    rc, y, h, scale, rstd = _marshal.rmsnorm(x, weight, residual, eps, group, get("y"), get("h"), get("scale"), get("rstd"))
     if rc:
         _check(rc, "p24_rmsnorm")
+    o = {"y": y, "rstd": rstd}
+    if h is not None:
+        o["h"] = h
+    if scale is not None:
+        o["scale"] = scale
     return o
 
 
@@ -960,28 +876,12 @@ def p24_rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor | No
     if stream is not None:
         with _on(stream):
             return p24_rmsnorm_bwd(dy, h, weight, rstd, dres, dweight, out, workspace)
-    ph, ldh, th = _rows(h, "h")
-    shape, dev = h.shape, h.device
-    at = _here(dev)
-    T, d = shape
-    pd, ldd, td = _rows(dy, "dy", shape, dev)
-    o, given = {}, {} if out is None else out
-    dx = given.get("dx")
-    if dx is None:
-        dx = torch.empty(shape, dtype=h.dtype, device=dev)
-    px, ldx, tx = _rows(dx, "dx", shape, dev)
-    o["dx"] = dx
-    pr, ldr, tr = (0, 0, tx) if dres is None else _rows(dres, "dres", shape, dev)
-    pw, tw = _vector(weight, d, "weight", dev)
-    pg, ws, n = 0, None, 0
-    if dweight or (dweight is None and weight is not None):
-        pg = _out(o, given, "dweight", (d,), torch.float32, dev)
-        workspace, ws, n = _scratch(workspace, lib.p24_rmsnorm_bwd_workspace_size(T, d), dev)
-    rc = lib.p24_rmsnorm_bwd(_RMSNORM_BWD.pack(T, d, th, td, tr, tx, tw, 0, ph, ldh, pd, ldd, pr, ldr, pw,
-                                               _per_row(rstd, (T,), torch.float32, "rstd", dev), px, ldx, pg), ws, n, at)
+    get = _NONE.get if out is None else out.get
+    wanted = weight is not None if dweight is None else dweight
+    rc, dx, dw = _marshal.rmsnorm_bwd(dy, h, weight, rstd, dres, get("dx"), get("dweight") if wanted else False, workspace)
     if rc:
         _check(rc, "p24_rmsnorm_bwd")
-    return o
+    return {"dx": dx, "dweight": dw} if wanted else {"dx": dx}
 
 
 def p24_dequant8(q: torch.Tensor, scale: torch.Tensor, group: int = 0, out: torch.Tensor | None = None,
@@ -990,17 +890,9 @@ def p24_dequant8(q: torch.Tensor, scale: torch.Tensor, group: int = 0, out: torc
     if stream is not None:
         with _on(stream):
             return p24_dequant8(q, scale, group, out)
-    pq, ldq, tq = _rows(q, "q", types=_NORM_TYPES)
-    if tq != P24_E4M3:
-        raise TypeError(f"q must be torch.float8_e4m3fn, got {q.dtype}")
-    (T, d), dev = q.shape, q.device
-    at = _here(dev)
-    out = torch.empty((T, d), dtype=torch.bfloat16, device=dev) if out is None else out
-    py, ldy, ty = _rows(out, "out", q.shape, dev)
-    ps, lds, ts = _rows(scale, "scale", (T, -(-d // group) if group > 0 else 1), dev)
-    if ts != P24_F32:
-        raise TypeError("scale must be torch.float32")
-    _check(lib.p24_dequant8(_DEQUANT8.pack(T, d, ty, group, pq, ldq, ps, lds, py, ldy), at), "p24_dequant8")
+    rc, out = _marshal.dequant8(q, scale, group, out)
+    if rc:
+        _check(rc, "p24_dequant8")
     return out
 
 
@@ -1011,16 +903,9 @@ def p24_embed(tokens: torch.Tensor, W: torch.Tensor, scale: float = 1.0, out: to
     if stream is not None:
         with _on(stream):
             return p24_embed(tokens, W, scale, out)
-    pw, ldw, tw = _rows(W, "W")
-    (V, d), dev = W.shape, W.device
-    at = _here(dev)
-    if tokens.dim() != 1:
-        raise ValueError("tokens must be 1-D")
-    T = tokens.shape[0]
-    pt = _per_row(tokens, (T,), torch.int32, "tokens", dev)
-    out = torch.empty((T, d), dtype=W.dtype, device=dev) if out is None else out
-    py, ldy, ty = _rows(out, "out", (T, d), dev)
-    _check(lib.p24_embed(_EMBED.pack(T, V, d, tw, ty, scale, pt, pw, ldw, py, ldy), at), "p24_embed")
+    rc, out = _marshal.embed(tokens, W, scale, out)
+    if rc:
+        _check(rc, "p24_embed")
     return out
 
 
@@ -1031,48 +916,10 @@ def p24_embed_bwd(dY: torch.Tensor, tokens: torch.Tensor, V: int, scale: float =
     if stream is not None:
         with _on(stream):
             return p24_embed_bwd(dY, tokens, V, scale, dW, accumulate, workspace)
-    py, ldy, ty = _rows(dY, "dY")
-    (T, d), dev = dY.shape, dY.device
-    at = _here(dev)
-    pt = _per_row(tokens, (T,), torch.int32, "tokens", dev)
-    if dW is None:
-        if accumulate:
-            raise ValueError("accumulate needs the dW to add to")
-        dW = torch.empty((V, d), dtype=dY.dtype, device=dev)
-    pw, ldw, tw = _rows(dW, "dW", (V, d), dev)
-    workspace, ws, n = _scratch(workspace, lib.p24_embed_bwd_workspace_size(T, d), dev)
-    a = _EMBED_BWD.pack(T, V, d, ty, tw, scale, 1 if accumulate else 0, pt, py, ldy, pw, ldw)
-    _check(lib.p24_embed_bwd(a, ws, n, at), "p24_embed_bwd")
+    rc, dW = _marshal.embed_bwd(dY, tokens, V, scale, dW, accumulate, workspace)
+    if rc:
+        _check(rc, "p24_embed_bwd")
     return dW
-
-
-def _tensor_list(ts, device, name: str) -> array.array:
-    """A list of tensors as p24_tensor[]."""
-    v, types, index = [], _LOGIT_TYPES, device.index
-    for t in ts:
-        code = types.get(t.dtype)
-        if code is None:
-            raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
-        if t.get_device() != index or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous tensors on {device}")
-        v += (t.data_ptr(), t.numel(), code)
-    return array.array("q", v)
-
-
-def _list_call(grads, norm, workspace):
-    if not grads:
-        raise ValueError("an empty list has no device to run on")
-    dev = grads[0].device
-    if dev.type != "cuda":
-        raise ValueError("the gradients must be CUDA tensors (libprune24 has no CPU path)")
-    at = _here(dev)
-    g = _tensor_list(grads, dev, "gradients")
-    if norm is None:
-        norm = torch.empty(1, dtype=torch.float32, device=dev)
-    elif norm.shape != (1,):
-        raise ValueError("norm must have one element")
-    pn = _per_row(norm, (1,), torch.float32, "norm", dev)
-    return at, g, norm, pn, _scratch(workspace, lib.p24_grad_norm_workspace_size(len(grads)), dev)
 
 
 def p24_grad_norm(grads, norm: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -1080,8 +927,9 @@ def p24_grad_norm(grads, norm: torch.Tensor | None = None, workspace: torch.Tens
     if stream is not None:
         with _on(stream):
             return p24_grad_norm(grads, norm, workspace)
-    at, g, norm, pn, (workspace, ws, n) = _list_call(grads, norm, workspace)
-    _check(lib.p24_grad_norm(g.buffer_info()[0], len(grads), pn, ws, n, at), "p24_grad_norm")
+    rc, norm = _marshal.grads(grads, None, None, norm, workspace)
+    if rc:
+        _check(rc, "p24_grad_norm")
     return norm
 
 
@@ -1092,12 +940,7 @@ def p24_clip_grads(grads, max_norm: float, out=None, norm: torch.Tensor | None =
     if stream is not None:
         with _on(stream):
             return p24_clip_grads(grads, max_norm, out, norm, workspace)
-    at, g, norm, pn, (workspace, ws, n) = _list_call(grads, norm, workspace)
-    to = None
-    if out is not None:
-        if len(out) != len(grads):
-            raise ValueError(f"{len(grads)} gradients, and {len(out)} tensors to write to")
-        o = _tensor_list(out, grads[0].device, "out")
-        to = o.buffer_info()[0]
-    _check(lib.p24_clip_grads(g.buffer_info()[0], to, len(grads), max_norm, pn, ws, n, at), "p24_clip_grads")
+    rc, norm = _marshal.grads(grads, out, max_norm, norm, workspace)
+    if rc:
+        _check(rc, "p24_clip_grads")
     return norm

@@ -2,15 +2,19 @@
 
 Each .cu under csrc/ is compiled in parallel to an object file under _build/,
 then all are linked into semi_structured_sparse_prune24_gb300/_lib/libprune24.so.
+csrc/p24_torch.cpp, the binding's marshalling of torch tensors, is compiled beside them
+(with torch's headers) and linked into _lib/_p24_torch.so, which uses libprune24.so.
 Nothing is installed outside the repository. Run: python semi_structured_sparse_prune24_gb300/build.py
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -23,6 +27,12 @@ LIB = os.path.join(LIBDIR, "libprune24.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--expt-relaxed-constexpr", f"-I{INCLUDE}", f"-I{CSRC}"]
+
+
+def _run(cmd: list[str], what: str) -> None:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what}:\n{r.stdout}\n{r.stderr}")
 
 
 def _nvcc() -> str:
@@ -43,10 +53,33 @@ def sources() -> list[str]:
 def _compile(nvcc: str, src: str) -> str:
     obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
     cmd = [nvcc, *ARCH, *NVCC_FLAGS, "-c", src, "-o", obj]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
+    _run(cmd, f"nvcc failed on {src}")
     return obj
+
+
+MARSHAL = os.path.join(LIBDIR, "_p24_torch.so")
+
+
+def _torch_dir() -> str:
+    return os.path.dirname(importlib.util.find_spec("torch").origin)  # without importing it
+
+
+def _compile_marshal(nvcc: str) -> str:
+    inc = os.path.join(_torch_dir(), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
+    obj = os.path.join(BUILD, "p24_torch.o")
+    _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++20", "-fPIC", "-D_GLIBCXX_USE_CXX11_ABI=1", f"-I{INCLUDE}", f"-I{inc}",
+          f"-I{os.path.join(inc, 'torch', 'csrc', 'api', 'include')}", f"-I{cuda}", f"-I{sysconfig.get_paths()['include']}",
+          "-c", os.path.join(CSRC, "p24_torch.cpp"), "-o", obj], "the host compiler failed on p24_torch.cpp")
+    return obj
+
+
+def _link_marshal(obj: str) -> None:
+    lib = os.path.join(_torch_dir(), "lib")
+    tmp = MARSHAL + ".tmp"
+    _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, f"-L{LIBDIR}", "-lprune24", f"-L{lib}", "-ltorch_python",
+          "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"], "link failed")
+    os.replace(tmp, MARSHAL)
 
 
 def build(verbose: bool = False) -> str:
@@ -55,16 +88,17 @@ def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        marshal = ex.submit(_compile_marshal, nvcc)
         objs = list(ex.map(lambda s: _compile(nvcc, s), srcs))
+        marshal = marshal.result()
     libdir = _cuda_lib_dir(nvcc)
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs,
-           f"-L{libdir}", "-Xlinker", f"-rpath={libdir}"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+           f"-L{libdir}", "-Xlinker", f"-rpath={libdir}", "-Xlinker", "-soname=libprune24.so"]
+    _run(cmd, "link failed")
     os.replace(tmp, LIB)
+    _link_marshal(marshal)
     if verbose:
         print(f"built {LIB}")
     return LIB

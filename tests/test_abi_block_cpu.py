@@ -142,9 +142,15 @@ def test_binding_refuses_host_tensors(N):
             call()
 
 
-def test_binding_refuses_another_device(N, monkeypatch):
-    monkeypatch.setattr(N, "_current_device", lambda: 0)
-    monkeypatch.setattr(N, "_raw_stream", lambda i: 77)
-    assert N._here(torch.device("cuda", 0)) == 77
-    with pytest.raises(ValueError, match="cuda:1"):
-        N._here(torch.device("cuda", 1))
+def test_binding_refuses_another_device(N):
+    assert N._marshal.require_device(0, 0) is None
+    with pytest.raises(ValueError, match="cuda:1, the current device is cuda:0"):
+        N._marshal.require_device(1, 0)
+
+
+def test_binding_refuses_what_is_no_tensor_or_number(N):
+    x = torch.zeros(2, 8)
+    for call in (lambda: N.p24_rmsnorm([1.0]), lambda: N.p24_grad_norm(3), lambda: N.p24_grad_norm([1, 2]),
+                 lambda: N.p24_embed(x, None), lambda: N._marshal.rmsnorm(x), lambda: N._marshal.grads()):
+        with pytest.raises(TypeError):
+            call()
