@@ -17,6 +17,7 @@
 // 65 more of 260 instructions a warp and piece, and in rows that start 16 bytes off a sector 1.6 times the L2
 // reads: the gradient of 16384 x 8191 252 us against 200.
 #include <algorithm>
+#include <type_traits>
 
 #include "stream_rows.cuh"
 
@@ -394,7 +395,7 @@ struct Reduce {
   }
 };
 
-template <bool kWarp, bool kAligned, bool kRing, int E, int C>
+template <bool kWarp, bool kAligned, bool kRing, int E, int C, bool kQuant>
 __global__ void __launch_bounds__(kWarp ? 256 : 1024, kWarp ? (C > 8 ? 3 : 4) : 1) rmsnorm_kernel(const p24_rmsnorm_args g, const Plan plan, int* status) {
   __shared__ float part[2][3][32];
   __shared__ Beside<2> beside[kWarp ? 8 : 1];
@@ -403,7 +404,7 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024, kWarp ? (C > 8 ? 3 : 4) : 
   const int lane = threadIdx.x & 31;
   const int per = kWarp ? blockDim.x >> 5 : 1, unit = kWarp ? threadIdx.x >> 5 : 0;
   const int64_t begin = static_cast<int64_t>(blockIdx.x) * per + unit, step = static_cast<int64_t>(gridDim.x) * per;
-  const bool quant = g.y_dtype == P24_E4M3, with_r = g.r != nullptr;
+  const bool with_r = g.r != nullptr;
   const Reduce<kWarp> reduce{part};
   Pieces<2, NV, E, kAligned, kRing> row;
   const Split<E, kAligned>& sp = row.sp;
@@ -416,7 +417,7 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024, kWarp ? (C > 8 ? 3 : 4) : 
   row.start(begin, kAligned ? 0 : plan.phase.of(begin), own);
   Weights<NV, E> w;
   float* tops = reinterpret_cast<float*>(own + plan.ring_bytes + (w.kHow == 1 ? sp.NT * C * 4 : 0));
-  const int groups = quant ? (sp.d + g.group - 1) / g.group : 0;
+  const int groups = kQuant ? (sp.d + g.group - 1) / g.group : 0;
   const int shift = groups > 1 ? 31 - __clz(g.group) : 30;  // several groups are of a power of two
   const Matrix h_out(g.h, g.ldh, g.r_dtype), y_out(g.y, g.ldy, g.y_dtype);
   const bool hv = sp.fits(h_out, begin), yv = sp.fits(y_out, begin);
@@ -494,7 +495,7 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024, kWarp ? (C > 8 ? 3 : 4) : 
 #pragma unroll
       for (int k = 0; k < E / 2; ++k) h[i].p[k] = h[i].p[k] * both(rstd) * wi.p[k];
     }
-    if (!quant) {
+    if (!kQuant) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if (sp.has(i)) store_vals<E>(y_out.row(t), E == 8 ? 0 : y_out.f32, sp.column(i), yv, h[i]);
@@ -731,47 +732,52 @@ __global__ void __launch_bounds__(1024) dweight_kernel(const float* parts, int G
   if (lane == 0 && blockIdx.x * 32 + warp < d) dw[blockIdx.x * 32 + warp] = s;
 }
 
-// Values of 8-bit codes. A CTA: blockDim.x threads with 8 columns each, blockDim.y rows, U of them for a thread.
-template <typename To, int U, bool kVec>
-__global__ void __launch_bounds__(256) dequant8_kernel(const p24_dequant8_args g, int shift) {
-  const Columns<kVec> k(blockIdx.y, threadIdx.x, blockDim.x, static_cast<int>(g.d));
+// Values of 8-bit codes. A CTA: blockDim.x threads with a piece of 8 columns each, blockDim.y rows, U of them for a
+// thread. Pieces lie on boundaries of 8 elements, in all rows alike, or row by row: then those at a row's ends are partly
+// outside it. Where the two matrices have no common boundaries they are moved element by element.
+enum Boundaries { kAlike, kByRow, kNone };
+template <typename To, int U, Boundaries kHow>
+__global__ void __launch_bounds__(256) dequant8_kernel(const p24_dequant8_args g, const Phase phase, int shift) {
+  const int d = static_cast<int>(g.d), piece = blockIdx.y * blockDim.x + threadIdx.x;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * U * blockDim.y + threadIdx.y;
   pdl_wait();
   pdl_trigger();
-  if (k.n == 0) return;
   uint2 b[U];
-  float sc[U][kVec ? 1 : 8];  // groups are multiples of 8 columns (shift: of how many), or the whole row
+  float sa[U], sb[U];  // a piece meets two groups at most, `cut` columns of it the first
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int64_t t = t0 + u * blockDim.y;
-    if (t >= g.T) break;
-    const uint8_t* q = static_cast<const uint8_t*>(g.q) + t * g.ldq + k.c;
-    const float* scale = g.scale + t * g.lds;
+    const int c = 8 * piece - (kHow == kByRow ? phase.of(t) : 0);
+    if (t >= g.T || c >= d) continue;
+    const uint8_t* q = static_cast<const uint8_t*>(g.q) + t * g.ldq + c;
     b[u] = make_uint2(0, 0);
-    if (kVec && k.n == 8) {
+    if (kHow != kNone && c >= 0 && c + 8 <= d) {
       b[u] = *reinterpret_cast<const uint2*>(q);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (i < k.n) (i < 4 ? b[u].x : b[u].y) |= static_cast<uint32_t>(q[i * k.step]) << (8 * (i & 3));
+        if (c + i >= 0 && c + i < d) (i < 4 ? b[u].x : b[u].y) |= static_cast<uint32_t>(q[i]) << (8 * (i & 3));
     }
-#pragma unroll
-    for (int i = 0; i < (kVec ? 1 : 8); ++i) sc[u][i] = i < k.n ? scale[(k.c + i * k.step) >> shift] : 0.f;
+    const float* scale = g.scale + t * g.lds;
+    sa[u] = scale[max(c, 0) >> shift];
+    sb[u] = kHow == kAlike ? sa[u] : scale[min(c + 7, d - 1) >> shift];
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int64_t t = t0 + u * blockDim.y;
-    if (t >= g.T) break;
+    const int c = 8 * piece - (kHow == kByRow ? phase.of(t) : 0);
+    if (t >= g.T || c >= d) continue;
+    const int cut = kHow == kAlike ? 8 : (((max(c, 0) >> shift) + 1) << shift) - c;
     float v[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const __half2_raw h =
           __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>((i < 2 ? b[u].x : b[u].y) >> (16 * (i & 1))), __NV_E4M3);
       const float2 f = __half22float2(__half2(h));
-      v[2 * i] = f.x * sc[u][kVec ? 0 : 2 * i];
-      v[2 * i + 1] = f.y * sc[u][kVec ? 0 : 2 * i + 1];
+      v[2 * i] = f.x * (2 * i < cut ? sa[u] : sb[u]);
+      v[2 * i + 1] = f.y * (2 * i + 1 < cut ? sa[u] : sb[u]);
     }
-    store_columns(static_cast<To*>(g.y) + t * g.ldy, k, v);
+    store8(static_cast<To*>(g.y) + t * g.ldy, c, d, kHow != kNone, v);
   }
 }
 
@@ -849,19 +855,23 @@ cudaError_t grid_of(K kern, const Shape& z, int64_t T, int64_t most, int64_t* gr
 }
 
 
-// Columns of a thread. 8, but 16 where CTAs of d / 8 threads leave an SM's 1024 a quarter empty or more (d = 5001:
-// one of 640): all bf16 8192 x 5001 60 us against 70, its gradient 71 against 81. With fp32 8 are faster there too.
-int columns_of(int d, int E, bool few) {
+// Columns of a thread. Of 8 a row of more than 4096 columns takes one CTA on an SM, of 16 two or more: those hide a
+// row's reduction behind each other, but have less of the ring. With one matrix to read 16 are faster (8192 rows of
+// 5001 bf16 35 us against 65, of 8192 43 against 54; the gradient without a skip connection's, of 6290, 70 against
+// 84), with a residual 8 are (16384 rows of 8192 166 against 176), unless they leave the SM a quarter empty (8192
+// rows of 5001: 60 against 70). In the gradient with fp32 8 always (8192 rows of 6290 125 against 172).
+int columns_of(int d, int E, bool residual, bool gradient, bool few) {
   if (d > 8192) return 16;
+  if (d <= 4096 || few || (E == 4 && (residual || gradient))) return 8;
   const int NT = (d + 255) / 256 * 32;
-  return E == 8 && !few && 1024 / NT * NT < 768 ? 16 : 8;
+  return !residual || 1024 / NT * NT < 768 ? 16 : 8;
 }
 
-template <bool kAligned, int E>
+template <bool kAligned, int E, bool kQuant>
 cudaError_t launch_norm(const p24_rmsnorm_args& g, Phase ph, bool ring, int* status, cudaStream_t s) {
   const int d = static_cast<int>(g.d);
   const int bytes = size_of(g.x_dtype) + (g.r ? size_of(g.r_dtype) : 0);
-  const size_t groups = g.y_dtype == P24_E4M3 ? (d + g.group - 1) / g.group : 0, own = (groups * sizeof(float) + 15) / 16 * 16;
+  const size_t groups = kQuant ? (d + g.group - 1) / g.group : 0, own = (groups * sizeof(float) + 15) / 16 * 16;
   auto go = [&](auto kern, const Shape& z) {
     int64_t grid = 0;
     cudaError_t e = grid_of(kern, z, g.T, INT64_MAX, &grid);
@@ -871,15 +881,15 @@ cudaError_t launch_norm(const p24_rmsnorm_args& g, Phase ph, bool ring, int* sta
     return e;
   };
   if (ring && d <= kWarpColumns) {
-    if (d <= 256) return go(rmsnorm_kernel<true, kAligned, true, E, 8>, ring_shape(d, 8, true, bytes, own, ph, 80 << 10));
-    return go(rmsnorm_kernel<true, kAligned, true, E, 16>, ring_shape(d, 16, true, bytes, own, ph, 80 << 10));
+    if (d <= 256) return go(rmsnorm_kernel<true, kAligned, true, E, 8, kQuant>, ring_shape(d, 8, true, bytes, own, ph, 80 << 10));
+    return go(rmsnorm_kernel<true, kAligned, true, E, 16, kQuant>, ring_shape(d, 16, true, bytes, own, ph, 80 << 10));
   }
   const bool few = g.T <= 2 * sm_count();
-  const int C = columns_of(d, E, few);
+  const int C = columns_of(d, E, g.r != nullptr, false, few);
   const Shape z = ring_shape(d, C, false, bytes, own, ph, 80 << 10);
   if (ring && d <= 16384 && z.plan.S > 0)
-    return C == 8 ? go(rmsnorm_kernel<false, kAligned, true, E, 8>, z) : go(rmsnorm_kernel<false, kAligned, true, E, 16>, z);
-  return go(rmsnorm_kernel<false, false, false, 4, 32>, direct_shape(d, 32, own, ph));
+    return C == 8 ? go(rmsnorm_kernel<false, kAligned, true, E, 8, kQuant>, z) : go(rmsnorm_kernel<false, kAligned, true, E, 16, kQuant>, z);
+  return go(rmsnorm_kernel<false, false, false, 4, 32, kQuant>, direct_shape(d, 32, own, ph));
 }
 
 // CTAs of the gradient, at most; each has a row of partial sums, and 8 rows or so of the batch for it.
@@ -901,7 +911,7 @@ cudaError_t launch_bwd(const p24_rmsnorm_bwd_args& g, Phase ph, bool ring, float
     return go(rmsnorm_bwd_kernel<true, kAligned, true, E, 16>, ring_shape(d, 16, true, bytes, 0, ph, 0));
   }
   const bool few = g.T <= 2 * sm_count();
-  const int C = columns_of(d, E, few);
+  const int C = columns_of(d, E, g.dres != nullptr, true, few);
   const Shape z = ring_shape(d, C, false, bytes, 0, ph, 0);
   if (ring && d <= 16384 && z.plan.S > 0)
     return C == 8 ? go(rmsnorm_bwd_kernel<false, kAligned, true, E, 8>, z) : go(rmsnorm_bwd_kernel<false, kAligned, true, E, 16>, z);
@@ -938,8 +948,12 @@ cudaError_t launch_rmsnorm(const p24_rmsnorm_args& a, int* status, cudaStream_t 
   if (!g.r) g.r_dtype = g.x_dtype, g.h = nullptr;
   if (g.y_dtype == P24_E4M3 && (g.group == 0 || g.group > g.d)) g.group = static_cast<int32_t>(g.d);
   const Layout l = layout_of({{g.x, g.ldx, g.x_dtype}, {g.r, g.ldr, g.r_dtype}, {g.h, g.ldh, g.r_dtype}, {g.y, g.ldy, g.y_dtype}}, 2, g.T, g.d, g.w);
-  if (l.wide) return l.aligned ? launch_norm<true, 8>(g, l.ph, l.ring, status, s) : launch_norm<false, 8>(g, l.ph, l.ring, status, s);
-  return l.aligned ? launch_norm<true, 4>(g, l.ph, l.ring, status, s) : launch_norm<false, 4>(g, l.ph, l.ring, status, s);
+  auto go = [&](auto quant) {
+    constexpr bool kQuant = decltype(quant)::value;
+    if (l.wide) return l.aligned ? launch_norm<true, 8, kQuant>(g, l.ph, l.ring, status, s) : launch_norm<false, 8, kQuant>(g, l.ph, l.ring, status, s);
+    return l.aligned ? launch_norm<true, 4, kQuant>(g, l.ph, l.ring, status, s) : launch_norm<false, 4, kQuant>(g, l.ph, l.ring, status, s);
+  };
+  return g.y_dtype == P24_E4M3 ? go(std::true_type()) : go(std::false_type());
 }
 
 cudaError_t launch_rmsnorm_bwd(const p24_rmsnorm_bwd_args& g, float* parts, int* status, cudaStream_t s) {
@@ -959,23 +973,30 @@ cudaError_t launch_rmsnorm_bwd(const p24_rmsnorm_bwd_args& g, float* parts, int*
 cudaError_t launch_dequant8(const p24_dequant8_args& a, cudaStream_t s) {
   p24_dequant8_args g = a;
   if (g.group == 0 || g.group > g.d) g.group = static_cast<int32_t>(g.d);
-  const bool vec = rows_aligned(g.q, g.ldq, P24_E4M3) && rows_aligned(g.y, g.ldy, g.y_dtype);
-  const RowThreads r = row_threads(g.d, 256);
+  const Lead q{g.q, g.ldq, P24_E4M3}, y{g.y, g.ldy, g.y_dtype};
+  Phase ph = phase_of({q});
+  if (g.T == 1) ph.step = 0;
+  const bool phased = in_phase(q, g.T, ph) && in_phase(y, g.T, ph), odd = phased && (ph.first != 0 || ph.step != 0);
+  const RowThreads r = row_threads(g.d + (odd ? 7 : 0), 256);
   const dim3 block(r.x, 256 / r.x);
-  int shift = 30;
+  int shift = 30;  // one group
   if (g.group < g.d)
     for (shift = 5; (1 << shift) < g.group;) ++shift;
   auto go = [&](auto kern, int u) {
     const int64_t rows = static_cast<int64_t>(u) * block.y;
-    const cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>((g.T + rows - 1) / rows), r.chunks), block, 0, s, g, shift);
+    const cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>((g.T + rows - 1) / rows), r.chunks), block, 0, s, g, ph, shift);
     if (e == cudaSuccess) count_launch();
     return e;
   };
   // 4 rows a thread where that leaves 8 CTAs for each SM
-  const bool many = vec && g.T * r.x * r.chunks >= 256 * 8 * 4 * sm_count();
-  if (g.y_dtype == P24_BF16)
-    return many ? go(dequant8_kernel<bf16, 4, true>, 4) : vec ? go(dequant8_kernel<bf16, 1, true>, 1) : go(dequant8_kernel<bf16, 1, false>, 1);
-  return many ? go(dequant8_kernel<float, 4, true>, 4) : vec ? go(dequant8_kernel<float, 1, true>, 1) : go(dequant8_kernel<float, 1, false>, 1);
+  const bool many = g.T * r.x * r.chunks >= 256 * 8 * 4 * sm_count();
+  auto how = [&](auto type) {
+    using To = decltype(type);
+    if (!phased) return go(dequant8_kernel<To, 1, kNone>, 1);
+    if (odd) return many ? go(dequant8_kernel<To, 4, kByRow>, 4) : go(dequant8_kernel<To, 1, kByRow>, 1);
+    return many ? go(dequant8_kernel<To, 4, kAlike>, 4) : go(dequant8_kernel<To, 1, kAlike>, 1);
+  };
+  return g.y_dtype == P24_BF16 ? how(bf16()) : how(float());
 }
 
 }  // namespace p24
