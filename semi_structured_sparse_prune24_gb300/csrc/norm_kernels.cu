@@ -892,15 +892,19 @@ cudaError_t launch_norm(const p24_rmsnorm_args& g, Phase ph, bool ring, int* sta
   return go(rmsnorm_kernel<false, false, false, 4, 32, kQuant>, direct_shape(d, 32, own, ph));
 }
 
-// CTAs of the gradient, at most; each has a row of partial sums, and 8 rows or so of the batch for it.
-int64_t bwd_ctas(int64_t T) { return std::min<int64_t>(T, std::max<int64_t>(2 * sm_count(), std::min<int64_t>(16 * sm_count(), T / 8))); }
+// CTAs of the gradient, at most: 8 rows or so of the batch for each, and a multiple of 8 (as units are). Each of them has
+// a row of partial sums, and one row of the batch at least.
+int64_t bwd_ctas(int64_t T) {
+  const int64_t n = std::max<int64_t>(2 * sm_count(), std::min<int64_t>(16 * sm_count(), T / 8));
+  return (n + 7) / 8 * 8;
+}
 
 template <bool kAligned, int E>
 cudaError_t launch_bwd(const p24_rmsnorm_bwd_args& g, Phase ph, bool ring, float* parts, int* status, cudaStream_t s, int64_t* used) {
   const int d = static_cast<int>(g.d);
   const int bytes = size_of(g.h_dtype) + size_of(g.dy_dtype) + (g.dres ? size_of(g.r_dtype) : 0);
   auto go = [&](auto kern, const Shape& z) {
-    cudaError_t e = grid_of(kern, z, g.T, bwd_ctas(g.T) + 7, used);
+    cudaError_t e = grid_of(kern, z, g.T, bwd_ctas(g.T), used);
     if (e != cudaSuccess) return e;
     e = launch_pdl(kern, dim3(static_cast<unsigned>(*used)), dim3(z.NT), z.smem, s, g, z.plan, parts, status);
     if (e == cudaSuccess) count_launch();
@@ -941,7 +945,7 @@ Layout layout_of(std::initializer_list<Lead> all, size_t n, int64_t T, int64_t d
 
 }  // namespace
 
-int64_t rmsnorm_bwd_parts(int64_t T, int64_t d) { return bwd_ctas(T) * d; }
+int64_t rmsnorm_bwd_parts(int64_t T, int64_t d) { return std::min(T, bwd_ctas(T)) * d; }
 
 cudaError_t launch_rmsnorm(const p24_rmsnorm_args& a, int* status, cudaStream_t s) {
   p24_rmsnorm_args g = a;

@@ -176,3 +176,19 @@ def test_a_gradient_beyond_32_bits(P):
     for x, v in ((t[:1000], 0.5), (t[n // 2: n // 2 + 1000], 0.5), (t[-1000:-1], 0.5), (t[-1:], 3.0), (small, 2.0)):
         e = half(x.dtype)
         assert bool(((x.double() - v * f).abs() <= (73 * U + e) * v * f).all())
+
+
+@pytest.mark.parametrize("T", [300, 2441, 3001, 4000, 5003, 9725, 20001])
+@pytest.mark.parametrize("d", [40, 300, 520, 1000, 4096])
+def test_the_gradient_stays_in_its_scratch(P, T, d):
+    """Partial sums of the weight's gradient are as many as the scratch was sized for, for every number of CTAs."""
+    from semi_structured_sparse_prune24_gb300 import _native as N
+    g = torch.Generator(device="cuda").manual_seed(T)
+    h, dy = matrix(T, d, BF, g), matrix(T, d, BF, g)
+    need, behind = N.lib.p24_rmsnorm_bwd_workspace_size(T, d), 16 * d * 4
+    ws = torch.full((need + behind,), 90, dtype=torch.uint8, device="cuda")
+    rstd = 1 / (h.double().square().mean(1) + 1e-6).sqrt()
+    o = P.p24_rmsnorm_bwd(dy, h, torch.ones(d, device="cuda"), rstd.float(), workspace=ws[:need])
+    assert bool((ws[need:] == 90).all())
+    xh = h.double() * rstd[:, None]
+    check(T, o["dweight"], (dy.double() * xh).sum(0), (T / 152 + 150) * U * (dy.double() * xh).abs().sum(0), "dweight")
