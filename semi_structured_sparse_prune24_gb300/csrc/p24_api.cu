@@ -138,7 +138,7 @@ cudaError_t row_kernel_slots(const void* kern, int NT, int ranks, size_t smem, i
   struct Known {
     const void* kern;
     size_t smem;
-    int dev, ranks, slots;
+    int dev, NT, ranks, slots;
   };
   constexpr int kKnown = 256;  // more than that are looked up every time
   static std::mutex lock;
@@ -149,7 +149,7 @@ cudaError_t row_kernel_slots(const void* kern, int NT, int ranks, size_t smem, i
   if (e != cudaSuccess) return e;
   const std::lock_guard<std::mutex> hold(lock);
   for (int i = 0; i < n; ++i)
-    if (known[i].kern == kern && known[i].ranks == ranks && known[i].smem == smem && known[i].dev == dev) {
+    if (known[i].kern == kern && known[i].NT == NT && known[i].ranks == ranks && known[i].smem == smem && known[i].dev == dev) {
       *slots = known[i].slots;
       return cudaSuccess;
     }
@@ -179,7 +179,7 @@ cudaError_t row_kernel_slots(const void* kern, int NT, int ranks, size_t smem, i
   }
   if (e != cudaSuccess) return e;
   if (found < 1) return cudaErrorInvalidConfiguration;
-  if (n < kKnown) known[n++] = Known{kern, smem, dev, ranks, found};
+  if (n < kKnown) known[n++] = Known{kern, smem, dev, NT, ranks, found};
   *slots = found;
   return cudaSuccess;
 }
