@@ -642,10 +642,11 @@ int p24_distill_topk_bwd(const p24_distill_args* a, void* stream);
  * What a pre-norm block and a training step have around the sparse FFN: the norm in front of
  * it with the residual's addition, the embedding, and the norm over all gradients. Matrices are
  * bf16 or fp32 as their dtype says, with any row stride that is at least the row and any
- * alignment that is a multiple of the element; rows whose pieces of 8 columns lie on 16-byte
- * boundaries (in a call: of all its tensors alike) move 16 bytes at a time, others in elements. Sums and statistics
- * are fp32 or wider and are added in a fixed order: repeated calls are bit-identical. Inputs and
- * outputs overlap only where a call says so.
+ * alignment that is a multiple of the element. Fastest are matrices whose rows all start on 16-byte
+ * boundaries, then those of a call whose rows start equally far from a boundary of 8 elements.
+ * Sums and statistics are fp32 or wider and are added in a fixed order: repeated calls are
+ * bit-identical. Inputs and outputs overlap only where a call says so. As above, the first call of its
+ * kind belongs before a stream capture.
  *
  * p24_rmsnorm -- root-mean-square norm of each row, after the residual's addition:
  *   h = x + r, rounded to r's type, where there is a residual (else h is x)
@@ -769,12 +770,13 @@ int p24_embed_bwd(const p24_embed_bwd_args* a, void* ws, size_t ws_bytes, void* 
 
 /*
  * p24_grad_norm -- the norm over n tensors (contiguous, bf16 or fp32, any sizes, aligned to their
- * element; an empty one counts nothing): norm[0] = sqrt(sum of g^2), fp32. Sums are fp64 over
- * threads' fp32 sums of a few dozen elements, so that neither their number nor their size costs digits.
+ * element; an empty one counts nothing): norm[0] = sqrt(sum of g^2), fp32. Threads' fp32 sums of a few dozen
+ * elements are added as pairs of fp32 numbers, and those outside 2^-100 .. 2^88 in fp64, so that neither the
+ * elements' number nor their size costs digits.
  *
  * p24_clip_grads -- the same, and g * min(1, max_norm / norm) goes to `out` (n tensors of the same
  * sizes and types; each is the input itself or does not overlap any input), or with out = NULL to the
- * gradients themselves. Where the norm is not finite the gradients stay as they are (out: a copy);
+ * gradients themselves. No two tensors that are written overlap. Where the norm is not finite the gradients stay as they are (out: a copy);
  * the norm says so. norm may be NULL. max_norm > 0 and finite.
  *
  * The list `g` is a host array and is read before the call returns. ws: device scratch of

@@ -936,11 +936,12 @@ def p24_grad_norm(grads, norm: torch.Tensor | None = None, workspace: torch.Tens
 def p24_clip_grads(grads, max_norm: float, out=None, norm: torch.Tensor | None = None,
                    workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Scales a list of gradients to a norm of at most max_norm, in place or into the tensors of `out` (same sizes and
-    types), and returns the norm they had (fp32 [1]). Where it is not finite they stay as they are."""
+    types), and returns the norm they had (fp32 [1]). Where it is not finite they stay as they are. A tensor that is
+    written overlaps no other of the lists and is listed once."""
     if stream is not None:
         with _on(stream):
             return p24_clip_grads(grads, max_norm, out, norm, workspace)
-    rc, norm = _marshal.grads(grads, out, max_norm, norm, workspace)
+    rc, norm = _marshal.grads(grads, out, float(max_norm), norm, workspace)
     if rc:
         _check(rc, "p24_clip_grads")
     return norm

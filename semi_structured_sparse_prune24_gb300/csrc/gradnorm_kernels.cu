@@ -7,7 +7,7 @@
 // neighbouring ones each read as fast, but scaled 743 MB in 246 us instead of 226). A thread
 // squares and adds the elements of a chunk in fp32, and chunks, threads and CTAs are added as pairs of fp32 numbers,
 // a sum and what its rounding left (Knuth's two-sum): the number of elements costs no digits. Chunks whose sum
-// lies outside 2^-100 .. 2^100 are squared and added again in fp64, so neither does their size. (All of it in
+// lies outside 2^-100 .. 2^88 (2^38 such sums still fit fp32) are squared and added again in fp64, so neither does their size. (All of it in
 // fp64 beyond the chunks took 45 us for 72 tensors of 4.8 MB: an SM adds two a clock.) Every sum has a fixed
 // order. The scaling pass goes through the chunks from the end, where the first
 // pass left off: what is in L2 still is read from there.
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) grad_squares_kernel(const __g
       for (int k = 0; k < 8; k += 2) s0 = fmaf(v[k], v[k], s0), s1 = fmaf(v[k + 1], v[k + 1], s1);
     }
     const float s = s0 + s1;
-    if (s >= 0x1p-100f && s <= 0x1p100f) {
+    if (s >= 0x1p-100f && s <= 0x1p88f) {
       total.in = add(total.in, Pair{s, 0.f});
       continue;
     }

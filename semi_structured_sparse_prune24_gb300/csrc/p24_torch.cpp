@@ -12,6 +12,9 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <torch/csrc/Exceptions.h>
+
+#include <algorithm>
 #include <string>
 #include <vector>
 
@@ -158,8 +161,8 @@ PyObject* call(const char* name, Py_ssize_t given, Py_ssize_t n, F&& f) {
     return f();
   } catch (const Refused& r) {
     PyErr_SetString(r.type, r.what.c_str());
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {  // torch's own, memory that is not there among them
+    torch::translate_exception_to_python(std::current_exception());
   }
   return nullptr;
 }
@@ -323,7 +326,8 @@ PyObject* py_embed_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// A sequence of tensors as p24_tensor[]; holds a reference to it meanwhile.
+// A sequence of tensors as p24_tensor[]; holds a reference to it meanwhile. Elements are taken in the order of memory, so
+// any tensor without holes will do.
 struct List {
   PyObject* seq;
   std::vector<p24_tensor> v;
@@ -345,8 +349,8 @@ struct List {
           device = cuda_index(t);
           if (device < 0) refuse_value(std::string(name) + " must be CUDA tensors (libprune24 has no CPU path)");
         }
-        if (cuda_index(t) != device || !t.is_contiguous())
-          refuse_value(std::string(name) + " must be contiguous tensors on " + device_name(device));
+        if (cuda_index(t) != device || !t.is_non_overlapping_and_dense())
+          refuse_value(std::string(name) + " must be dense tensors on " + device_name(device));
         v.push_back(p24_tensor{const_cast<void*>(t.const_data_ptr()), t.numel(), code});
       }
     } catch (...) {
@@ -356,7 +360,34 @@ struct List {
   }
   ~List() { Py_DECREF(seq); }
   List(const List&) = delete;
+  const at::Tensor& at(size_t i) const { return THPVariable_Unpack(PySequence_Fast_GET_ITEM(seq, static_cast<Py_ssize_t>(i))); }
 };
+
+// Tensors that are scaled overlap no others: one that is listed twice would be scaled twice, or while it is read.
+void require_apart(const std::vector<p24_tensor>& g, const std::vector<p24_tensor>& to) {
+  struct Range {
+    uintptr_t begin, end;
+    bool written;
+  };
+  std::vector<Range> all;
+  all.reserve(2 * g.size());
+  auto add = [&](const p24_tensor& t, bool written) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(t.p);
+    if (t.n > 0) all.push_back(Range{p, p + static_cast<uintptr_t>(t.n) * (t.dtype == P24_BF16 ? 2 : 4), written});
+  };
+  for (size_t i = 0; i < g.size(); ++i) {
+    add(to[i], true);
+    if (to[i].p != g[i].p) add(g[i], false);
+  }
+  auto before = [](const Range& a, const Range& b) { return a.begin < b.begin; };
+  if (!std::is_sorted(all.begin(), all.end(), before)) std::sort(all.begin(), all.end(), before);
+  uintptr_t written = 0, any = 0;
+  for (const Range& r : all) {
+    if (r.begin < (r.written ? any : written)) refuse_value("tensors that are scaled must not overlap others, nor be listed twice");
+    any = std::max(any, r.end);
+    if (r.written) written = std::max(written, r.end);
+  }
+}
 
 // (gradients, out or None, max_norm or None for the norm alone, norm, workspace) -> (status, norm)
 PyObject* py_grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -372,12 +403,18 @@ PyObject* py_grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (a[2] == Py_None) {
       rc = p24_grad_norm(g.v.data(), count, pn, ws.p, ws.bytes, stream);
     } else if (a[1] == Py_None) {
+      require_apart(g.v, g.v);
       rc = p24_clip_grads(g.v.data(), nullptr, count, number(a[2], "max_norm"), pn, ws.p, ws.bytes, stream);
     } else {
       const List out(a[1], "out");
       if (out.v.size() != g.v.size())
         refuse_value(std::to_string(count) + " gradients, and " + std::to_string(out.v.size()) + " tensors to write to");
-      if (out.device != g.device) refuse_value("out must be contiguous tensors on " + device_name(g.device));
+      if (out.device != g.device) refuse_value("out must be dense tensors on " + device_name(g.device));
+      for (size_t i = 0; i < g.v.size(); ++i)
+        if (out.v[i].n == g.v[i].n && !(out.at(i).is_contiguous() && g.at(i).is_contiguous()) &&
+            (out.at(i).sizes() != g.at(i).sizes() || out.at(i).strides() != g.at(i).strides()))
+          refuse_value("out must have the gradients' strides");
+      require_apart(g.v, out.v);
       rc = p24_clip_grads(g.v.data(), out.v.data(), count, number(a[2], "max_norm"), pn, ws.p, ws.bytes, stream);
     }
     return built(rc, {result(a[3], norm)});

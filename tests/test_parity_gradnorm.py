@@ -1,7 +1,7 @@
 """GPU parity of p24_grad_norm and p24_clip_grads against the fp64 oracle (oracle/block_oracle.py).
 
 Tolerances, u = 2^-24: a thread adds the squares of at most 128 elements in fp32 (130u relative on a sum of positive
-terms), the rest is fp64; on the norm half of it, and its rounding: 70u. A scaled gradient: 70u, the quotient,
+terms), the rest is pairs of fp32 numbers or fp64 (less than u in all); on the norm half of it, and its rounding: 70u. A scaled gradient: 70u, the quotient,
 the product, and the output's rounding: (73u + half a step) |g|."""
 import numpy as np
 import pytest
@@ -162,3 +162,45 @@ def test_refusals_of_the_binding(P):
                       (lambda: P.p24_grad_norm(g, workspace=torch.empty(8, dtype=torch.uint8, device="cuda")), P.P24Error)):
         with pytest.raises(err):
             call()
+
+
+def test_a_tensor_listed_twice(P):
+    """Counted twice by the norm; refused where it would be scaled twice, or written while it is read."""
+    buf = torch.ones(64, device="cuda")
+    a, b, c = buf[:32], buf[32:], torch.ones(32, device="cuda")
+    assert float(P.p24_grad_norm([a, b, a])) == 96 ** 0.5
+    for grads, out in (([a, b, a], None), ([b, buf[31:33]], None), ([a, c], [c, b]), ([a, b], [c, c]), ([a], [buf[1:33]])):
+        with pytest.raises(ValueError, match="overlap"):
+            P.p24_clip_grads(grads, 1.0, out=out)
+    assert bool((buf == 1).all()) and bool((c == 1).all())
+    n = P.p24_clip_grads([a, b, torch.empty(0, device="cuda"), buf[:0]], 1.0)     # neighbours and empty ones are apart
+    assert float(n) == 8.0 and bool((buf == 0.125).all())
+    n = P.p24_clip_grads([a, a], 1.0, out=[c, torch.empty_like(c)])               # read twice
+    assert float(n) == 1.0
+
+
+def test_dense_tensors_in_another_order(P):
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn((33, 70), generator=g, device="cuda")
+    want = P.p24_grad_norm([x])
+    assert torch.equal(P.p24_grad_norm([x.t()]), want)
+    o = torch.empty((33, 70), device="cuda").t()
+    P.p24_clip_grads([x.t()], 1.0, out=[o])
+    y = x.clone()
+    P.p24_clip_grads([y], 1.0)
+    assert torch.equal(o, y.t())
+    for bad in (x[:, :69], x[::2], x.expand(2, 33, 70)):
+        with pytest.raises(ValueError):
+            P.p24_grad_norm([bad])
+    with pytest.raises(ValueError, match="strides"):
+        P.p24_clip_grads([x.t()], 1.0, out=[torch.empty((70, 33), device="cuda")])
+    with pytest.raises(TypeError):
+        P.p24_clip_grads([x], None)
+
+
+@pytest.mark.parametrize("e", [40, 47])
+def test_many_sums_at_the_upper_end(P, e):
+    """2^34 elements of 2^e (a tensor of 2 GB listed 16 times): the sum of squares passes fp32's range for e = 47. Powers
+    of two, so every sum is exact."""
+    x = torch.full((1 << 30,), 2.0 ** e, dtype=BF, device="cuda")
+    assert float(P.p24_grad_norm([x] * 16)) == 2.0 ** (e + 17)
