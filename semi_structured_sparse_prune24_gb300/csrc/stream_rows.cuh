@@ -104,12 +104,6 @@ __device__ __forceinline__ void put(Raw8<float>& r, int i, float x) {
     if (k == i) w[k] = __float_as_uint(x);
 }
 
-// Whether the pieces of a row of phase s lie on 16-byte boundaries in this tensor.
-template <typename T>
-__device__ __forceinline__ bool pieces_aligned(const T* row, int s) {
-  return (reinterpret_cast<uintptr_t>(row + (8 - s)) & 15u) == 0;
-}
-
 // Columns [c, c + 8) of a row of d columns; those outside it are 0. `vec`: the row's pieces are aligned.
 template <typename T>
 __device__ __forceinline__ Raw8<T> load8(const T* row, int c, int d, bool vec) {

@@ -132,9 +132,11 @@ class StudentStep:
 
     with a 2:4 FFN as in DistillStep, and its gradients scaled to a norm of at most max_norm. Weights come in a dict
     (bf16 E [V, d], W_up, W_down, W_head [V, d]; fp32 w_in, w_out [d], b_up, b_down), their gradients go out under
-    "d" + their names. Without a W_head the head's weights are E (tied), and E has both gradients."""
+    "d" + their names. Without a W_head the head's weights are E (tied), and E has both gradients; norms and biases
+    that are None or not there are left out, and have no gradient."""
 
     MATRICES = ("E", "W_up", "W_down", "W_head")
+    VECTORS = ("w_in", "w_out", "b_up", "b_down")
 
     def __init__(self, M: int, d: int, ffn: int, V: int, scale: float = 1.0, eps: float = 1e-6, device="cuda"):
         self.layer = DistillStep(M, d, ffn, V, device)
@@ -151,6 +153,9 @@ class StudentStep:
         for name, shape in (("E", (V, d)), ("w_in", (d,)), ("W_up", (ffn, d)), ("b_up", (ffn,)), ("W_down", (d, ffn)),
                             ("b_down", (d,)), ("w_out", (d,)), ("W_head", (V, d))):
             _shape(w.get(name), shape, name)
+        for name in self.MATRICES[:3]:
+            if w.get(name) is None:
+                raise ValueError(f"a step needs {name}")
         with N._on(stream):
             x = N.p24_embed(tokens, w["E"], self.scale)
             a = N.p24_rmsnorm(x, w["w_in"], eps=self.eps)
@@ -158,20 +163,23 @@ class StudentStep:
             b = N.p24_rmsnorm(Y, w["w_out"], residual=x, eps=self.eps, out={"h": Y})
             o = head.step(b["y"], w["E"] if tied else w["W_head"], top_idx, top_logp, dkl, labels, dce, temperature, tail)
             back = N.p24_rmsnorm_bwd(o.pop("dY"), b["h"], w["w_out"], b["rstd"])
-            dh, o["dw_out"] = back["dx"], back["dweight"]
+            dh, o["dw_out"] = back["dx"], back.get("dweight")
             self.layer._backward(o, dh, a["y"], H)
             back = N.p24_rmsnorm_bwd(o.pop("dX"), x, w["w_in"], a["rstd"], dres=dh, out={"dx": dh})
-            o["dw_in"] = back["dweight"]
+            o["dw_in"] = back.get("dweight")
+            for name in self.VECTORS:
+                if w.get(name) is None:
+                    o.pop("d" + name)
             dW = o.pop("dW")
             if tied:
                 o["dE"] = N.p24_embed_bwd(back["dx"], tokens, V, self.scale, dW=dW, accumulate=True)
             else:
                 o["dW_head"], o["dE"] = dW, N.p24_embed_bwd(back["dx"], tokens, V, self.scale)
             if max_norm is not None:
-                o["norm"] = N.p24_clip_grads([o[k] for k in self.gradients(tied)], max_norm)
+                o["norm"] = N.p24_clip_grads([o[k] for k in self.gradients(tied) if k in o], max_norm)
         return o
 
     @classmethod
     def gradients(cls, tied: bool = False) -> list[str]:
-        """The names of run's gradients."""
-        return ["d" + n for n in cls.MATRICES if not (tied and n == "W_head")] + ["dw_in", "dw_out", "db_up", "db_down"]
+        """The names of run's gradients, where every norm and bias has weights."""
+        return ["d" + n for n in cls.MATRICES + cls.VECTORS if not (tied and n == "W_head")]

@@ -1,7 +1,8 @@
 """GPU parity of p24_grad_norm and p24_clip_grads against the fp64 oracle (oracle/block_oracle.py).
 
 Tolerances, u = 2^-24: a thread adds the squares of at most 128 elements in fp32 (130u relative on a sum of positive
-terms), the rest is pairs of fp32 numbers or fp64 (less than u in all); on the norm half of it, and its rounding: 70u. A scaled gradient: 70u, the quotient,
+terms), the rest is pairs of fp32 numbers or fp64 (less than u in all); on the norm half of it, and its rounding: 70u. A
+scaled gradient: 70u, the quotient,
 the product, and the output's rounding: (73u + half a step) |g|."""
 import numpy as np
 import pytest

@@ -134,3 +134,25 @@ def test_a_step_is_refused_inputs_of_other_sizes(P):
     for k in ("E", "w_in", "W_up", "W_head"):
         with pytest.raises(ValueError):
             step.run(tokens, {**w, k: w[k][:32]}, idx, val, dkl)
+
+
+@pytest.mark.parametrize("absent", [("b_up", "b_down"), ("w_in", "w_out"), ("w_out", "b_up")])
+def test_a_step_without_some_norms_or_biases(P, absent):
+    """They have no gradient, the norm counts none for them, and the others are those of ones and zeros in their place."""
+    from semi_structured_sparse_prune24_gb300.distill import StudentStep
+    w, _, tokens, idx, val = inputs(64, 64, 64, 64, 4, 3)
+    dkl = torch.full((64,), 1.0 / 64, device="cuda")
+    step = StudentStep(64, 64, 64, 64)
+    o = step.run(tokens, {k: v for k, v in w.items() if k not in absent}, idx, val, dkl, max_norm=1e9)
+    neutral = {k: (v if k not in absent else torch.ones_like(v) if k[0] == "w" else torch.zeros_like(v)) for k, v in w.items()}
+    want = step.run(tokens, neutral, idx, val, dkl, max_norm=None)
+    names = [k for k in step.gradients() if k[1:] not in absent]
+    assert set(names) | {"kl", "norm"} <= set(o) and not any("d" + k in o for k in absent)
+    for k in names:
+        if k != "db_up":        # by atomics
+            assert torch.equal(o[k], want[k]), k
+    n = float(torch.stack([o[k].double().square().sum() for k in names]).sum().sqrt())
+    assert abs(float(o["norm"]) - n) <= 1e-6 * n
+    for k in ("E", "W_up", "W_down"):
+        with pytest.raises(ValueError, match=k):
+            step.run(tokens, {**w, k: None}, idx, val, dkl)
