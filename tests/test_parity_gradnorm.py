@@ -170,7 +170,8 @@ def test_a_tensor_listed_twice(P):
     """Counted twice by the norm; refused where it would be scaled twice, or written while it is read."""
     buf = torch.ones(64, device="cuda")
     a, b, c = buf[:32], buf[32:], torch.ones(32, device="cuda")
-    assert float(P.p24_grad_norm([a, b, a])) == 96 ** 0.5
+    n = float(P.p24_grad_norm([a, b, a]))
+    assert abs(n - 96 ** 0.5) <= 70 * U * n
     for grads, out in (([a, b, a], None), ([b, buf[31:33]], None), ([a, c], [c, b]), ([a, b], [c, c]), ([a], [buf[1:33]])):
         with pytest.raises(ValueError, match="overlap"):
             P.p24_clip_grads(grads, 1.0, out=out)
