@@ -146,20 +146,20 @@ class StudentStep:
             tail: bool = True, max_norm: float | None = 1.0, stream=None) -> dict:
         """Returns kl (and ce) per token, the gradients, and with max_norm their norm before they were scaled.
         tokens: int32 [M]; one outside 0..V-1 is padding."""
-        w, head = weights, self.layer.head
+        w, head = {k: weights.get(k) for k in self.MATRICES + self.VECTORS}, self.layer.head
         M, d, ffn, V = head.M, head.d, self.layer.ffn, head.V
-        tied = w.get("W_head") is None
+        tied = w["W_head"] is None
         _shape(tokens, (M,), "tokens")
         for name, shape in (("E", (V, d)), ("w_in", (d,)), ("W_up", (ffn, d)), ("b_up", (ffn,)), ("W_down", (d, ffn)),
                             ("b_down", (d,)), ("w_out", (d,)), ("W_head", (V, d))):
-            _shape(w.get(name), shape, name)
+            _shape(w[name], shape, name)
         for name in self.MATRICES[:3]:
-            if w.get(name) is None:
+            if w[name] is None:
                 raise ValueError(f"a step needs {name}")
         with N._on(stream):
             x = N.p24_embed(tokens, w["E"], self.scale)
             a = N.p24_rmsnorm(x, w["w_in"], eps=self.eps)
-            H, Y = self.layer._forward(a["y"], w["W_up"], w.get("b_up"), w["W_down"], w.get("b_down"))
+            H, Y = self.layer._forward(a["y"], w["W_up"], w["b_up"], w["W_down"], w["b_down"])
             b = N.p24_rmsnorm(Y, w["w_out"], residual=x, eps=self.eps, out={"h": Y})
             o = head.step(b["y"], w["E"] if tied else w["W_head"], top_idx, top_logp, dkl, labels, dce, temperature, tail)
             back = N.p24_rmsnorm_bwd(o.pop("dY"), b["h"], w["w_out"], b["rstd"])
@@ -168,7 +168,7 @@ class StudentStep:
             back = N.p24_rmsnorm_bwd(o.pop("dX"), x, w["w_in"], a["rstd"], dres=dh, out={"dx": dh})
             o["dw_in"] = back.get("dweight")
             for name in self.VECTORS:
-                if w.get(name) is None:
+                if w[name] is None:
                     o.pop("d" + name)
             dW = o.pop("dW")
             if tied:
