@@ -346,14 +346,14 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3) |
          static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3)) << 16;
 }
-// Of values times a factor, one for the first `cut` columns and another for the rest.
+// Of values times a factor.
 template <int E>
-__device__ __forceinline__ void store_e4m3(uint8_t* row, int c, bool vec, const Vals<E>& a, float fa, float fb, int cut) {
+__device__ __forceinline__ void store_e4m3(uint8_t* row, int c, bool vec, Vals<E> a, float f) {
   float v[E];
+#pragma unroll
+  for (int k = 0; k < E / 2; ++k) a.p[k] = a.p[k] * both(f);
   to_array(a, v);
   uint32_t q[E / 4];
-#pragma unroll
-  for (int k = 0; k < E; ++k) v[k] *= k < cut ? fa : fb;
 #pragma unroll
   for (int k = 0; k < E / 4; ++k) q[k] = e4m3x4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
   if (vec) {
@@ -366,8 +366,10 @@ __device__ __forceinline__ void store_e4m3(uint8_t* row, int c, bool vec, const 
 }
 // A scale and what values are multiplied by, from the largest magnitude. The reciprocal is that of the
 // stored scale, so that code times scale is the nearest to the value that the code allows; below 2^-118
-// a scale's reciprocal leaves fp32's range, and the scale stays there.
+// a scale's reciprocal leaves fp32's range, and the scale stays there. The reciprocal is the approximate one, a unit
+// in the last place off at most: a value times it is as far off as the product's own rounding twice over.
 __device__ __forceinline__ float scale_of(float top) { return top == 0.f ? 1.f : max_nan(top * (1.f / 448.f), 0x1p-118f); }
+__device__ __forceinline__ float one_over(float scale) { return __fdividef(1.f, scale); }
 template <int E>
 __device__ __forceinline__ float top_of(const Vals<E>& a) {
   float v[E], top = 0.f;
@@ -386,9 +388,19 @@ struct Plan {
 // Sum or maximum over a unit; `k`: which of the reductions of a row, `odd`: the row's parity.
 template <bool kWarp>
 struct Reduce {
-  float (*part)[3][32];
+  float (*part)[4][32];
   __device__ __forceinline__ float add(float x, int odd, int k) const { return kWarp ? warp_add(x) : cta_add(x, part[odd][k]); }
   __device__ __forceinline__ float max(float x, int odd, int k) const { return kWarp ? lanes_max(x) : cta_max(x, part[odd][k]); }
+  // A sum and a maximum together.
+  __device__ __forceinline__ void add_max(float& x, float& top, int odd, int k, int l) const {
+    x = warp_add(x), top = lanes_max(top);
+    if (kWarp) return;
+    const unsigned at = threadIdx.x & 31, warps = blockDim.x >> 5;
+    if (at == 0) part[odd][k][threadIdx.x >> 5] = x, part[odd][l][threadIdx.x >> 5] = top;
+    __syncthreads();
+    x = warp_add(at < warps ? part[odd][k][at] : 0.f);
+    top = lanes_max(at < warps ? part[odd][l][at] : 0.f);
+  }
   __device__ __forceinline__ void sync() const {
     if (kWarp) __syncwarp();
     else __syncthreads();
@@ -397,7 +409,7 @@ struct Reduce {
 
 template <bool kWarp, bool kAligned, bool kRing, int E, int C, bool kQuant>
 __global__ void __launch_bounds__(kWarp ? 256 : 1024, kWarp ? (C > 8 ? 3 : 4) : 1) rmsnorm_kernel(const p24_rmsnorm_args g, const Plan plan, int* status) {
-  __shared__ float part[2][3][32];
+  __shared__ float part[2][4][32];
   __shared__ Beside<2> beside[kWarp ? 8 : 1];
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr int NV = C / E;
@@ -467,7 +479,21 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024, kWarp ? (C > 8 ? 3 : 4) : 
       for (int i = 0; i < NV; ++i)
         if (sp.has(i)) store_vals<E>(h_out.row(t), row.f32(1), sp.column(i), hv, h[i]);
     }
-    const float total = reduce.add(fmaf(e, e, sum_of<E>(sums)), odd, 0);
+    float total = fmaf(e, e, sum_of<E>(sums)), top = 0.f;
+    if (kQuant && groups == 1) {  // the row's scale with the same meeting of the threads, from the largest |h w|
+      top = fabsf(e * w.edge);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (!sp.has(i)) continue;
+        Vals<E> wi = w.get(sp, i);
+#pragma unroll
+        for (int k = 0; k < E / 2; ++k) wi.p[k] = wi.p[k] * h[i].p[k];
+        top = max_nan(top, top_of(wi));
+      }
+      reduce.add_max(total, top, odd, 0, 3);
+    } else {
+      total = reduce.add(total, odd, 0);
+    }
     // every thread has read its pieces: the reduction says so
     if (kRing) {
       row.fill(t + plan.S * step, row.stage);
@@ -485,6 +511,7 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024, kWarp ? (C > 8 ? 3 : 4) : 
         }
       const float small = e * 0x1p-80f;
       rstd = 0x1p-80f * rsqrtf(reduce.add(fmaf(small, small, sum_of<E>(sums)), odd, 1) * inv_d);
+      top = 0.f;
     }
     if (g.rstd && sp.tid == 0) g.rstd[t] = rstd;
     e = e * rstd * w.edge;
@@ -506,15 +533,20 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024, kWarp ? (C > 8 ? 3 : 4) : 
     const bool qv = kAligned || (reinterpret_cast<uintptr_t>(y + sp.c0) & (E - 1)) == 0;
     float* scales = g.scale + t * g.lds;
     if (groups == 1) {
-      float top = fabsf(e);
+      if (top >= 0x1p-100f && top <= 0x1p100f) {
+        top *= rstd;
+      } else {  // h w leaves fp32's range, or is no number
+        top = fabsf(e);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) top = max_nan(top, top_of(h[i]));
-      const float sc = scale_of(reduce.max(top, odd, 2)), inv = 1.f / sc;
+        for (int i = 0; i < NV; ++i) top = max_nan(top, top_of(h[i]));
+        top = reduce.max(top, odd, 2);
+      }
+      const float sc = scale_of(top), f = one_over(sc);
       if (sp.tid == 0) scales[0] = sc;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (sp.has(i)) store_e4m3<E>(y, sp.column(i), qv, h[i], inv, inv, E);
-      if (sp.has_edge()) y[sp.edge] = static_cast<uint8_t>(e4m3x4(e * inv, 0.f, 0.f, 0.f));
+        if (sp.has(i)) store_e4m3<E>(y, sp.column(i), qv, h[i], f);
+      if (sp.has_edge()) y[sp.edge] = static_cast<uint8_t>(e4m3x4(e * f, 0.f, 0.f, 0.f));
     } else if (kAligned && g.group <= 32 * E) {
       // a group is some neighbouring lanes' pieces
       const int lanes = g.group / E;
@@ -522,10 +554,10 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024, kWarp ? (C > 8 ? 3 : 4) : 
       for (int i = 0; i < NV; ++i) {
         float top = top_of(h[i]);
         for (int k = lanes >> 1; k; k >>= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, k));
-        const float sc = scale_of(top), inv = 1.f / sc;
+        const float sc = scale_of(top);
         if (!sp.has(i)) continue;
         if ((lane & (lanes - 1)) == 0) scales[sp.column(i) >> shift] = sc;
-        store_e4m3<E>(y, sp.column(i), qv, h[i], inv, inv, E);
+        store_e4m3<E>(y, sp.column(i), qv, h[i], one_over(sc));
       }
     } else {
       // A piece meets at most two groups, from column `cut` of it on the second. Magnitudes are ordered as whole
@@ -551,10 +583,13 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024, kWarp ? (C > 8 ? 3 : 4) : 
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if (!sp.has(i)) continue;
-        const int c = sp.column(i), ga = c >> shift, gb = (c + E - 1) >> shift;
-        store_e4m3<E>(y, c, qv, h[i], 1.f / scale_of(tops[ga]), 1.f / scale_of(tops[gb]), ga == gb ? E : (gb << shift) - c);
+        const int c = sp.column(i), ga = c >> shift, gb = (c + E - 1) >> shift, cut = ga == gb ? E : (gb << shift) - c;
+        const float fa = one_over(scale_of(tops[ga])), fb = one_over(scale_of(tops[gb]));
+#pragma unroll
+        for (int k = 0; k < E / 2; ++k) h[i].p[k] = h[i].p[k] * two(2 * k < cut ? fa : fb, 2 * k + 1 < cut ? fa : fb);
+        store_e4m3<E>(y, c, qv, h[i], 1.f);
       }
-      if (sp.has_edge()) y[sp.edge] = static_cast<uint8_t>(e4m3x4(e * (1.f / scale_of(tops[sp.edge >> shift])), 0.f, 0.f, 0.f));
+      if (sp.has_edge()) y[sp.edge] = static_cast<uint8_t>(e4m3x4(e * one_over(scale_of(tops[sp.edge >> shift])), 0.f, 0.f, 0.f));
       for (int i = sp.tid; i < groups; i += sp.NT) scales[i] = scale_of(tops[i]);
       reduce.sync();  // before the next row's groups
     }
@@ -567,7 +602,7 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024, kWarp ? (C > 8 ? 3 : 4) : 
 // of `parts`.
 template <bool kWarp, bool kAligned, bool kRing, int E, int C>
 __global__ void __launch_bounds__(kWarp ? 256 : 1024, kWarp ? 3 : 1) rmsnorm_bwd_kernel(const p24_rmsnorm_bwd_args g, const Plan plan, float* parts, int* status) {
-  __shared__ float part[2][3][32];
+  __shared__ float part[2][4][32];
   __shared__ Beside<3> beside[kWarp ? 8 : 1];
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr int NV = C / E;
@@ -855,16 +890,26 @@ cudaError_t grid_of(K kern, const Shape& z, int64_t T, int64_t most, int64_t* gr
 }
 
 
-// Columns of a thread. Of 8 a row of more than 4096 columns takes one CTA on an SM, of 16 two or more: those hide a
-// row's reduction behind each other, but have less of the ring. With one matrix to read 16 are faster (8192 rows of
-// 5001 bf16 35 us against 65, of 8192 43 against 54; the gradient without a skip connection's, of 6290, 70 against
-// 84), with a residual 8 are (16384 rows of 8192 166 against 176), unless they leave the SM a quarter empty (8192
-// rows of 5001: 60 against 70). In the gradient with fp32 8 always (8192 rows of 6290 125 against 172).
-int columns_of(int d, int E, bool residual, bool gradient, bool few) {
+// Columns of a thread, 8 or 16. 16 halve the instructions that a row's reduction, its wait and its addresses take
+// (164 in all for a warp's 256 columns; issue slots are the forward's bound, 70%), and allow a row of more than 4096
+// columns more CTAs on an SM; 8 have twice the ring. us, 8 and 16, rows of bf16 unless said:
+//   one matrix to read: 16 (16384 x 4096 51 and 48, x 4095 73 and 46, x 1024 14.0 and 11.8, 8192 x 8192 52 and 43)
+//   with a residual: 8 (16384 x 4096 81 and 90, x 768 15.3 and 17.6; x 8192 166 and 176), unless they leave the SM a
+//     quarter empty (8192 x 5001 70 and 60)
+//   8-bit codes, half as many instructions again: 16 (16384 x 4096 without a residual 73 and 55, with one 87 and 81),
+//     with a residual where a row is more than 1024 columns (x 1024 25 and 24, x 768 18.7 and 21.7)
+//   fp32: 8 (8192 x 4096 43 and 47), for codes without a residual as above (43 and 39)
+//   the gradient: 8 (16384 x 4096 64 and 67, x 1024 22 and 28), 16 without a skip connection's in rows of more than 4096
+//     bf16 (8192 x 6290 84 and 70; fp32 125 and 172)
+//   few rows: 8, for a row's time is a thread's
+int columns_of(int d, int E, bool residual, bool quant, bool gradient, bool few) {
   if (d > 8192) return 16;
-  if (d <= 4096 || few || (E == 4 && (residual || gradient))) return 8;
   const int NT = (d + 255) / 256 * 32;
-  return !residual || 1024 / NT * NT < 768 ? 16 : 8;
+  const bool empty = d > 4096 && 1024 / NT * NT < 768;
+  if (few) return 8;
+  if (gradient) return E == 8 && d > 4096 && (!residual || empty) ? 16 : 8;
+  if (quant) return (residual ? E == 8 && d > 1024 : E == 8 || d > 1024) ? 16 : 8;
+  return E == 8 && (!residual || empty) ? 16 : 8;
 }
 
 template <bool kAligned, int E, bool kQuant>
@@ -885,7 +930,7 @@ cudaError_t launch_norm(const p24_rmsnorm_args& g, Phase ph, bool ring, int* sta
     return go(rmsnorm_kernel<true, kAligned, true, E, 16, kQuant>, ring_shape(d, 16, true, bytes, own, ph, 80 << 10));
   }
   const bool few = g.T <= 2 * sm_count();
-  const int C = columns_of(d, E, g.r != nullptr, false, few);
+  const int C = columns_of(d, E, g.r != nullptr, kQuant, false, few);
   const Shape z = ring_shape(d, C, false, bytes, own, ph, 80 << 10);
   if (ring && d <= 16384 && z.plan.S > 0)
     return C == 8 ? go(rmsnorm_kernel<false, kAligned, true, E, 8, kQuant>, z) : go(rmsnorm_kernel<false, kAligned, true, E, 16, kQuant>, z);
@@ -915,7 +960,7 @@ cudaError_t launch_bwd(const p24_rmsnorm_bwd_args& g, Phase ph, bool ring, float
     return go(rmsnorm_bwd_kernel<true, kAligned, true, E, 16>, ring_shape(d, 16, true, bytes, 0, ph, 0));
   }
   const bool few = g.T <= 2 * sm_count();
-  const int C = columns_of(d, E, g.dres != nullptr, true, few);
+  const int C = columns_of(d, E, g.dres != nullptr, false, true, few);
   const Shape z = ring_shape(d, C, false, bytes, 0, ph, 0);
   if (ring && d <= 16384 && z.plan.S > 0)
     return C == 8 ? go(rmsnorm_bwd_kernel<false, kAligned, true, E, 8>, z) : go(rmsnorm_bwd_kernel<false, kAligned, true, E, 16>, z);

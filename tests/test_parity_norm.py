@@ -311,3 +311,25 @@ def test_refusals_of_the_binding(P):
         P.p24_rmsnorm(torch.zeros((64, 4), dtype=BF, device="cuda").t(), w)
     with pytest.raises(P.P24Error):
         P.p24_rmsnorm_bwd(x, x, w, torch.ones(4, device="cuda"), workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("d", [4, 130, 520, 4096, 4099, 20000])
+@pytest.mark.parametrize("sx,sw", [(1e15, 1e25), (1e-5, 1e-36), (1e25, 1e10), (1e-3, 1e-3), (3e-20, 1.0)])
+def test_row_scales_where_products_with_the_weight_leave_fp32(P, d, sx, sw):
+    """The scale of a whole row is found from h w before the norm is known, where that is representable. The scale within
+    that of the values, E + 6u; a code is one of those that the value times 1 -+ 2^-15 rounds to."""
+    g = torch.Generator(device="cuda").manual_seed(d)
+    x = torch.randn((3, d), generator=g, device="cuda") * sx
+    x[1] = 0
+    w = torch.randn(d, generator=g, device="cuda") * sw
+    o = P.p24_rmsnorm(x, w, eps=1e-12, group=0)
+    h = x.double()
+    y = h / (h.square().mean(1, keepdim=True) + 1e-12).sqrt() * w.double()
+    top = y.abs().amax(1, keepdim=True) / 448
+    s = torch.where(top == 0, 1.0, top.clamp_min(2.0 ** -118))
+    u = 2.0 ** -24
+    assert bool(((o["scale"].double() - s).abs() <= 86 * u * s).all())
+    v = y / s
+    q = o["y"].float()
+    near = [(v * (1 + k * 2.0 ** -15)).clamp(-448, 448).float().to(torch.float8_e4m3fn).float() for k in (-1, 1)]
+    assert bool(((q == near[0]) | (q == near[1])).all())
