@@ -1,10 +1,11 @@
 """ctypes binding of libprune24 (include/prune24.h): argument marshalling only.
 
 Every call forwards raw device pointers, sizes and row strides of torch tensors
-to the C ABI and runs on the current torch CUDA stream; all arithmetic happens
-in the library's CUDA kernels. Output tensors the caller does not pass are
+to the C ABI (those of the calls around the FFN through csrc/p24_torch.cpp) and
+runs on the current torch CUDA stream; all arithmetic happens in the library's
+CUDA kernels. Output tensors the caller does not pass are
 allocated with torch (device memory is torch's job here). There is no CPU path:
-if the shared library is missing, importing this module raises.
+if the shared libraries are missing, importing this module raises.
 """
 from __future__ import annotations
 

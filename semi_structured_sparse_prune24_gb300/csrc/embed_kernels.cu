@@ -17,22 +17,28 @@
 namespace p24 {
 namespace {
 
+// Neighbouring columns that are moved at once, where rows are aligned.
+template <typename A, typename B>
+constexpr int piece() {
+  return sizeof(A) == 4 || sizeof(B) == 4 ? 4 : 8;
+}
+
 // ---------------------------------------------------------------- lookup
 // A CTA: blockDim.x threads with 8 columns each, blockDim.y rows, U of them for a thread.
-template <typename Tw, typename To, int U, bool kVec>
+template <typename Tw, typename To, int U, int E>
 __global__ void __launch_bounds__(256) embed_kernel(const p24_embed_args g) {
-  const Columns<kVec> k(blockIdx.y, threadIdx.x, blockDim.x, static_cast<int>(g.d));
+  const Columns<E> k(blockIdx.y, threadIdx.x, blockDim.x, static_cast<int>(g.d));
   const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * U) * blockDim.y + threadIdx.y;
   pdl_wait();
   pdl_trigger();
-  if (k.n == 0) return;
+  if (k.none()) return;
   int tok[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int64_t t = t0 + u * blockDim.y;
     tok[u] = t < g.T ? g.tokens[t] : -1;
   }
-  Loaded<kVec, Tw> r[U];
+  Loaded<E, Tw> r[U];
 #pragma unroll
   for (int u = 0; u < U; ++u)
     if (tok[u] >= 0 && tok[u] < g.V) r[u] = load_columns(static_cast<const Tw*>(g.W) + static_cast<int64_t>(tok[u]) * g.ldw, k);
@@ -250,7 +256,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const p24_embe
 
 // ---------------------------------------------------------------- sums
 constexpr int kBlockMost = 64;  // sorted positions of a block, at most
-constexpr int kJoinThreads = 512;
+constexpr int kSumThreads = 128, kJoinThreads = 512;
 
 struct SumArgs {
   p24_embed_bwd_args g;
@@ -265,8 +271,8 @@ __device__ __forceinline__ float* part_of(const SumArgs& a, int64_t block, int w
   return a.parts + (2 * block + which) * a.wide + (static_cast<int64_t>(blockIdx.y) * width + threadIdx.x) * 8;
 }
 
-template <bool kVec, typename To>
-__device__ __forceinline__ void put_row(const p24_embed_bwd_args& g, int v, const Columns<kVec>& k, float (&s)[8]) {
+template <int E, typename To>
+__device__ __forceinline__ void put_row(const p24_embed_bwd_args& g, int v, const Columns<E>& k, float (&s)[8]) {
   To* to = static_cast<To*>(g.dW) + static_cast<int64_t>(v) * g.lddw;
 #pragma unroll
   for (int i = 0; i < 8; ++i) s[i] *= g.scale;
@@ -279,14 +285,14 @@ __device__ __forceinline__ void put_row(const p24_embed_bwd_args& g, int v, cons
   store_columns(to, k, s);
 }
 
-template <typename Td, typename To, int U, bool kVec>
-__global__ void __launch_bounds__(256) embed_sum_kernel(const SumArgs a) {
+template <typename Td, typename To, int U, int E>
+__global__ void __launch_bounds__(kSumThreads, E == 1 ? 4 : sizeof(Td) == 4 ? 7 : 8) embed_sum_kernel(const SumArgs a) {
   __shared__ int2 e[kBlockMost + 2];  // the block's, with its neighbours around it
   const p24_embed_bwd_args& g = a.g;
   const int V = static_cast<int>(g.V);
   const int64_t p0 = static_cast<int64_t>(blockIdx.x) * a.length;
   const int n = static_cast<int>(min(static_cast<int64_t>(a.length), g.T - p0));
-  const Columns<kVec> k(blockIdx.y, threadIdx.x, blockDim.x, static_cast<int>(g.d));
+  const Columns<E> k(blockIdx.y, threadIdx.x, blockDim.x, static_cast<int>(g.d));
   pdl_wait();
   pdl_trigger();
   for (int i = threadIdx.x; i < n + 2; i += blockDim.x) {
@@ -294,14 +300,14 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const SumArgs a) {
     e[i] = p >= 0 && p < g.T ? a.sorted[p] : make_int2(-1, -1);
   }
   __syncthreads();
-  if (k.n == 0) return;
+  if (k.none()) return;
   const Td* dy = static_cast<const Td*>(g.dY);
   float s[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) s[i] = 0.f;
   int start = 1;
   for (int i0 = 1; i0 <= n && e[i0].x < V; i0 += U) {
-    Loaded<kVec, Td> r[U];
+    Loaded<E, Td> r[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (i0 + u <= n && e[i0 + u].x < V) r[u] = load_columns(dy + static_cast<int64_t>(e[i0 + u].y) * g.lddy, k);
@@ -317,7 +323,7 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const SumArgs a) {
       // a run ends, or the block does
       const bool enters = start == 1 && e[0].x == e[1].x, leaves = i == n && e[n + 1].x == e[n].x;
       if (!enters && !leaves) {
-        put_row<kVec, To>(g, e[i].x, k, s);
+        put_row<E, To>(g, e[i].x, k, s);
       } else {
         float* to = part_of(a, blockIdx.x, enters ? 0 : 1, blockDim.x);
         reinterpret_cast<float4*>(to)[0] = make_float4(s[0], s[1], s[2], s[3]);
@@ -332,12 +338,12 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const SumArgs a) {
 
 // For each run that crosses blocks, at the first border that it crosses: its parts, added up by blockDim.y groups of
 // threads that take neighbouring ones, and then group by group.
-template <typename To, bool kVec>
+template <typename To, int E>
 __global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(const SumArgs a) {
   __shared__ float groups[kJoinThreads][8];
   const p24_embed_bwd_args& g = a.g;
   const int64_t blocks = (g.T + a.length - 1) / a.length;
-  const Columns<kVec> k(blockIdx.y, threadIdx.x, blockDim.x, static_cast<int>(g.d));
+  const Columns<E> k(blockIdx.y, threadIdx.x, blockDim.x, static_cast<int>(g.d));
   const int me = threadIdx.y * blockDim.x + threadIdx.x;
   pdl_wait();
   pdl_trigger();
@@ -368,11 +374,11 @@ __global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(const SumArgs 
 #pragma unroll
     for (int i = 0; i < 8; ++i) groups[me][i] = s[i];
     __syncthreads();
-    if (threadIdx.y == 0 && k.n > 0) {
+    if (threadIdx.y == 0 && !k.none()) {
       for (int y = 1; y < static_cast<int>(blockDim.y); ++y)
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[i] += groups[y * blockDim.x + threadIdx.x][i];
-      put_row<kVec, To>(g, v, k, s);
+      put_row<E, To>(g, v, k, s);
     }
     __syncthreads();
   }
@@ -387,21 +393,20 @@ int block_length(int64_t T, int64_t d) {
 }
 int64_t sort_bytes(int64_t T) { return (T * 8 + 255) / 256 * 256; }
 
-constexpr int kSumThreads = 128;
 int64_t wide_of(int64_t d) {
   const RowThreads r = row_threads(d, kSumThreads);
   return static_cast<int64_t>(r.x) * r.chunks * 8;
 }
 
-template <typename Td, typename To, bool kVec>
+template <typename Td, typename To, int E>
 cudaError_t launch_sums_as(const SumArgs& a, cudaStream_t s) {
   const RowThreads r = row_threads(a.g.d, kSumThreads);
   const int64_t blocks = (a.g.T + a.length - 1) / a.length;
-  cudaError_t e = launch_pdl(embed_sum_kernel<Td, To, 4, kVec>, dim3(static_cast<unsigned>(blocks), r.chunks), dim3(r.x), 0, s, a);
+  cudaError_t e = launch_pdl(embed_sum_kernel<Td, To, 4, E>, dim3(static_cast<unsigned>(blocks), r.chunks), dim3(r.x), 0, s, a);
   if (e != cudaSuccess) return e;
   count_launch();
   if (blocks == 1) return e;
-  e = launch_pdl(embed_join_kernel<To, kVec>, dim3(static_cast<unsigned>(std::min<int64_t>(blocks - 1, 65535)), r.chunks),
+  e = launch_pdl(embed_join_kernel<To, E>, dim3(static_cast<unsigned>(std::min<int64_t>(blocks - 1, 65535)), r.chunks),
                  dim3(r.x, kJoinThreads / r.x), 0, s, a);
   if (e == cudaSuccess) count_launch();
   return e;
@@ -409,13 +414,14 @@ cudaError_t launch_sums_as(const SumArgs& a, cudaStream_t s) {
 template <typename Td, typename To>
 cudaError_t launch_sums(const SumArgs& a, cudaStream_t s) {
   const bool vec = rows_aligned(a.g.dY, a.g.lddy, a.g.dy_dtype) && rows_aligned(a.g.dW, a.g.lddw, a.g.dw_dtype);
-  return vec ? launch_sums_as<Td, To, true>(a, s) : launch_sums_as<Td, To, false>(a, s);
+  return vec ? launch_sums_as<Td, To, sizeof(Td) == 2 ? piece<Td, To>() : 8>(a, s) : launch_sums_as<Td, To, 1>(a, s);
 }
 
 template <typename Tw, typename To>
 cudaError_t launch_embed_as(const p24_embed_args& g, cudaStream_t s) {
   const bool vec = rows_aligned(g.W, g.ldw, g.w_dtype) && rows_aligned(g.Y, g.ldy, g.y_dtype);
   const RowThreads r = row_threads(g.d, 256);
+  constexpr int E = piece<Tw, To>();
   const dim3 block(r.x, 256 / r.x);
   auto go = [&](auto kern, int u) {
     const int64_t rows = static_cast<int64_t>(u) * block.y;
@@ -424,8 +430,8 @@ cudaError_t launch_embed_as(const p24_embed_args& g, cudaStream_t s) {
     return e;
   };
   // 4 rows a thread where that leaves 8 CTAs for each SM
-  if (g.T * r.x * r.chunks >= 256 * 8 * 4 * sm_count()) return vec ? go(embed_kernel<Tw, To, 4, true>, 4) : go(embed_kernel<Tw, To, 4, false>, 4);
-  return vec ? go(embed_kernel<Tw, To, 1, true>, 1) : go(embed_kernel<Tw, To, 1, false>, 1);
+  if (g.T * r.x * r.chunks >= 256 * 8 * 4 * sm_count()) return vec ? go(embed_kernel<Tw, To, 4, E>, 4) : go(embed_kernel<Tw, To, 4, 1>, 4);
+  return vec ? go(embed_kernel<Tw, To, 1, E>, 1) : go(embed_kernel<Tw, To, 1, 1>, 1);
 }
 
 }  // namespace

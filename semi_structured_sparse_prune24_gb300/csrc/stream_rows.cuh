@@ -134,55 +134,105 @@ __device__ __forceinline__ void store8(T* row, int c, int d, bool vec, const flo
   }
 }
 
-// A thread's 8 columns of a row: neighbours, moved 16 bytes at a time, where every row of a matrix lies on 16-byte
-// boundaries (kVec), else every blockDim.x-th one, moved element by element, so that a warp's access still covers
-// whole sectors (16384 x 767 bf16 looked up with 8 neighbours an element at a time 36 us, like this 17).
-template <bool kVec>
+// A thread's 8 columns of a row, in pieces of E neighbours that are moved at once, piece p `width` pieces from the one
+// before. Where every row of a matrix lies on 16-byte boundaries E is 8, or 4 where a matrix is fp32: then too a warp's
+// access covers whole sectors. Other rows take E = 1 for the same reason (16384 x 767 bf16 looked up with 8 neighbours
+// an element at a time 36 us, like this 17).
+template <int E>
 struct Columns {
-  int c, step, n;  // the first, from one to the next, how many of the 8 there are
-  __device__ __forceinline__ Columns(int chunk, int tid, int width, int d) {
-    c = chunk * width * 8 + (kVec ? 8 * tid : tid);
-    step = kVec ? 1 : width;
-    n = c >= d ? 0 : min(8, (d - c + step - 1) / step);
-  }
+  int c, step, d;  // the first, from one piece to the next, of a row
+  __device__ __forceinline__ Columns(int chunk, int tid, int width, int d_) : c(chunk * width * 8 + E * tid), step(E * width), d(d_) {}
+  __device__ __forceinline__ bool none() const { return c >= d; }
 };
-// A thread's elements as they lie in memory.
-template <bool kVec, typename T>
+// E elements in one access.
+template <int bytes>
+struct Word;
+template <>
+struct Word<2> { using type = uint16_t; };
+template <>
+struct Word<4> { using type = uint32_t; };
+template <>
+struct Word<8> { using type = uint2; };
+template <>
+struct Word<16> { using type = uint4; };
+template <>
+struct Word<32> { struct type { uint4 q[2]; }; };
+
+// A thread's elements as they lie in memory; those outside the row are 0.
+template <int E, typename T>
 struct Loaded {
-  Raw8<T> r;
+  union {
+    typename Word<E * sizeof(T)>::type w[8 / E];
+    uint32_t u[2 * sizeof(T)];
+  };
 };
 template <typename T>
-struct Loaded<false, T> {
+struct Loaded<1, T> {  // (pairs of bf16 in a register would be put together load by load)
   T e[8];
 };
-template <bool kVec, typename T>
-__device__ __forceinline__ Loaded<kVec, T> load_columns(const T* row, const Columns<kVec>& k) {
-  Loaded<kVec, T> x;
-  if constexpr (kVec) {
-    x.r = load8(row, k.c, k.c + k.n, true);
-  } else {
+template <int E, typename T>
+__device__ __forceinline__ Loaded<E, T> load_columns(const T* row, const Columns<E>& k) {
+  Loaded<E, T> x;
+  if constexpr (E == 1) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x.e[i] = i < k.n ? row[k.c + i * k.step] : static_cast<T>(0.f);
-  }
-  return x;
-}
-template <bool kVec, typename T>
-__device__ __forceinline__ void values(const Loaded<kVec, T>& x, float (&v)[8]) {
-  if constexpr (kVec) {
-    unpack8(x.r, v);
+    for (int i = 0; i < 8; ++i) x.e[i] = k.c + i * k.step < k.d ? row[k.c + i * k.step] : static_cast<T>(0.f);
+    return x;
   } else {
+    using W = typename Word<E * sizeof(T)>::type;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = to_float(x.e[i]);
+    for (unsigned i = 0; i < 2 * sizeof(T); ++i) x.u[i] = 0;
+#pragma unroll
+    for (int p = 0; p < 8 / E; ++p) {
+      const int c = k.c + p * k.step;
+      if (c + E <= k.d) {
+        x.w[p] = *reinterpret_cast<const W*>(row + c);
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+          if (c + i < k.d) {
+            const int at = p * E + i;
+            if (sizeof(T) == 4) x.u[at] = bits_of(row[c + i]);
+            else x.u[at / 2] |= bits_of(row[c + i]) << (16 * (at & 1));
+          }
+      }
+    }
+    return x;
   }
 }
-template <bool kVec, typename T>
-__device__ __forceinline__ void store_columns(T* row, const Columns<kVec>& k, const float (&v)[8]) {
-  if (kVec && k.n == 8) {
-    store8(row, k.c, k.c + 8, true, v);
-  } else {
+template <int E, typename T>
+__device__ __forceinline__ void values(const Loaded<E, T>& x, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (E == 1) v[i] = to_float(x.e[i]);
+    else if constexpr (sizeof(T) == 4) v[i] = __uint_as_float(x.u[i]);
+    else if ((i & 1) == 0) widen(x.u[i / 2], v[i], v[i + 1]);
+  }
+}
+template <int E, typename T>
+__device__ __forceinline__ void store_columns(T* row, const Columns<E>& k, const float (&v)[8]) {
+  if constexpr (E == 1) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < k.n) row[k.c + i * k.step] = static_cast<T>(v[i]);
+      if (k.c + i * k.step < k.d) row[k.c + i * k.step] = static_cast<T>(v[i]);
+  } else {
+    using W = typename Word<E * sizeof(T)>::type;
+    Loaded<E, T> x;
+#pragma unroll
+    for (unsigned i = 0; i < 2 * sizeof(T); ++i) {
+      if constexpr (sizeof(T) == 4) x.u[i] = __float_as_uint(v[i]);
+      else x.u[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    }
+#pragma unroll
+    for (int p = 0; p < 8 / E; ++p) {
+      const int c = k.c + p * k.step;
+      if (c + E <= k.d) {
+        *reinterpret_cast<W*>(row + c) = x.w[p];
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+          if (c + i < k.d) row[c + i] = static_cast<T>(v[p * E + i]);
+      }
+    }
   }
 }
 
