@@ -8,6 +8,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/Allocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -108,21 +109,25 @@ PyObject* result(PyObject* given, const at::Tensor& t) {
 }
 
 struct Scratch {
-  at::Tensor t;
+  c10::DataPtr own;
   void* p = nullptr;
   size_t bytes = 0;
 };
-// A call's scratch: the caller's, or one that is the current stream's memory when it is dropped.
+// A call's scratch: the caller's, or one from torch's allocator (without a tensor around it, 0.9 us a call), which is the
+// current stream's memory again when it is dropped.
 Scratch scratch(PyObject* given, size_t need, const at::Tensor& like) {
   Scratch s;
   if (given == Py_None) {
-    s.t = at::empty({static_cast<int64_t>(std::max<size_t>(need, 16))}, like.options().dtype(at::kByte).layout(at::kStrided));
+    static c10::Allocator* const memory = c10::GetAllocator(c10::DeviceType::CUDA);
+    s.bytes = std::max<size_t>(need, 16);
+    s.own = memory->allocate(s.bytes);
+    s.p = s.own.get();
   } else {
-    s.t = tensor(given, "workspace");
-    if (cuda_index(s.t) != cuda_index(like) || !s.t.is_contiguous())
+    const at::Tensor& t = tensor(given, "workspace");
+    if (cuda_index(t) != cuda_index(like) || !t.is_contiguous())
       refuse_value("the workspace must be a contiguous tensor on " + device_name(cuda_index(like)));
+    s.p = t.data_ptr(), s.bytes = t.nbytes();
   }
-  s.p = s.t.data_ptr(), s.bytes = s.t.nbytes();
   return s;
 }
 
