@@ -893,23 +893,27 @@ cudaError_t grid_of(K kern, const Shape& z, int64_t T, int64_t most, int64_t* gr
 // Columns of a thread, 8 or 16. 16 halve the instructions that a row's reduction, its wait and its addresses take
 // (164 in all for a warp's 256 columns; issue slots are the forward's bound, 70%), and allow a row of more than 4096
 // columns more CTAs on an SM; 8 have twice the ring. us, 8 and 16, rows of bf16 unless said:
-//   one matrix to read: 16 (16384 x 4096 51 and 48, x 4095 73 and 46, x 1024 14.0 and 11.8, 8192 x 8192 52 and 43)
+//   one matrix to read: 16 (16384 x 4096 51 and 48, x 4095 73 and 46, x 1024 14.0 and 11.8, 8192 x 8192 52 and 43); with
+//     fp32 in aligned rows 8 (8192 x 4096 to fp32 35 and 39, x 8192 fp32 86 and 93; x 6290 to fp32 89 and 61)
 //   with a residual: 8 (16384 x 4096 81 and 90, x 768 15.3 and 17.6; x 8192 166 and 176), unless they leave the SM a
-//     quarter empty (8192 x 5001 70 and 60)
-//   8-bit codes, half as many instructions again: 16 (16384 x 4096 without a residual 73 and 55, with one 87 and 81),
-//     with a residual where a row is more than 1024 columns (x 1024 25 and 24, x 768 18.7 and 21.7)
-//   fp32: 8 (8192 x 4096 43 and 47), for codes without a residual as above (43 and 39)
+//     quarter empty (8192 x 5001 70 and 60, beside an fp32 stream 94 and 83)
+//   8-bit codes, half as many instructions again: 16 (16384 x 4096 without a residual 73 and 53, with one 87 and 82),
+//     with a residual where a row is more than 1024 columns (x 1024 25 and 24, x 768 18.7 and 21.7), or beside an
+//     fp32 stream in unaligned rows of more than 4096 (8192 x 6290 129 and 107, x 8192 115 and 129)
 //   the gradient: 8 (16384 x 4096 64 and 67, x 1024 22 and 28), 16 without a skip connection's in rows of more than 4096
 //     bf16 (8192 x 6290 84 and 70; fp32 125 and 172)
 //   few rows: 8, for a row's time is a thread's
-int columns_of(int d, int E, bool residual, bool quant, bool gradient, bool few) {
+int columns_of(int d, int E, bool aligned, bool residual, bool quant, bool gradient, bool few) {
   if (d > 8192) return 16;
+  if (few) return 8;
   const int NT = (d + 255) / 256 * 32;
   const bool empty = d > 4096 && 1024 / NT * NT < 768;
-  if (few) return 8;
-  if (gradient) return E == 8 && d > 4096 && (!residual || empty) ? 16 : 8;
-  if (quant) return (residual ? E == 8 && d > 1024 : E == 8 || d > 1024) ? 16 : 8;
-  return E == 8 && (!residual || empty) ? 16 : 8;
+  bool more;
+  if (gradient) more = E == 8 && d > 4096 && (!residual || empty);
+  else if (quant && residual) more = E == 8 ? d > 1024 : !aligned && d > 4096;
+  else if (quant) more = E == 8 || d > 1024;
+  else more = residual ? empty : E == 8 || !aligned;
+  return more ? 16 : 8;
 }
 
 template <bool kAligned, int E, bool kQuant>
@@ -930,7 +934,7 @@ cudaError_t launch_norm(const p24_rmsnorm_args& g, Phase ph, bool ring, int* sta
     return go(rmsnorm_kernel<true, kAligned, true, E, 16, kQuant>, ring_shape(d, 16, true, bytes, own, ph, 80 << 10));
   }
   const bool few = g.T <= 2 * sm_count();
-  const int C = columns_of(d, E, g.r != nullptr, kQuant, false, few);
+  const int C = columns_of(d, E, kAligned, g.r != nullptr, kQuant, false, few);
   const Shape z = ring_shape(d, C, false, bytes, own, ph, 80 << 10);
   if (ring && d <= 16384 && z.plan.S > 0)
     return C == 8 ? go(rmsnorm_kernel<false, kAligned, true, E, 8, kQuant>, z) : go(rmsnorm_kernel<false, kAligned, true, E, 16, kQuant>, z);
@@ -960,7 +964,7 @@ cudaError_t launch_bwd(const p24_rmsnorm_bwd_args& g, Phase ph, bool ring, float
     return go(rmsnorm_bwd_kernel<true, kAligned, true, E, 16>, ring_shape(d, 16, true, bytes, 0, ph, 0));
   }
   const bool few = g.T <= 2 * sm_count();
-  const int C = columns_of(d, E, g.dres != nullptr, false, true, few);
+  const int C = columns_of(d, E, kAligned, g.dres != nullptr, false, true, few);
   const Shape z = ring_shape(d, C, false, bytes, 0, ph, 0);
   if (ring && d <= 16384 && z.plan.S > 0)
     return C == 8 ? go(rmsnorm_bwd_kernel<false, kAligned, true, E, 8>, z) : go(rmsnorm_bwd_kernel<false, kAligned, true, E, 16>, z);
