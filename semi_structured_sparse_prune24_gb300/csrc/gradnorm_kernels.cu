@@ -3,14 +3,15 @@
 //
 //   norm = sqrt(sum over all tensors and elements of g^2);   g <- g min(1, max_norm / norm)
 //
-// The tensors are cut into chunks of 4 to 32 KB; CTA b of a fixed grid takes chunks b, b + grid, ... (a stretch of
-// neighbouring ones each read as fast, but scaled 743 MB in 246 us instead of 226). A thread
-// squares and adds the elements of a chunk in fp32, and chunks, threads and CTAs are added as pairs of fp32 numbers,
-// a sum and what its rounding left (Knuth's two-sum): the number of elements costs no digits. Chunks whose sum
-// lies outside 2^-100 .. 2^88 (2^38 such sums still fit fp32) are squared and added again in fp64, so neither does their size. (All of it in
-// fp64 beyond the chunks took 45 us for 72 tensors of 4.8 MB: an SM adds two a clock.) Every sum has a fixed
-// order. The scaling pass goes through the chunks from the end, where the first
-// pass left off: what is in L2 still is read from there.
+// The bound is memory: 743 MB of bf16 and fp32 in 106 us (7.0 TB/s), scaled into other tensors in 348 in all (6.4). The
+// tensors are cut into chunks of 4 to 32 KB; CTA b of a fixed grid takes chunks b, b + grid, ... (a stretch of
+// neighbouring ones each read as fast, but scaled 743 MB in 246 us instead of 226). A thread squares and adds the
+// elements of a chunk in fp32, and chunks, threads and CTAs are added as pairs of fp32 numbers, a sum and what its
+// rounding left (Knuth's two-sum): the number of elements costs no digits. Chunks whose sum lies outside 2^-100 .. 2^88
+// (2^38 such sums still fit fp32) are squared and added again in fp64, so neither does their size. (All of it in fp64
+// beyond the chunks took 45 us for 72 tensors of 4.8 MB: an SM adds two a clock.) Every sum has a fixed order. The
+// scaling pass goes through the chunks from the end, where the first pass left off: what is in L2 still is read from
+// there.
 #include <algorithm>
 
 #include "stream_rows.cuh"
