@@ -749,6 +749,105 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024, kWarp ? 3 : 1) rmsnorm_bwd
   }
 }
 
+// The gradient of few rows in one launch, for then a second one's 2 us are much of the call: a CTA a row, straight from
+// memory, while the first `columns` CTAs add up 64 columns of the weight's gradient each from the inputs, which are read
+// twice for that (dx in the place of one of them: those CTAs are a launch of their own). us, and with a ring and parts:
+//   16 rows of 128 1.8 and 3.2, of 4096 2.6 and 4.0, of 8192 3.3 and 5.4;  128 rows of 128 3.0 and 3.7, of 4096 3.4 and
+//   4.9, of 8192 5.2 and 6.7;  300 rows of 512 5.2 and 4.5, of 2049 5.4 and 8.6, of 4096 5.5 and 6.4, of 8192 9.1 and 8.2
+// (With 256 threads 128 rows of 128 took 4.8, with 1024 128 rows of 4096 4.2; with the matrices' types looked at in the
+// loop, which kept its loads from going out together, 8.9.)
+bool few_rows(int64_t T, int64_t d) { return d <= 8192 && T <= (d > 512 && d <= 4096 ? 2 * sm_count() : 128); }
+constexpr unsigned kFewThreads = 512;  // at least
+constexpr int kFewColumns = 64;
+template <typename Th, typename Td>
+__device__ __forceinline__ void few_columns(const p24_rmsnorm_bwd_args& g, int c, int from, int step, float (&s)[2]) {
+  const int d = static_cast<int>(g.d), T = static_cast<int>(g.T);
+  const Th* h = static_cast<const Th*>(g.h) + c;
+  const Td* dy = static_cast<const Td*>(g.dy) + c;
+  const bool a = c < d, b = c + 32 < d;
+#pragma unroll 8
+  for (int t = from; t < T; t += step) {
+    const float now = g.rstd[t];
+    if (a) s[0] = fmaf(to_float(dy[t * g.lddy]), to_float(h[t * g.ldh]) * now, s[0]);
+    if (b) s[1] = fmaf(to_float(dy[t * g.lddy + 32]), to_float(h[t * g.ldh + 32]) * now, s[1]);
+  }
+}
+template <bool kAligned>
+__global__ void __launch_bounds__(1024) rmsnorm_bwd_few_kernel(const p24_rmsnorm_bwd_args g, const Phase phase, int columns) {
+  __shared__ float part[32];
+  __shared__ float sums[kFewColumns][33];
+  const int d = static_cast<int>(g.d), lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  Pieces<3, 2, 4, kAligned, false> row;
+  const Split<4, kAligned>& sp = row.sp;
+  row.sp.NT = blockDim.x, row.sp.tid = threadIdx.x, row.sp.d = d;
+  row.in[0] = Matrix(g.h, g.ldh, g.h_dtype);
+  row.in[1] = Matrix(g.dy, g.lddy, g.dy_dtype);
+  row.in[2] = Matrix(g.dres, g.ldres, g.r_dtype);
+  pdl_wait();
+  pdl_trigger();
+  if (static_cast<int>(blockIdx.x) < columns) {
+    const int c = blockIdx.x * kFewColumns + lane;
+    float s[2] = {0.f, 0.f};
+    if (row.f32(0)) {
+      if (row.f32(1)) few_columns<float, float>(g, c, warp, warps, s);
+      else few_columns<float, bf16>(g, c, warp, warps, s);
+    } else {
+      if (row.f32(1)) few_columns<bf16, float>(g, c, warp, warps, s);
+      else few_columns<bf16, bf16>(g, c, warp, warps, s);
+    }
+    sums[lane][warp] = s[0], sums[lane + 32][warp] = s[1];
+    __syncthreads();
+    for (int i = warp; i < kFewColumns; i += warps) {
+      const float x = warp_add(lane < warps ? sums[i][lane] : 0.f);
+      if (lane == 0 && blockIdx.x * kFewColumns + i < d) g.dw[blockIdx.x * kFewColumns + i] = x;
+    }
+    return;
+  }
+  const int64_t t = blockIdx.x - columns;
+  const bool with_r = g.dres != nullptr;
+  row.m = with_r ? 3 : 2;
+  row.start(t, kAligned ? 0 : phase.of(t), nullptr);
+  const Matrix out(g.dx, g.lddx, g.dx_dtype);
+  const bool ov = sp.fits(out, t);
+  const float now = g.rstd[t];
+  Vals<4> xh[2], v[2], r[2];
+  float eh = 0.f, eg = 0.f, er = 0.f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    r[i] = filled<4>(0.f);
+    if (!sp.has(i)) continue;
+    xh[i] = row.get(0, i, t), v[i] = row.get(1, i, t);
+    if (with_r) r[i] = row.get(2, i, t);
+  }
+  if (sp.has_edge()) {
+    eh = row.edge(0, t), eg = row.edge(1, t);
+    if (with_r) er = row.edge(2, t);
+  }
+  Weights<2, 4> w;
+  w.start(sp, g.w, g.w_dtype, nullptr);
+  eh *= now, eg *= w.edge;
+  Two dots = both(0.f);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (!sp.has(i)) continue;
+    const Vals<4> wi = w.get(sp, i);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      xh[i].p[k] = xh[i].p[k] * both(now), v[i].p[k] = v[i].p[k] * wi.p[k];
+      dots = fma(v[i].p[k], xh[i].p[k], dots);
+    }
+  }
+  const float mean = cta_add(fmaf(eg, eh, sum_of<4>(dots)), part) / static_cast<float>(d);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (!sp.has(i)) continue;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) v[i].p[k] = fma(both(now), fma(xh[i].p[k], both(-mean), v[i].p[k]), r[i].p[k]);
+    store_vals<4>(out.row(t), out.f32, sp.column(i), ov, v[i]);
+  }
+  if (sp.has_edge()) put_element(out.row(t), out.f32, sp.edge, fmaf(now, fmaf(eh, -mean, eg), er));
+}
+
 // Column sums of the CTAs' parts [G, d]: 32 columns of a CTA, 32 warps that take
 // every 32nd row each. The parts come from L2; 2 to 3 us, most of them the launch and two dependent steps.
 __global__ void __launch_bounds__(1024) dweight_kernel(const float* parts, int G, int d, float* dw) {
@@ -1015,6 +1114,18 @@ cudaError_t launch_rmsnorm_bwd(const p24_rmsnorm_bwd_args& g, float* parts, int*
   int64_t used = 0;
   float* to = g.dw ? parts : nullptr;
   cudaError_t e;
+  if (few_rows(g.T, g.d)) {
+    auto go = [&](unsigned rows, unsigned columns) {
+      const dim3 grid(rows + columns), block(std::max(kFewThreads, static_cast<unsigned>((g.d + 255) / 256 * 32)));
+      e = l.aligned ? launch_pdl(rmsnorm_bwd_few_kernel<true>, grid, block, 0, s, g, l.ph, static_cast<int>(columns))
+                    : launch_pdl(rmsnorm_bwd_few_kernel<false>, grid, block, 0, s, g, l.ph, static_cast<int>(columns));
+      if (e == cudaSuccess) count_launch();
+      return e;
+    };
+    const unsigned rows = static_cast<unsigned>(g.T), columns = g.dw ? static_cast<unsigned>((g.d + kFewColumns - 1) / kFewColumns) : 0;
+    if (columns == 0 || (g.dx != g.h && g.dx != g.dy)) return go(rows, columns);
+    return go(0, columns) != cudaSuccess ? e : go(rows, 0);  // in place: the columns first
+  }
   if (l.wide) e = l.aligned ? launch_bwd<true, 8>(g, l.ph, l.ring, to, status, s, &used) : launch_bwd<false, 8>(g, l.ph, l.ring, to, status, s, &used);
   else e = l.aligned ? launch_bwd<true, 4>(g, l.ph, l.ring, to, status, s, &used) : launch_bwd<false, 4>(g, l.ph, l.ring, to, status, s, &used);
   if (e != cudaSuccess || !g.dw) return e;

@@ -192,3 +192,46 @@ def test_the_gradient_stays_in_its_scratch(P, T, d):
     assert bool((ws[need:] == 90).all())
     xh = h.double() * rstd[:, None]
     check(T, o["dweight"], (dy.double() * xh).sum(0), (T / 152 + 150) * U * (dy.double() * xh).abs().sum(0), "dweight")
+
+
+@pytest.mark.parametrize("T", [1, 2, 9, 31, 127, 128, 129, 304, 305])
+@pytest.mark.parametrize("d", [1, 8, 13, 64, 65, 500, 2049, 4096, 8191, 8192, 8193])
+@pytest.mark.parametrize("h,dy,r,dx,pad,off", [(BF, BF, BF, BF, 0, 0), (F32, BF, F32, F32, 0, 0), (BF, F32, None, BF, 3, 1),
+                                               (F32, F32, BF, BF, 1, 2)])
+def test_the_gradient_of_few_rows(P, T, d, h, dy, r, dx, pad, off):
+    """One launch for few rows, two for more."""
+    g = torch.Generator(device="cuda").manual_seed(T + d)
+    w = 1 + 0.2 * torch.randn(d, generator=g, device="cuda")
+    check_bwd(P, matrix(T, d, dy, g, pad, off, 0.1), matrix(T, d, h, g, pad, off), w,
+              None if r is None else matrix(T, d, r, g, 0, 0, 0.1), dx)
+
+
+@pytest.mark.parametrize("T,d", [(1, 40), (60, 2049), (128, 4096), (128, 8192), (200, 512), (3000, 1001), (1500, 4096), (600, 8191), (9000, 40)])
+@pytest.mark.parametrize("where", ["h", "dy", "dres"])
+def test_the_gradient_in_place(P, T, d, where):
+    """dx in the place of an input, to the rounding of the same with a place of its own; dweight counts the inputs."""
+    g = torch.Generator(device="cuda").manual_seed(T + d)
+    m = {k: matrix(T, d, BF, g) for k in ("h", "dy", "dres")}
+    w = 1 + 0.2 * torch.randn(d, generator=g, device="cuda")
+    rstd = (1 / (m["h"].double().square().mean(1) + 1e-6).sqrt()).float()
+    a = P.p24_rmsnorm_bwd(m["dy"], m["h"], w, rstd, dres=m["dres"])
+    xh = m["h"].double() * rstd.double()[:, None]
+    mass = (m["dy"].double() * xh).abs().sum(0)
+    b = P.p24_rmsnorm_bwd(m["dy"], m["h"], w, rstd, dres=m["dres"], out={"dx": m[where]})
+    assert b["dx"] is m[where]
+    # each is off by check_bwd's bound and half a step. With |g| <= 8, rstd and mean |g xh| <= 1.5 that bound is at most
+    # 1.5 (4u 8 + |xh| (166u 1.5 + 306u 1.5)) + 80u 1.5 (8 + 1.5 |xh|) + 4u 12 < 1300u (1 + |xh|)
+    gap, most = (a["dx"].double() - b["dx"].double()).abs(), a["dx"].double().abs().maximum(b["dx"].double().abs())
+    assert bool((gap <= 2 * (half(BF) * most + 1300 * U * (1 + xh.abs()))).all())
+    check(T, b["dweight"], a["dweight"].double(), 2 * (T / 152 + 150) * U * mass, "dweight")
+
+
+@pytest.mark.parametrize("T,d", [(1, 40), (300, 2049), (3000, 1001), (1500, 4096), (600, 8191), (9000, 40), (300, 20000)])
+def test_the_norm_in_place(P, T, d):
+    """The stream updated in place and the branch overwritten by the norm: the same bits as with places of their own."""
+    g = torch.Generator(device="cuda").manual_seed(T + d)
+    x, r, w = matrix(T, d, BF, g), matrix(T, d, BF, g), torch.randn(d, generator=g, device="cuda")
+    a = P.p24_rmsnorm(x, w, residual=r)
+    b = P.p24_rmsnorm(x, w, residual=r, out={"h": r, "y": x})
+    assert b["h"] is r and b["y"] is x
+    assert torch.equal(a["h"], r) and torch.equal(a["y"], x) and torch.equal(a["rstd"], b["rstd"])
