@@ -3,16 +3,15 @@
 //
 //   Y[t] = scale W[tokens[t]]            dW[v] = scale sum over t with tokens[t] = v of dY[t]
 //
-// The gradient in three launches. First the positions are sorted by token, stably, by one cluster of
-// CTAs (a radix sort by digits of at most 9 bits; whole numbers, so the order is always the same), while
-// the other SMs write zeros to the table's rows that no token names. Then blocks of kept length of the
-// sorted positions are summed, whatever the runs of equal tokens in them are: a frequent token is many
-// blocks' work. A run inside a block goes to its row of the table, a run that crosses blocks leaves its
-// parts in the workspace, and the third launch adds those in the order of the blocks.
+// The gradient in four launches. The positions are sorted by token, stably, by one CTA or a cluster of eight (a radix
+// sort by digits of at most 9 bits; whole numbers, so the order is always the same), while a kernel beside it writes
+// zeros to the table. Then blocks of kept length of the sorted positions are summed, whatever the runs of equal tokens in
+// them are: a frequent token is many blocks' work. A run inside a block goes to its row of the table, a run that crosses
+// blocks leaves its parts in the workspace, and the last launch adds those in the order of the blocks.
 // Sums are fp32, in the order of the positions within a block; no atomics on values.
 //
 // Lookups are bound by memory (16384 x 4096 bf16 to fp32 51 us), the gradient by the zeros where the table is large (the
-// same over 131072 to fp32 366 us, 6.2 TB/s) and by the sort's dependent passes where it is small or narrow (16384 x 128
+// same over 131072 to fp32 325 us, 6.6 TB/s) and by the sort's dependent passes where it is small or narrow (16384 x 128
 // over 5000 25 us, of which the sort is 13).
 #include <algorithm>
 
@@ -63,7 +62,6 @@ __global__ void __launch_bounds__(256) embed_kernel(const p24_embed_args g) {
 constexpr int kSortThreads = 1024, kSortWarps = 32, kDigit = 9, kBins = 1 << kDigit;
 constexpr int kSortCtas = 8;          // the portable cluster size
 constexpr int kHeld = 4;
-constexpr int kFillRows = 1 << 17;    // rows of the table that a CTA looks at together: a bit each
 
 struct SortShared {
   uint32_t count[kSortWarps][kBins];  // a warp's elements with each digit; then where its next one goes
@@ -202,60 +200,71 @@ __device__ __forceinline__ void rank_tokens(const int32_t* tokens, int T, int64_
   to[place] = make_int2(mine, tid);
 }
 
-// `n` bytes of zeros, by `lanes` threads: what lies between 16-byte boundaries by bulk copies from `zeros` in shared memory
-// (16384 x 4096 over 131072, fp32: 385 us, with stores 398; 5000 x 5001 over 50257 205 and 227).
-constexpr int kZeros = 8192;
-__device__ __forceinline__ void zero_row(uint8_t* p, int64_t n, int unit, const uint8_t* zeros, int lane, int lanes) {
-  const int64_t head = min(n, static_cast<int64_t>((16 - (reinterpret_cast<uintptr_t>(p) & 15u)) & 15u));
-  const int64_t body = (n - head) & ~int64_t(15), tail = head + body;
-  const int64_t ends = (head + n - tail) / unit;
-  for (int e = lane; e < ends; e += lanes) {
-    const int64_t at = e * unit < head ? e * unit : tail + e * unit - head;
-    if (unit == 2) *reinterpret_cast<uint16_t*>(p + at) = 0;
-    else *reinterpret_cast<uint32_t*>(p + at) = 0;
-  }
-  for (int64_t i = static_cast<int64_t>(lane) * kZeros; i < body; i += static_cast<int64_t>(lanes) * kZeros)
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(p + head + i), "r"(smem_u32(zeros)),
-                 "r"(static_cast<uint32_t>(min(body - i, static_cast<int64_t>(kZeros))))
-                 : "memory");
-}
-
-// CTAs [0, ctas): the sort. The others: zeros for the table's rows without a token.
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const p24_embed_bwd_args g, int bits, int passes, int ctas, int2* a, int2* b) {
   extern __shared__ __align__(16) uint8_t raw[];
   pdl_wait();
   pdl_trigger();
-  if (static_cast<int>(blockIdx.x) < ctas) {
-    if (g.T <= kFewTokens) rank_tokens(g.tokens, static_cast<int>(g.T), g.V, a, reinterpret_cast<int*>(raw));
-    else sort_tokens(g.tokens, g.T, g.V, bits, passes, a, b, blockIdx.x, ctas, *reinterpret_cast<SortShared*>(raw));
-    return;
-  }
-  uint32_t* used = reinterpret_cast<uint32_t*>(raw);
-  uint8_t* zeros = raw + kFillRows / 8;
-  for (int i = threadIdx.x; i < kZeros / 16; i += kSortThreads) reinterpret_cast<uint4*>(zeros)[i] = make_uint4(0, 0, 0, 0);
-  fence_proxy_async_smem();  // the bulk copies read them; the barrier below comes before the first
-  const int64_t fills = gridDim.x - ctas, f = blockIdx.x - ctas;
-  const int64_t end = g.V * (f + 1) / fills;
-  const int unit = g.dw_dtype == P24_BF16 ? 2 : 4;
-  for (int64_t lo = g.V * f / fills; lo < end; lo += kFillRows) {
-    const int rows = static_cast<int>(min(end - lo, static_cast<int64_t>(kFillRows)));
-    __syncthreads();
-    for (int i = threadIdx.x; i < (rows + 31) / 32; i += kSortThreads) used[i] = 0;
-    __syncthreads();
+  if (g.T <= kFewTokens) rank_tokens(g.tokens, static_cast<int>(g.T), g.V, a, reinterpret_cast<int*>(raw));
+  else sort_tokens(g.tokens, g.T, g.V, bits, passes, a, b, blockIdx.x, ctas, *reinterpret_cast<SortShared*>(raw));
+}
+
+// ---------------------------------------------------------------- zeros
+// `n` bytes of zeros by `threads` threads, of which this is the i-th: 16 bytes at a time between boundaries of 128.
+__device__ __forceinline__ void zero_bytes(uint8_t* p, int64_t n, int unit, int i, int threads) {
+  const int64_t head = min(n, static_cast<int64_t>((128 - (reinterpret_cast<uintptr_t>(p) & 127u)) & 127u));
+  const int64_t vecs = (n - head) / 16, tail = head + vecs * 16;
 #pragma unroll 4
-    for (int64_t t = threadIdx.x; t < g.T; t += kSortThreads) {
-      const int64_t v = g.tokens[t] - lo;
-      if (v >= 0 && v < rows) atomicOr(&used[v >> 5], 1u << (v & 31));
-    }
-    __syncthreads();
-    // a warp a row, or a thread where that is one copy (8192 x 128 over 131072: 13 us against 21)
-    const bool alone = g.d * unit <= kZeros / 4;
-    const int lane = alone ? 0 : threadIdx.x & 31, lanes = alone ? 1 : 32;
-    for (int i = threadIdx.x / lanes; i < rows; i += kSortThreads / lanes)
-      if (!(used[i >> 5] >> (i & 31) & 1))
-        zero_row(static_cast<uint8_t*>(g.dW) + (lo + i) * g.lddw * unit, g.d * unit, unit, zeros, lane, lanes);
+  for (int64_t k = i; k < vecs; k += threads) reinterpret_cast<uint4*>(p + head)[k] = make_uint4(0, 0, 0, 0);
+  for (int64_t e = static_cast<int64_t>(i) * unit; e < head + n - tail; e += threads * unit) {
+    uint8_t* at = p + (e < head ? e : tail + e - head);
+    if (unit == 2) *reinterpret_cast<uint16_t*>(at) = 0;
+    else *reinterpret_cast<uint32_t*>(at) = 0;
   }
-  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+// A table's zeros, its rows with a token among them: many small CTAs, which the hardware starts in the order of memory.
+// (1 GB in 141 us, 7.6 TB/s; by CTAs that stay and take every n-th piece, stores or bulk copies of any size, 157 to 171.
+// Zeros for the rows without a token only, from the SMs that do not sort: 16384 x 4096 over 131072, fp32, 371 us, like
+// this 325; over 32000 121 and 117; 2000 x 2000 over 8000, bf16, 21.4 and 22.4.) It needs nothing of the sort's that was
+// launched before it and does not wait for it: all of the sort's CTAs had waited for what came before them when they let
+// this kernel start. But the sums, which wait for this one, need the sort: the last CTA here waits for it at its end.
+// `first`: there was no sort.
+constexpr int kZeroThreads = 256, kZeroBytes = kZeroThreads * 4 * 16;
+struct Zeros {
+  uint8_t* p;
+  int64_t n;         // bytes, of a row where there are rows
+  int64_t rows, ld;  // rows of a table with gaps, bytes from one to the next; or 0
+  int each;          // rows of a CTA
+  int unit;
+  bool first;
+};
+__global__ void __launch_bounds__(kZeroThreads) embed_zero_kernel(const Zeros z) {
+  if (z.first) pdl_wait();
+  pdl_trigger();
+  if (z.rows == 0) {
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * kZeroBytes - (blockIdx.x ? reinterpret_cast<uintptr_t>(z.p) & 127u : 0);
+    const int64_t end = static_cast<int64_t>(blockIdx.x + 1) * kZeroBytes - (reinterpret_cast<uintptr_t>(z.p) & 127u);
+    zero_bytes(z.p + at, min(end, z.n) - at, z.unit, threadIdx.x, kZeroThreads);
+  } else {
+    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * z.each, end = min(r0 + z.each, z.rows);
+    for (int64_t r = r0 + (threadIdx.x >> 5); r < end; r += kZeroThreads / 32)
+      zero_bytes(z.p + r * z.ld, z.n, z.unit, threadIdx.x & 31, 32);
+  }
+  if (!z.first && blockIdx.x == gridDim.x - 1) pdl_wait();
+}
+
+cudaError_t launch_zeros(const p24_embed_bwd_args& g, cudaStream_t s) {
+  const int unit = size_of(g.dw_dtype);
+  const int64_t bytes = g.d * unit;
+  Zeros z{static_cast<uint8_t*>(g.dW), bytes, g.V, g.lddw * unit, static_cast<int>(8 * std::max<int64_t>(1, 2048 / bytes)), unit, g.T == 0};
+  int64_t grid = (g.V + z.each - 1) / z.each;
+  if (g.lddw == g.d || g.V == 1) {
+    z.n = g.V * bytes, z.rows = 0;
+    grid = (z.n + (reinterpret_cast<uintptr_t>(z.p) & 127u) + kZeroBytes - 1) / kZeroBytes;
+  }
+  const cudaError_t e = launch_pdl(embed_zero_kernel, dim3(static_cast<unsigned>(grid)), dim3(kZeroThreads), 0, s, z);
+  if (e == cudaSuccess) count_launch();
+  return e;
 }
 
 // ---------------------------------------------------------------- sums
@@ -451,6 +460,7 @@ cudaError_t launch_embed(const p24_embed_args& g, cudaStream_t s) {
 }
 
 cudaError_t launch_embed_bwd(const p24_embed_bwd_args& g, void* ws, cudaStream_t s) {
+  if (g.T == 0) return launch_zeros(g, s);
   SumArgs a{g, nullptr, nullptr, wide_of(g.d), block_length(g.T, g.d)};
   int2* first = static_cast<int2*>(ws);
   int2* second = reinterpret_cast<int2*>(static_cast<uint8_t*>(ws) + sort_bytes(g.T));
@@ -459,21 +469,15 @@ cudaError_t launch_embed_bwd(const p24_embed_bwd_args& g, void* ws, cudaStream_t
   int total = 1;  // of the keys 0..V
   while (g.V >> total) ++total;
   const int passes = (total + kDigit - 1) / kDigit, bits = (total + passes - 1) / passes;
-  // One CTA, or a cluster of 8: 1024 tokens 9 us and 12, 4096 17 and 12, 16384 46 and 14. But beside a cluster fewer
-  // CTAs fit to write the zeros, so where those take longer anyway one sorts: 16384 x 4096 over 131072, fp32, 398 us
-  // with the cluster, 372 without. (6 TB/s of zeros; 10 us and 2.4 ns a token.)
-  const double zeros_us = g.accumulate ? 0.0 : static_cast<double>(g.V) * g.d * size_of(g.dw_dtype) / 6e6;
-  const int ctas = g.T <= 1024 || 10.0 + 2.4e-3 * g.T < zeros_us ? 1 : kSortCtas;
+  // One CTA, or a cluster of 8: 1024 tokens 9 us and 12, 4096 17 and 12, 16384 46 and 14.
+  const int ctas = g.T <= 1024 ? 1 : kSortCtas;
   const void* kern = reinterpret_cast<const void*>(embed_sort_kernel);
   int slots = 0;
-  static_assert(sizeof(SortShared) % 16 == 0 && sizeof(SortShared) >= kFillRows / 8 + kZeros, "the fill's shared memory");
   const size_t smem = sizeof(SortShared);
   cudaError_t e = row_kernel_slots(kern, kSortThreads, ctas, smem, &slots);
   if (e != cudaSuccess) return e;
-  // one cluster sorts; the others, as many as fit, write zeros
-  const int64_t grid = (g.accumulate ? 1 : std::max<int64_t>(2, slots)) * ctas;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kSortThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -488,7 +492,7 @@ cudaError_t launch_embed_bwd(const p24_embed_bwd_args& g, void* ws, cudaStream_t
   e = cudaLaunchKernelEx(&cfg, embed_sort_kernel, g, bits, passes, ctas, first, second);
   if (e != cudaSuccess) return e;
   count_launch();
-  if (g.T == 0) return cudaSuccess;
+  if (!g.accumulate && (e = launch_zeros(g, s)) != cudaSuccess) return e;
   if (g.dy_dtype == P24_BF16) return g.dw_dtype == P24_BF16 ? launch_sums<bf16, bf16>(a, s) : launch_sums<bf16, float>(a, s);
   return g.dw_dtype == P24_BF16 ? launch_sums<float, bf16>(a, s) : launch_sums<float, float>(a, s);
 }

@@ -172,3 +172,21 @@ def test_refusals_of_the_binding(P):
                       (lambda: P.p24_embed_bwd(W[:2], t, 5, dW=W[:4]), ValueError)):
         with pytest.raises(err):
             call()
+
+
+@pytest.mark.parametrize("V", [1, 63, 64, 65, 4095, 8129, 8192, 8193, 16390, 40000])
+@pytest.mark.parametrize("off", [0, 1, 37, 64])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("gap", [0, 3])
+def test_zeros_end_where_the_table_does(P, V, off, dt, gap):
+    """Tables whose first and last bytes lie anywhere between boundaries, with gaps between rows or without, and guards."""
+    for T in (0, 3):
+        flat = torch.full((off + V * (1 + gap) + 70,), 7.0, dtype=dt, device="cuda")
+        dW = flat[off:off + V * (1 + gap)].view(V, 1 + gap)[:, :1]
+        tok = torch.full((T,), V - 1, dtype=torch.int32, device="cuda")
+        P.p24_embed_bwd(torch.ones((T, 1), dtype=dt, device="cuda"), tok, V, dW=dW)
+        want = torch.zeros((V, 1), dtype=dt, device="cuda")
+        want[V - 1] = T
+        assert torch.equal(dW, want)
+        dW.fill_(7.0)
+        assert bool((flat == 7.0).all())
