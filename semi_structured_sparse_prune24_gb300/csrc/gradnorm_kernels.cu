@@ -3,7 +3,7 @@
 //
 //   norm = sqrt(sum over all tensors and elements of g^2);   g <- g min(1, max_norm / norm)
 //
-// The bound is memory: 743 MB of bf16 and fp32 in 106 us (7.0 TB/s), scaled into other tensors in 348 in all (6.4). The
+// The bound is memory: 743 MB of bf16 and fp32 in 106 us (7.0 TB/s), scaled into other tensors in 330 in all (6.8). The
 // tensors are cut into chunks of 4 to 32 KB; CTA b of a fixed grid takes chunks b, b + grid, ... (a stretch of
 // neighbouring ones each read as fast, but scaled 743 MB in 246 us instead of 226). A thread squares and adds the
 // elements of a chunk in fp32, and chunks, threads and CTAs are added as pairs of fp32 numbers, a sum and what its
@@ -219,15 +219,28 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const Sum* sums, in
   if (threadIdx.x == 0) *norm = x;
 }
 
-template <int N>
+// kLong: a CTA a chunk, started by the hardware in the order of memory, and the norm is there already. Else the CTAs that
+// run at once take the chunks in turn, and each finds the norm from the sums: a launch less. (743 MB 348 us by CTAs that
+// stay, 342 by 4 times as many, 330 by one a chunk; 84 MB 36 either way, 16 MB 10.9 and 11.3.)
+constexpr int64_t kLongBytes = 80 << 20;
+template <int N, bool kLong>
 __global__ void __launch_bounds__(kThreads, kCtas) grad_scale_kernel(const __grid_constant__ Table<N> t, const Sum* sums, int n,
                                                               float max_norm, float* norm) {
   __shared__ SumShared sh;
-  int at = t.last[blockIdx.x];
+  int at = 0;
+  if (kLong) {
+    for (int hi = t.count; hi - at > 1;) {
+      const int mid = (at + hi) >> 1;
+      if (t.e[mid].chunk <= t.chunks - 1 - static_cast<int>(blockIdx.x)) at = mid;
+      else hi = mid;
+    }
+  } else {
+    at = t.last[blockIdx.x];
+  }
   pdl_wait();
   pdl_trigger();
-  const float x = norm_of(sums, n, sh);
-  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = x;
+  const float x = kLong ? *norm : norm_of(sums, n, sh);
+  if (!kLong && norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = x;
   const bool over = x > max_norm && x < __int_as_float(0x7f800000);  // a norm that is no number scales nothing
   const float f = over ? max_norm / x : 1.f;
   for (int c = t.chunks - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x) {
@@ -319,7 +332,7 @@ template <int N>
 cudaError_t run_list(const p24_tensor* g, const p24_tensor* out, int64_t n, bool scale, float max_norm, float* norm, Sum* sums,
                      cudaStream_t s) {
   Table<N> t;
-  int64_t used = 0;
+  int64_t used = 0, bytes = 0;
   cudaError_t e;
   for (int64_t i = 0; i < n;) {
     i = fill_table(t, g, nullptr, n, i);
@@ -328,29 +341,32 @@ cudaError_t run_list(const p24_tensor* g, const p24_tensor* out, int64_t n, bool
     if (e != cudaSuccess) return e;
     count_launch();
     used += t.ctas;
+    bytes += static_cast<int64_t>(t.chunks) * t.vecs * 16;
   }
-  if (scale && used > 0) {
-    for (int64_t i = 0; i < n;) {
-      i = fill_table(t, g, out, n, i);
-      if (t.chunks == 0) continue;
-      e = launch_pdl(grad_scale_kernel<N>, dim3(static_cast<unsigned>(t.ctas)), dim3(kThreads), 0, s, t, static_cast<const Sum*>(sums),
-                     static_cast<int>(used), max_norm, norm);
-      if (e != cudaSuccess) return e;
-      count_launch();
-    }
-    return cudaSuccess;
+  const bool longer = scale && bytes > kLongBytes;
+  if (longer && !norm) norm = reinterpret_cast<float*>(sums + used);
+  if ((!scale || longer || used == 0) && norm) {
+    e = launch_pdl(grad_norm_kernel, dim3(1), dim3(kThreads), 0, s, static_cast<const Sum*>(sums), static_cast<int>(used), norm);
+    if (e != cudaSuccess) return e;
+    count_launch();
   }
-  if (!norm) return cudaSuccess;  // an empty list, and no norm asked for
-  e = launch_pdl(grad_norm_kernel, dim3(1), dim3(kThreads), 0, s, static_cast<const Sum*>(sums), static_cast<int>(used), norm);
-  if (e == cudaSuccess) count_launch();
-  return e;
+  for (int64_t i = scale && used > 0 ? 0 : n; i < n;) {
+    i = fill_table(t, g, out, n, i);
+    if (t.chunks == 0) continue;
+    const auto kern = longer ? grad_scale_kernel<N, true> : grad_scale_kernel<N, false>;
+    e = launch_pdl(kern, dim3(static_cast<unsigned>(longer ? t.chunks : t.ctas)), dim3(kThreads), 0, s, t, static_cast<const Sum*>(sums),
+                   static_cast<int>(used), max_norm, norm);
+    if (e != cudaSuccess) return e;
+    count_launch();
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
 
-// A sum for each CTA of the launches that a list of n tensors takes.
+// A sum for each CTA of the launches that a list of n tensors takes, and one for the norm where there is no place for it.
 size_t grad_norm_workspace(int64_t n) {
-  return static_cast<size_t>(std::max<int64_t>(1, (n + kMostTable - 1) / kMostTable) * grid_most()) * sizeof(Sum);
+  return static_cast<size_t>(std::max<int64_t>(1, (n + kMostTable - 1) / kMostTable) * grid_most() + 1) * sizeof(Sum);
 }
 
 cudaError_t launch_grad_norm(const p24_tensor* g, const p24_tensor* out, int64_t n, bool scale, float max_norm, float* norm,

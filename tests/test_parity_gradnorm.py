@@ -207,3 +207,36 @@ def test_many_sums_at_the_upper_end(P, e):
     of two, so every sum is exact."""
     x = torch.full((1 << 30,), 2.0 ** e, dtype=BF, device="cuda")
     assert float(P.p24_grad_norm([x] * 16)) == 2.0 ** (e + 17)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("given", [False, True])
+def test_long_lists(P, dt, given):
+    """More than 80 MB, of tensors that end inside chunks, lie at odd offsets and are empty: clipped in place and into
+    others, with a place for the norm and through the C call without one."""
+    import ctypes as C
+    from semi_structured_sparse_prune24_gb300 import _native as N
+    g = torch.Generator(device="cuda").manual_seed(3)
+    flat = torch.randn(40_000_000 if dt == F32 else 60_000_000, generator=g, device="cuda").to(dt)
+    cuts = [0, 1, 12, 5000, 5001, 2_000_003, 2_000_003, 20_000_000, 20_000_017, flat.numel()]
+    grads = [flat[a:b] for a, b in zip(cuts, cuts[1:])]
+    want = float(flat.double().square().sum().sqrt())
+    f = 0.25
+    out = [torch.empty_like(t) for t in grads]
+    if given:
+        norm = P.p24_clip_grads(grads, 0.25 * want, out=out)
+        assert abs(float(norm) - want) <= 70 * U * want
+        f = 0.25 * want / float(norm)
+    else:
+        ws = torch.empty(int(N.lib.p24_grad_norm_workspace_size(len(grads))), dtype=torch.uint8, device="cuda")
+        lists = [(N.p24_tensor * len(ts))(*[N.p24_tensor(t.data_ptr(), t.numel(), N.P24_F32 if dt == F32 else N.P24_BF16) for t in ts])
+                 for ts in (grads, out)]
+        rc = N.lib.p24_clip_grads(C.addressof(lists[0]), C.addressof(lists[1]), len(grads), 0.25 * want, None, ws.data_ptr(),
+                                  ws.numel(), torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+    e = torch.finfo(dt).eps / 2
+    for t, o in zip(grads, out):
+        w = t.double() * f
+        assert bool(((o.double() - w).abs() <= (75 * U + e) * w.abs() + TINY[dt]).all())
+    P.p24_clip_grads(grads, 0.25 * want)
+    assert all(torch.equal(t, o) for t, o in zip(grads, out))
