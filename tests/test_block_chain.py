@@ -98,3 +98,36 @@ def test_two_streams_at_once(P):
     torch.cuda.synchronize()
     for o, w in zip(got, want):
         assert all(torch.equal(x, y) for x, y in zip(o, w))
+
+
+def test_tables_gradients_back_to_back(P):
+    """A table's gradient read, scaled, written by another kernel and made again, without a wait on the host between: its
+    zeros overtake nothing that came before them, and what comes after finds the sums."""
+    g = torch.Generator(device="cuda").manual_seed(11)
+    V, d = 40000, 1000
+    dW = torch.empty((V, d), dtype=torch.bfloat16, device="cuda")
+    runs = []
+    for T in (1, 300, 5000):
+        tok = torch.randint(0, V, (T,), generator=g, device="cuda").int()
+        dY = torch.randn((T, d), generator=g, device="cuda").bfloat16()
+        table = P.p24_embed_bwd(dY, tok, V)
+        torch.cuda.synchronize()
+        norm = P.p24_grad_norm([table])
+        clipped = table.clone()
+        P.p24_clip_grads([clipped], 1.0)
+        torch.cuda.synchronize()
+        runs.append((tok, dY, table, norm, clipped))
+    got = []
+    for k in range(30):
+        tok, dY = runs[k % 3][:2]
+        P.p24_embed_bwd(dY, tok, V, dW=dW)
+        got.append((P.p24_grad_norm([dW]), P.p24_embed(tok, dW), P.p24_clip_grads([dW], 1.0), P.p24_embed(tok, dW)))
+        if k % 7 == 3:
+            dW.fill_(float("nan"))
+        elif k % 7 == 5:
+            P.p24_rmsnorm(dY, None, out={"y": dW[:len(dY)]})
+    torch.cuda.synchronize()
+    for k, (norm, rows, again, scaled) in enumerate(got):
+        tok, _, table, want, clipped = runs[k % 3]
+        assert torch.equal(norm, want) and torch.equal(again, want)
+        assert torch.equal(rows, table[tok.long()]) and torch.equal(scaled, clipped[tok.long()])
