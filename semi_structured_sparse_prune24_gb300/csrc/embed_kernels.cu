@@ -3,11 +3,11 @@
 //
 //   Y[t] = scale W[tokens[t]]            dW[v] = scale sum over t with tokens[t] = v of dY[t]
 //
-// The gradient in four launches. The positions are sorted by token, stably, by one CTA or a cluster of eight (a radix
-// sort by digits of at most 9 bits; whole numbers, so the order is always the same), while a kernel beside it writes
-// zeros to the table. Then blocks of kept length of the sorted positions are summed, whatever the runs of equal tokens in
-// them are: a frequent token is many blocks' work. A run inside a block goes to its row of the table, a run that crosses
-// blocks leaves its parts in the workspace, and the last launch adds those in the order of the blocks.
+// The gradient in four launches. The positions are sorted by token, stably, by a cluster of eight CTAs (a radix sort by
+// digits of at most 9 bits) or, if they are few, by counting; whole numbers, so the order is always the same. A kernel
+// beside that writes zeros to the table. Then blocks of kept length of the sorted positions are summed, whatever the runs
+// of equal tokens in them are: a frequent token is many blocks' work. A run inside a block goes to its row of the table,
+// a run that crosses blocks leaves its parts in the workspace, and the last launch adds those in the order of the blocks.
 // Sums are fp32, in the order of the positions within a block; no atomics on values.
 //
 // Lookups are bound by memory (16384 x 4096 bf16 to fp32 51 us), the gradient by the zeros where the table is large (the
@@ -79,12 +79,12 @@ __device__ __forceinline__ uint32_t load_cta(const uint32_t* p, int rank) {
   return v;
 }
 
-// (token, position), by token; a token outside 0..V-1 is V. `ctas`: those that sort, one cluster, through a and b.
-// (16384 tokens over 5000: one CTA 46 us, a cluster of 8 14.)
+// (token, position), by token; a token outside 0..V-1 is V. By a cluster, through a and b. (16384 tokens over 5000: one CTA
+// 46 us, a cluster of 8 14.)
 __device__ __forceinline__ void sort_tokens(const int32_t* tokens, int64_t T, int64_t V, int bits, int passes, int2* a, int2* b,
-                                            int rank, int ctas, SortShared& sh) {
+                                            int rank, SortShared& sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t warps = static_cast<int64_t>(ctas) * kSortWarps;
+  const int64_t warps = static_cast<int64_t>(kSortCtas) * kSortWarps;
   const int64_t span = (T + warps * 32 - 1) / (warps * 32) * 32;
   const int64_t lo = (static_cast<int64_t>(rank) * kSortWarps + warp) * span, hi = min(T, lo + span);
   const int bins = 1 << bits;
@@ -130,17 +130,15 @@ __device__ __forceinline__ void sort_tokens(const int32_t* tokens, int64_t T, in
       }
       sh.total[tid] = mine;
     }
-    uint32_t before = 0, all = mine;
-    if (ctas > 1) {
-      cluster_barrier_all();
-      all = 0;
-      if (tid < bins)
-        for (int r = 0; r < ctas; ++r) {
-          const uint32_t n = load_cta(&sh.total[tid], r);
-          if (r < rank) before += n;
-          all += n;
-        }
-    }
+    uint32_t before = 0, all = 0;
+    cluster_barrier_all();
+    if (tid < bins)
+#pragma unroll
+      for (int r = 0; r < kSortCtas; ++r) {
+        const uint32_t n = load_cta(&sh.total[tid], r);
+        if (r < rank) before += n;
+        all += n;
+      }
     // exclusive sums over the digits
     uint32_t up = all;
 #pragma unroll
@@ -173,39 +171,45 @@ __device__ __forceinline__ void sort_tokens(const int32_t* tokens, int64_t T, in
       }
     }
     // the others' elements are there, and their totals read, before the next pass
-    if (ctas > 1) cluster_barrier_all();
-    else __syncthreads();
+    cluster_barrier_all();
   }
 }
 
-// The same for few tokens, by one CTA: an element's place is the number of those before it. (256 tokens over a
-// vocabulary of 2000: 3.8 us against 6.0 by digits.)
-constexpr int kFewTokens = 256;
-__device__ __forceinline__ void rank_tokens(const int32_t* tokens, int T, int64_t V, int2* to, int* keys) {
-  const int tid = threadIdx.x, padded = (T + 3) / 4 * 4;
-  if (tid < padded) {
-    const int32_t v = tid < T ? tokens[tid] : 0;
-    keys[tid] = tid < T ? (v >= 0 && v < V ? v : static_cast<int>(V)) : 0x7fffffff;
-  }
-  __syncthreads();
-  if (tid >= T) return;
-  const int mine = keys[tid];
-  int place = 0;
-#pragma unroll 4
-  for (int j = 0; j < padded; j += 4) {
-    const int4 k = *reinterpret_cast<const int4*>(keys + j);
-    place += (k.x < mine || (k.x == mine && j < tid)) + (k.y < mine || (k.y == mine && j + 1 < tid)) +
-             (k.z < mine || (k.z == mine && j + 2 < tid)) + (k.w < mine || (k.w == mine && j + 3 < tid));
-  }
-  to[place] = make_int2(mine, tid);
-}
-
-__global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const p24_embed_bwd_args g, int bits, int passes, int ctas, int2* a, int2* b) {
+__global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const p24_embed_bwd_args g, int bits, int passes, int2* a, int2* b) {
   extern __shared__ __align__(16) uint8_t raw[];
   pdl_wait();
   pdl_trigger();
-  if (g.T <= kFewTokens) rank_tokens(g.tokens, static_cast<int>(g.T), g.V, a, reinterpret_cast<int*>(raw));
-  else sort_tokens(g.tokens, g.T, g.V, bits, passes, a, b, blockIdx.x, ctas, *reinterpret_cast<SortShared*>(raw));
+  sort_tokens(g.tokens, g.T, g.V, bits, passes, a, b, blockIdx.x, *reinterpret_cast<SortShared*>(raw));
+}
+
+// The same for fewer tokens, a warp each: an element's place is the number of those before it. (The whole gradient of 300 x
+// 1000 bf16 over 2000 6.9 us, by one CTA 10.2; of 1000 x 4 over 131072 8.4 and 15.1; of 4000 x 1000 over 8000 18.1, by a
+// cluster 21.0; of 8192 x 1024 over 32000 31.3 and 27.4.)
+constexpr int kRankMost = 4096, kRankThreads = 1024;
+__device__ __forceinline__ int below(const int4& k, int x) { return (k.x < x) + (k.y < x) + (k.z < x) + (k.w < x); }
+__global__ void __launch_bounds__(kRankThreads) embed_rank_kernel(const int32_t* tokens, int T, int V, int2* to) {
+  extern __shared__ __align__(16) int keys[];
+  const int lane = threadIdx.x & 31, me = blockIdx.x * (kRankThreads / 32) + (threadIdx.x >> 5), chunks = (T + 127) / 128;
+  pdl_wait();
+  pdl_trigger();
+  for (int i = threadIdx.x; i < chunks * 128; i += kRankThreads) {
+    const int32_t v = i < T ? tokens[i] : 0x7fffffff;
+    keys[i] = i < T ? (v >= 0 && v < V ? v : V) : 0x7fffffff;
+  }
+  __syncthreads();
+  if (me >= T) return;
+  const int mine = keys[me], own = me / 128;
+  const int4* q = reinterpret_cast<const int4*>(keys) + lane;
+  int place = 0;
+#pragma unroll 4
+  for (int c = 0; c < own; ++c) place += below(q[32 * c], mine + 1);  // equal ones are before it
+  const int4 k = q[32 * own];
+  const int before = me - (128 * own + 4 * lane);  // of these four
+  place += (k.x < mine + (before > 0)) + (k.y < mine + (before > 1)) + (k.z < mine + (before > 2)) + (k.w < mine + (before > 3));
+#pragma unroll 4
+  for (int c = own + 1; c < chunks; ++c) place += below(q[32 * c], mine);
+  place = __reduce_add_sync(~0u, place);
+  if (lane == 0) to[place] = make_int2(mine, me);
 }
 
 // ---------------------------------------------------------------- zeros
@@ -466,30 +470,37 @@ cudaError_t launch_embed_bwd(const p24_embed_bwd_args& g, void* ws, cudaStream_t
   int2* second = reinterpret_cast<int2*>(static_cast<uint8_t*>(ws) + sort_bytes(g.T));
   a.sorted = first;
   a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 2 * sort_bytes(g.T));
-  int total = 1;  // of the keys 0..V
-  while (g.V >> total) ++total;
-  const int passes = (total + kDigit - 1) / kDigit, bits = (total + passes - 1) / passes;
-  // One CTA, or a cluster of 8: 1024 tokens 9 us and 12, 4096 17 and 12, 16384 46 and 14.
-  const int ctas = g.T <= 1024 ? 1 : kSortCtas;
-  const void* kern = reinterpret_cast<const void*>(embed_sort_kernel);
-  int slots = 0;
-  const size_t smem = sizeof(SortShared);
-  cudaError_t e = row_kernel_slots(kern, kSortThreads, ctas, smem, &slots);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(kSortThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(ctas);
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = ctas > 1 ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, embed_sort_kernel, g, bits, passes, ctas, first, second);
+  // Few tokens are ranked, up to 4096 where the sort would not be hidden behind the zeros (at 7.5 TB/s): it takes one
+  // cluster and leaves the other SMs to them.
+  const double zeros_us = g.accumulate ? 0.0 : static_cast<double>(g.V) * g.d * size_of(g.dw_dtype) / 7.5e6;
+  cudaError_t e;
+  if (g.T <= kRankMost / 2 || (g.T <= kRankMost && zeros_us < 14.0)) {
+    const int T = static_cast<int>(g.T), warps = kRankThreads / 32;
+    e = launch_pdl(embed_rank_kernel, dim3((T + warps - 1) / warps), dim3(kRankThreads), static_cast<size_t>((T + 127) / 128 * 128) * sizeof(int),
+                   s, g.tokens, T, static_cast<int>(g.V), first);
+  } else {
+    int total = 1;  // of the keys 0..V
+    while (g.V >> total) ++total;
+    const int passes = (total + kDigit - 1) / kDigit, bits = (total + passes - 1) / passes;
+    int slots = 0;
+    const size_t smem = sizeof(SortShared);
+    e = row_kernel_slots(reinterpret_cast<const void*>(embed_sort_kernel), kSortThreads, kSortCtas, smem, &slots);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kSortCtas);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kSortCtas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, embed_sort_kernel, g, bits, passes, first, second);
+  }
   if (e != cudaSuccess) return e;
   count_launch();
   if (!g.accumulate && (e = launch_zeros(g, s)) != cudaSuccess) return e;

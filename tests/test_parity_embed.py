@@ -190,3 +190,19 @@ def test_zeros_end_where_the_table_does(P, V, off, dt, gap):
         assert torch.equal(dW, want)
         dW.fill_(7.0)
         assert bool((flat == 7.0).all())
+
+
+@pytest.mark.parametrize("T", [1, 2, 31, 32, 33, 127, 128, 129, 255, 1000, 2047, 2048, 2049, 4095, 4096, 4097, 8192, 20000])
+@pytest.mark.parametrize("V,d", [(3, 8), (500, 9), (60000, 1), (60000, 520)])
+def test_every_way_to_sort(P, T, V, d):
+    """Tokens ranked by a warp each, or sorted by a cluster, by their number and the table's size. Whole numbers, whose sums
+    are exact in fp32 in any order; frequent tokens, and padding on both sides."""
+    g = torch.Generator(device="cuda").manual_seed(T + V)
+    tok = (torch.rand(T, generator=g, device="cuda") ** 4 * (V + 2)).int() - 1
+    dY = torch.randint(-8, 9, (T, d), generator=g, device="cuda").float()
+    want = torch.zeros((V + 2, d), device="cuda", dtype=torch.float64)
+    want.index_add_(0, tok.long() + 1, dY.double())
+    want = want[1:V + 1].float()
+    assert torch.equal(P.p24_embed_bwd(dY, tok, V), want)
+    old = torch.randint(-8, 9, (V, d), generator=g, device="cuda").float()
+    assert torch.equal(P.p24_embed_bwd(dY, tok, V, dW=old.clone(), accumulate=True), want + old)
