@@ -347,12 +347,49 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3) |
          static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3)) << 16;
 }
-// Of values times a factor.
+// A scale from the largest magnitude: a 448th of it, rounded once (the product with 1/448 and one step of refinement
+// give that for each of the 2^23 fractions), and no less than 2^-118, below which its reciprocal leaves fp32's range.
+__device__ __forceinline__ float scale_of(float top) {
+  if (top == 0.f) return 1.f;
+  const float s = top * (1.f / 448.f);
+  return max_nan(s < __int_as_float(0x7f800000) ? fmaf(fmaf(s, -448.f, top), 1.f / 448.f, s) : s, 0x1p-118f);
+}
+// What values are divided by, a scale. A quotient is the value times an approximate reciprocal, off by some units in the
+// last place, and a step of refinement: the remainder is exact or off by 2^-22 of such a unit, so what is rounded in the end
+// is within 2^-20 units of the true quotient, and exactly it where the quotient has few bits, as the midpoint of two codes
+// has. (The product alone is one of the neighbours of a midpoint as often as not.) Values come with their sign turned, which
+// keeps that of zeros. Beside a scale below 2^-90 the remainder would lie among the smallest numbers: both are taken times
+// 2^64. An infinite scale gives 0, and for infinite values NaN; so does a scale that is NaN.
+struct Divisor {
+  float s, neg, up;  // the scale, which the remainder is found with; -1 / scale; 2^64 or 1
+};
+__device__ __forceinline__ Divisor by(float scale) {
+  Divisor v;
+  v.up = scale < 0x1p-90f ? 0x1p64f : 1.f;
+  v.s = scale * v.up;
+  v.neg = -__fdividef(1.f, v.s);
+  if (v.s == __int_as_float(0x7f800000)) v.s = 0.f;
+  return v;
+}
+__device__ __forceinline__ float quotient(float minus, const Divisor& v) {
+  minus *= v.up;
+  const float q = minus * v.neg;
+  return fmaf(fmaf(q, v.s, minus), v.neg, q);
+}
+// Of -a, the columns from `cut` on by another scale than those before it.
 template <int E>
-__device__ __forceinline__ void store_e4m3(uint8_t* row, int c, bool vec, Vals<E> a, float f) {
+__device__ __forceinline__ void store_e4m3(uint8_t* row, int c, bool vec, Vals<E> a, const Divisor& x, const Divisor& y, int cut) {
   float v[E];
+  if (x.up != 1.f || y.up != 1.f) {
 #pragma unroll
-  for (int k = 0; k < E / 2; ++k) a.p[k] = a.p[k] * both(f);
+    for (int k = 0; k < E / 2; ++k) a.p[k] = a.p[k] * two(2 * k < cut ? x.up : y.up, 2 * k + 1 < cut ? x.up : y.up);
+  }
+#pragma unroll
+  for (int k = 0; k < E / 2; ++k) {
+    const Two s = two(2 * k < cut ? x.s : y.s, 2 * k + 1 < cut ? x.s : y.s), neg = two(2 * k < cut ? x.neg : y.neg, 2 * k + 1 < cut ? x.neg : y.neg);
+    const Two q = a.p[k] * neg;
+    a.p[k] = fma(fma(q, s, a.p[k]), neg, q);
+  }
   to_array(a, v);
   uint32_t q[E / 4];
 #pragma unroll
@@ -365,12 +402,11 @@ __device__ __forceinline__ void store_e4m3(uint8_t* row, int c, bool vec, Vals<E
     for (int k = 0; k < E; ++k) row[c + k] = static_cast<uint8_t>(q[k / 4] >> (8 * (k & 3)));
   }
 }
-// A scale and what values are multiplied by, from the largest magnitude. The reciprocal is that of the
-// stored scale, so that code times scale is the nearest to the value that the code allows; below 2^-118
-// a scale's reciprocal leaves fp32's range, and the scale stays there. The reciprocal is the approximate one, a unit
-// in the last place off at most: a value times it is as far off as the product's own rounding twice over.
-__device__ __forceinline__ float scale_of(float top) { return top == 0.f ? 1.f : max_nan(top * (1.f / 448.f), 0x1p-118f); }
-__device__ __forceinline__ float one_over(float scale) { return __fdividef(1.f, scale); }
+template <int E>
+__device__ __forceinline__ void store_e4m3(uint8_t* row, int c, bool vec, const Vals<E>& a, const Divisor& x) {
+  store_e4m3<E>(row, c, vec, a, x, x, E);
+}
+__device__ __forceinline__ uint8_t e4m3(float x) { return static_cast<uint8_t>(e4m3x4(x, 0.f, 0.f, 0.f)); }
 template <int E>
 __device__ __forceinline__ float top_of(const Vals<E>& a) {
   float v[E], top = 0.f;
@@ -515,13 +551,14 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024, kWarp ? (C > 8 ? 3 : 4) : 
       top = 0.f;
     }
     if (g.rstd && sp.tid == 0) g.rstd[t] = rstd;
-    e = e * rstd * w.edge;
+    const float by_rstd = kQuant ? -rstd : rstd;  // codes are made from -y
+    e = e * by_rstd * w.edge;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (!sp.has(i)) continue;
       const Vals<E> wi = w.get(sp, i);
 #pragma unroll
-      for (int k = 0; k < E / 2; ++k) h[i].p[k] = h[i].p[k] * both(rstd) * wi.p[k];
+      for (int k = 0; k < E / 2; ++k) h[i].p[k] = h[i].p[k] * both(by_rstd) * wi.p[k];
     }
     if (!kQuant) {
 #pragma unroll
@@ -542,12 +579,13 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024, kWarp ? (C > 8 ? 3 : 4) : 
         for (int i = 0; i < NV; ++i) top = max_nan(top, top_of(h[i]));
         top = reduce.max(top, odd, 2);
       }
-      const float sc = scale_of(top), f = one_over(sc);
+      const float sc = scale_of(top);
+      const Divisor v = by(sc);
       if (sp.tid == 0) scales[0] = sc;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (sp.has(i)) store_e4m3<E>(y, sp.column(i), qv, h[i], f);
-      if (sp.has_edge()) y[sp.edge] = static_cast<uint8_t>(e4m3x4(e * f, 0.f, 0.f, 0.f));
+        if (sp.has(i)) store_e4m3<E>(y, sp.column(i), qv, h[i], v);
+      if (sp.has_edge()) y[sp.edge] = e4m3(quotient(e, v));
     } else if (kAligned && g.group <= 32 * E) {
       // a group is some neighbouring lanes' pieces
       const int lanes = g.group / E;
@@ -558,7 +596,7 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024, kWarp ? (C > 8 ? 3 : 4) : 
         const float sc = scale_of(top);
         if (!sp.has(i)) continue;
         if ((lane & (lanes - 1)) == 0) scales[sp.column(i) >> shift] = sc;
-        store_e4m3<E>(y, sp.column(i), qv, h[i], one_over(sc));
+        store_e4m3<E>(y, sp.column(i), qv, h[i], by(sc));
       }
     } else {
       // A piece meets at most two groups, from column `cut` of it on the second. Magnitudes are ordered as whole
@@ -585,12 +623,9 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024, kWarp ? (C > 8 ? 3 : 4) : 
       for (int i = 0; i < NV; ++i) {
         if (!sp.has(i)) continue;
         const int c = sp.column(i), ga = c >> shift, gb = (c + E - 1) >> shift, cut = ga == gb ? E : (gb << shift) - c;
-        const float fa = one_over(scale_of(tops[ga])), fb = one_over(scale_of(tops[gb]));
-#pragma unroll
-        for (int k = 0; k < E / 2; ++k) h[i].p[k] = h[i].p[k] * two(2 * k < cut ? fa : fb, 2 * k + 1 < cut ? fa : fb);
-        store_e4m3<E>(y, c, qv, h[i], 1.f);
+        store_e4m3<E>(y, c, qv, h[i], by(scale_of(tops[ga])), by(scale_of(tops[gb])), cut);
       }
-      if (sp.has_edge()) y[sp.edge] = static_cast<uint8_t>(e4m3x4(e * one_over(scale_of(tops[sp.edge >> shift])), 0.f, 0.f, 0.f));
+      if (sp.has_edge()) y[sp.edge] = e4m3(quotient(e, by(scale_of(tops[sp.edge >> shift]))));
       for (int i = sp.tid; i < groups; i += sp.NT) scales[i] = scale_of(tops[i]);
       reduce.sync();  // before the next row's groups
     }
