@@ -89,6 +89,8 @@ Rows rows(const at::Tensor& t, const char* name, const Shape* want = nullptr, bo
   r.p = t.const_data_ptr();
   return r;
 }
+// One that is written to: memory that it shares with a lazy copy becomes its own.
+void* written(const at::Tensor& t) { return t.mutable_data_ptr(); }
 // A contiguous vector of n elements.
 const void* vector(const at::Tensor& t, const char* name, int64_t n, at::ScalarType type, int device) {
   if (t.scalar_type() != type) refuse_type(std::string(name) + " must be " + c10::toString(type) + ", got " + c10::toString(t.scalar_type()));
@@ -209,7 +211,7 @@ PyObject* py_rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor y = output(a[5], "y", {s.T, s.d}, x, quant ? at::kFloat8_e4m3fn : x.scalar_type());
     const Rows ry = rows(y, "y", &s, true);
     if (quant != (ry.code == P24_E4M3)) refuse_type("y is 8 bits with a group, and is not without one");
-    g.y_dtype = ry.code, g.y = const_cast<void*>(ry.p), g.ldy = ry.ld;
+    g.y_dtype = ry.code, g.y = written(y), g.ldy = ry.ld;
     at::Tensor h, scale;
     g.r_dtype = rx.code;
     if (a[2] != Py_None) {
@@ -218,17 +220,18 @@ PyObject* py_rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n) {
       h = output(a[6], "h", {s.T, s.d}, r, r.scalar_type());
       const Rows rh = rows(h, "h", &s);
       if (rh.code != rr.code) refuse_type("h must have the residual's type");
-      g.r_dtype = rr.code, g.r = rr.p, g.ldr = rr.ld, g.h = const_cast<void*>(rh.p), g.ldh = rh.ld;
+      g.r_dtype = rr.code, g.r = rr.p, g.ldr = rr.ld, g.h = written(h), g.ldh = rh.ld;
     }
     if (quant) {
       const Shape ss{s.T, groups_of(s.d, group), s.device};
       scale = output(a[7], "scale", {ss.T, ss.d}, x, at::kFloat);
       const Rows rs = rows(scale, "scale", &ss);
       if (rs.code != P24_F32) refuse_type("scale must be torch.float32");
-      g.scale = static_cast<float*>(const_cast<void*>(rs.p)), g.lds = rs.ld;
+      g.scale = static_cast<float*>(written(scale)), g.lds = rs.ld;
     }
     const at::Tensor rstd = output(a[8], "rstd", {s.T}, x, at::kFloat);
-    g.rstd = static_cast<float*>(const_cast<void*>(vector(rstd, "rstd", s.T, at::kFloat, s.device)));
+    vector(rstd, "rstd", s.T, at::kFloat, s.device);
+    g.rstd = static_cast<float*>(written(rstd));
     const int rc = p24_rmsnorm(&g, stream);
     return built(rc, {result(a[5], y), h.defined() ? result(a[6], h) : none(), scale.defined() ? result(a[7], scale) : none(),
                       result(a[8], rstd)});
@@ -254,7 +257,7 @@ PyObject* py_rmsnorm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     g.rstd = static_cast<const float*>(vector(tensor(a[3], "rstd"), "rstd", s.T, at::kFloat, s.device));
     const at::Tensor dx = output(a[5], "dx", {s.T, s.d}, h, h.scalar_type());
     const Rows rx = rows(dx, "dx", &s);
-    g.r_dtype = g.dx_dtype = rx.code, g.dx = const_cast<void*>(rx.p), g.lddx = rx.ld;
+    g.r_dtype = g.dx_dtype = rx.code, g.dx = written(dx), g.lddx = rx.ld;
     if (a[4] != Py_None) {
       const Rows rr = rows(tensor(a[4], "dres"), "dres", &s);
       g.r_dtype = rr.code, g.dres = rr.p, g.ldres = rr.ld;
@@ -263,7 +266,8 @@ PyObject* py_rmsnorm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Scratch ws;
     if (a[6] != Py_False) {
       dw = output(a[6], "dweight", {s.d}, h, at::kFloat);
-      g.dw = static_cast<float*>(const_cast<void*>(vector(dw, "dweight", s.d, at::kFloat, s.device)));
+      vector(dw, "dweight", s.d, at::kFloat, s.device);
+      g.dw = static_cast<float*>(written(dw));
       ws = scratch(a[7], p24_rmsnorm_bwd_workspace_size(s.T, s.d), h);
     }
     const int rc = p24_rmsnorm_bwd(&g, ws.p, ws.bytes, stream);
@@ -286,7 +290,7 @@ PyObject* py_dequant8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Rows rs = rows(tensor(a[1], "scale"), "scale", &ss);
     if (rs.code != P24_F32) refuse_type("scale must be torch.float32");
     const p24_dequant8_args g{s.T, s.d, ry.code, group_of(group), rq.p, rq.ld, static_cast<const float*>(rs.p), rs.ld,
-                              const_cast<void*>(ry.p), ry.ld};
+                              written(y), ry.ld};
     const int rc = p24_dequant8(&g, stream);
     return built(rc, {result(a[3], y)});
   });
@@ -304,7 +308,7 @@ PyObject* py_embed(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor y = output(a[3], "out", {s.T, s.d}, W, W.scalar_type());
     const Rows ry = rows(y, "out", &s);
     const p24_embed_args g{s.T, rw.T, s.d, rw.code, ry.code, number(a[2], "scale"), static_cast<const int32_t*>(t), rw.p, rw.ld,
-                           const_cast<void*>(ry.p), ry.ld};
+                           written(y), ry.ld};
     const int rc = p24_embed(&g, stream);
     return built(rc, {result(a[3], y)});
   });
@@ -325,7 +329,7 @@ PyObject* py_embed_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Rows rw = V < 1 ? Rows{} : rows(dW, "dW", &sw);
     const Scratch ws = scratch(a[6], p24_embed_bwd_workspace_size(ry.T, ry.d), dY);
     const p24_embed_bwd_args g{ry.T, V, ry.d, ry.code, rw.code, number(a[3], "scale"), accumulate ? 1 : 0,
-                               static_cast<const int32_t*>(t), ry.p, ry.ld, const_cast<void*>(rw.p), rw.ld};
+                               static_cast<const int32_t*>(t), ry.p, ry.ld, V < 1 ? nullptr : written(dW), rw.ld};
     const int rc = p24_embed_bwd(&g, ws.p, ws.bytes, stream);
     return built(rc, {result(a[4], dW)});
   });
@@ -338,7 +342,7 @@ struct List {
   std::vector<p24_tensor> v;
   int device = -1;
   at::Tensor first;
-  List(PyObject* o, const char* name) : seq(PySequence_Fast(o, "")) {
+  List(PyObject* o, const char* name, bool write) : seq(PySequence_Fast(o, "")) {
     if (!seq) {
       PyErr_Clear();
       refuse_type(std::string(name) + " must be a list of tensors");
@@ -356,7 +360,7 @@ struct List {
         }
         if (cuda_index(t) != device || !t.is_non_overlapping_and_dense())
           refuse_value(std::string(name) + " must be dense tensors on " + device_name(device));
-        v.push_back(p24_tensor{const_cast<void*>(t.const_data_ptr()), t.numel(), code});
+        v.push_back(p24_tensor{write ? written(t) : const_cast<void*>(t.const_data_ptr()), t.numel(), code});
       }
     } catch (...) {
       Py_DECREF(seq);
@@ -397,11 +401,12 @@ void require_apart(const std::vector<p24_tensor>& g, const std::vector<p24_tenso
 // (gradients, out or None, max_norm or None for the norm alone, norm, workspace) -> (status, norm)
 PyObject* py_grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return call("grads", n, 5, [&] {
-    const List g(a[0], "gradients");
+    const List g(a[0], "gradients", a[2] != Py_None && a[1] == Py_None);
     if (g.v.empty()) refuse_value("an empty list has no device to run on");
     void* stream = stream_on(g.device);
     const at::Tensor norm = output(a[3], "norm", {1}, g.first, at::kFloat);
-    float* pn = static_cast<float*>(const_cast<void*>(vector(norm, "norm", 1, at::kFloat, g.device)));
+    vector(norm, "norm", 1, at::kFloat, g.device);
+    float* pn = static_cast<float*>(written(norm));
     const int64_t count = static_cast<int64_t>(g.v.size());
     const Scratch ws = scratch(a[4], p24_grad_norm_workspace_size(count), g.first);
     int rc;
@@ -411,7 +416,7 @@ PyObject* py_grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
       require_apart(g.v, g.v);
       rc = p24_clip_grads(g.v.data(), nullptr, count, number(a[2], "max_norm"), pn, ws.p, ws.bytes, stream);
     } else {
-      const List out(a[1], "out");
+      const List out(a[1], "out", true);
       if (out.v.size() != g.v.size())
         refuse_value(std::to_string(count) + " gradients, and " + std::to_string(out.v.size()) + " tensors to write to");
       if (out.device != g.device) refuse_value("out must be dense tensors on " + device_name(g.device));
