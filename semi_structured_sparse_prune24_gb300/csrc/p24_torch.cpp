@@ -154,6 +154,14 @@ float number(PyObject* o, const char* name) {
   }
   return static_cast<float>(v);
 }
+bool truth(PyObject* o, const char* name) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {
+    PyErr_Clear();
+    refuse_type(std::string(name) + " must be true or false");
+  }
+  return v == 1;
+}
 int32_t group_of(int64_t g) { return g < 0 || g > 256 ? -1 : static_cast<int32_t>(g); }  // the library refuses what is left
 int64_t groups_of(int64_t d, int64_t group) { return group > 0 ? (d + group - 1) / group : 1; }
 
@@ -317,12 +325,12 @@ PyObject* py_embed(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // (dY, tokens, V, scale, dW, accumulate, workspace) -> (status, dW)
 PyObject* py_embed_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return call("embed_bwd", n, 7, [&] {
+    const bool accumulate = truth(a[5], "accumulate");
     const at::Tensor& dY = tensor(a[0], "dY");
     const Rows ry = rows(dY, "dY");
     void* stream = stream_on(ry.device);
     const void* t = vector(tensor(a[1], "tokens"), "tokens", ry.T, at::kInt, ry.device);
     const int64_t V = whole(a[2], "V");
-    const bool accumulate = PyObject_IsTrue(a[5]) == 1;
     if (accumulate && a[4] == Py_None) refuse_value("accumulate needs the dW to add to");
     const Shape sw{V, ry.d, ry.device};
     const at::Tensor dW = a[4] == Py_None && V < 1 ? dY : output(a[4], "dW", {V, ry.d}, dY, dY.scalar_type());
