@@ -5,7 +5,8 @@ to the C ABI (those of the calls around the FFN through csrc/p24_torch.cpp) and
 runs on the current torch CUDA stream; all arithmetic happens in the library's
 CUDA kernels. Output tensors the caller does not pass are
 allocated with torch (device memory is torch's job here). There is no CPU path:
-if the shared libraries are missing, importing this module raises.
+if libprune24 is missing, importing this module raises; if the marshalling of the
+calls around the FFN is, or was built for another torch, those calls raise.
 """
 from __future__ import annotations
 
@@ -186,11 +187,27 @@ def _load_marshal():
     loader = importlib.machinery.ExtensionFileLoader("_p24_torch", path)
     module = importlib.util.module_from_spec(importlib.machinery.ModuleSpec("_p24_torch", loader, origin=path))
     loader.exec_module(module)
+    if module.torch_version != torch.__version__:
+        raise ImportError(f"the tensors' marshalling was built for torch {module.torch_version}, this is {torch.__version__}: "
+                          "run __graft_entry__.build() or python semi_structured_sparse_prune24_gb300/build.py")
     return module
 
 
+class _Unavailable:
+    """Stands for the marshalling where it does not load: the calls that need it say why, the others go on."""
+
+    def __init__(self, why: Exception):
+        self._why = str(why)
+
+    def __getattr__(self, name):
+        raise ImportError(f"the calls around the FFN are not available: {self._why}")
+
+
 lib = _load()
-_marshal = _load_marshal()  # uses the library that has just been loaded
+try:
+    _marshal = _load_marshal()  # uses the library that has just been loaded
+except ImportError as e:
+    _marshal = _Unavailable(e)
 
 
 def _check(code: int, where: str) -> None:

@@ -3,13 +3,13 @@
 Each .cu under csrc/ is compiled in parallel to an object file under _build/,
 then all are linked into semi_structured_sparse_prune24_gb300/_lib/libprune24.so.
 csrc/p24_torch.cpp, the binding's marshalling of torch tensors, is compiled beside them
-(with torch's headers) and linked into _lib/_p24_torch.so, which uses libprune24.so.
+(with torch's headers) and linked into _lib/_p24_torch.so, which uses libprune24.so; where that
+fails libprune24.so is there all the same, and the build says so.
 Nothing is installed outside the repository. Run: python semi_structured_sparse_prune24_gb300/build.py
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
-import importlib.util
 import os
 import shutil
 import subprocess
@@ -60,30 +60,33 @@ def _compile(nvcc: str, src: str) -> str:
 MARSHAL = os.path.join(LIBDIR, "_p24_torch.so")
 
 
-def _torch_dir() -> str:
-    return os.path.dirname(importlib.util.find_spec("torch").origin)  # without importing it
-
-
 def _compile_marshal(nvcc: str) -> str:
-    inc = os.path.join(_torch_dir(), "include")
+    import torch  # while the kernels are compiled: which ABI it has, and where it is
+
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
     obj = os.path.join(BUILD, "p24_torch.o")
-    _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++20", "-fPIC", "-D_GLIBCXX_USE_CXX11_ABI=1", f"-I{INCLUDE}", f"-I{inc}",
+    _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", f"-DP24_TORCH_VERSION=\"{torch.__version__}\"",
+          f"-I{INCLUDE}", f"-I{inc}",
           f"-I{os.path.join(inc, 'torch', 'csrc', 'api', 'include')}", f"-I{cuda}", f"-I{sysconfig.get_paths()['include']}",
           "-c", os.path.join(CSRC, "p24_torch.cpp"), "-o", obj], "the host compiler failed on p24_torch.cpp")
     return obj
 
 
 def _link_marshal(obj: str) -> None:
-    lib = os.path.join(_torch_dir(), "lib")
+    import torch
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = MARSHAL + ".tmp"
     _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, f"-L{LIBDIR}", "-lprune24", f"-L{lib}", "-ltorch_python",
-          "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"], "link failed")
+          "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"], "link of p24_torch failed")
     os.replace(tmp, MARSHAL)
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every CUDA source for sm_103a and link the shared library. Returns its path."""
+    """Compile every CUDA source for sm_103a and link the shared library, then the binding's marshalling. Returns the
+    library's path. Raises where either fails; the library does not need the marshalling."""
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
@@ -91,14 +94,15 @@ def build(verbose: bool = False) -> str:
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
         marshal = ex.submit(_compile_marshal, nvcc)
         objs = list(ex.map(lambda s: _compile(nvcc, s), srcs))
-        marshal = marshal.result()
     libdir = _cuda_lib_dir(nvcc)
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs,
            f"-L{libdir}", "-Xlinker", f"-rpath={libdir}", "-Xlinker", "-soname=libprune24.so"]
     _run(cmd, "link failed")
     os.replace(tmp, LIB)
-    _link_marshal(marshal)
+    if os.path.exists(MARSHAL):
+        os.remove(MARSHAL)  # of another build: not to be used if this one fails
+    _link_marshal(marshal.result())
     if verbose:
         print(f"built {LIB}")
     return LIB

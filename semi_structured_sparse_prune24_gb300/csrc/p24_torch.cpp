@@ -453,4 +453,8 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_p24_torch", "Marshalling of torch
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__p24_torch() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__p24_torch() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "torch_version", P24_TORCH_VERSION) < 0) Py_CLEAR(m);
+  return m;
+}
