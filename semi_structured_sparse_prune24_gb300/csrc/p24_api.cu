@@ -8,8 +8,10 @@
 #include <cstdint>
 #include <cstring>
 #include <initializer_list>
+#include <new>
 
 #include "p24_internal.h"
+#include "slot_table.h"
 
 namespace p24 {
 namespace {
@@ -135,24 +137,14 @@ int sm_count() {
 }
 
 cudaError_t row_kernel_slots(const void* kern, int NT, int ranks, size_t smem, int* slots) {
-  struct Known {
-    const void* kern;
-    size_t smem;
-    int dev, NT, ranks, slots;
-  };
-  constexpr int kKnown = 256;  // more than that are looked up every time
   static std::mutex lock;
-  static Known known[kKnown];
-  static int n = 0;
+  static SlotTable* const known = new (std::nothrow) SlotTable;  // not taken down while threads still launch
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const std::lock_guard<std::mutex> hold(lock);
-  for (int i = 0; i < n; ++i)
-    if (known[i].kern == kern && known[i].NT == NT && known[i].ranks == ranks && known[i].smem == smem && known[i].dev == dev) {
-      *slots = known[i].slots;
-      return cudaSuccess;
-    }
+  const SlotKey key{kern, smem, dev, NT, ranks};
+  if (known && (*slots = known->find(key)) != 0) return cudaSuccess;
   cudaFuncAttributes fa;
   int most = 0;
   if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
@@ -179,7 +171,7 @@ cudaError_t row_kernel_slots(const void* kern, int NT, int ranks, size_t smem, i
   }
   if (e != cudaSuccess) return e;
   if (found < 1) return cudaErrorInvalidConfiguration;
-  if (n < kKnown) known[n++] = Known{kern, smem, dev, NT, ranks, found};
+  if (known) known->put(key, found);
   *slots = found;
   return cudaSuccess;
 }
