@@ -1,12 +1,6 @@
 // stream_rows.cuh -- what the kernels on rows of hidden states share (RMS norm, embedding, gradient
-// norm): pieces of 8 elements in fp32, loads and stores of them at any alignment, and reductions
-// over a CTA in a fixed order.
-//
-// A row of d elements is walked in pieces of 8 columns, piece j from column 8 j - s on, where s is
-// the row's phase: how many elements it starts past a 16-byte boundary (of bf16; 32 of fp32). Rows
-// of one matrix differ in it where the stride is not a multiple of 8. A tensor whose pieces lie on
-// 16-byte boundaries is read and written 16 bytes at a time, another one, and the pieces that hang
-// over a row's ends, element by element.
+// norm): fp32 in pairs, a thread's columns of a row and loads and stores of them (embedding), stores of 8
+// neighbouring columns (dequantisation), and reductions over a CTA in a fixed order.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -56,25 +50,10 @@ struct Raw8 {
   uint4 q[sizeof(T) / 2];
 };
 
-// Two bf16 of a register, and eight elements, as fp32.
+// Two bf16 of a register as fp32.
 __device__ __forceinline__ void widen(uint32_t w, float& a, float& b) {
   a = __uint_as_float(w << 16);
   b = __uint_as_float(w & 0xffff0000u);
-}
-__device__ __forceinline__ void unpack8(const Raw8<bf16>& r, float (&v)[8]) {
-  widen(r.q[0].x, v[0], v[1]);
-  widen(r.q[0].y, v[2], v[3]);
-  widen(r.q[0].z, v[4], v[5]);
-  widen(r.q[0].w, v[6], v[7]);
-}
-__device__ __forceinline__ void unpack8(const Raw8<float>& r, float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    v[4 * i] = __uint_as_float(r.q[i].x);
-    v[4 * i + 1] = __uint_as_float(r.q[i].y);
-    v[4 * i + 2] = __uint_as_float(r.q[i].z);
-    v[4 * i + 3] = __uint_as_float(r.q[i].w);
-  }
 }
 __device__ __forceinline__ void pack8(Raw8<bf16>& r, const float (&v)[8]) {
   r.q[0] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
@@ -89,37 +68,7 @@ __device__ __forceinline__ void pack8(Raw8<float>& r, const float (&v)[8]) {
 __device__ __forceinline__ uint32_t bits_of(bf16 x) { return __bfloat16_as_ushort(x); }
 __device__ __forceinline__ uint32_t bits_of(float x) { return __float_as_uint(x); }
 
-// Element i of a piece, put into it (the others are 0 or already there).
-__device__ __forceinline__ void put(Raw8<bf16>& r, int i, bf16 x) {
-  const uint32_t b = bits_of(x) << (16 * (i & 1));
-  uint32_t* w = reinterpret_cast<uint32_t*>(r.q);
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (k == i / 2) w[k] |= b;
-}
-__device__ __forceinline__ void put(Raw8<float>& r, int i, float x) {
-  uint32_t* w = reinterpret_cast<uint32_t*>(r.q);
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    if (k == i) w[k] = __float_as_uint(x);
-}
-
-// Columns [c, c + 8) of a row of d columns; those outside it are 0. `vec`: the row's pieces are aligned.
-template <typename T>
-__device__ __forceinline__ Raw8<T> load8(const T* row, int c, int d, bool vec) {
-  Raw8<T> r;
-  if (vec && c >= 0 && c + 8 <= d) {
-#pragma unroll
-    for (unsigned i = 0; i < sizeof(T) / 2; ++i) r.q[i] = reinterpret_cast<const uint4*>(row + c)[i];
-  } else {
-#pragma unroll
-    for (unsigned i = 0; i < sizeof(T) / 2; ++i) r.q[i] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i >= 0 && c + i < d) put(r, i, row[c + i]);
-  }
-  return r;
-}
+// Columns [c, c + 8) of a row of d columns, without those outside it. `vec`: pieces lie on 16-byte boundaries.
 template <typename T>
 __device__ __forceinline__ void store8(T* row, int c, int d, bool vec, const float (&v)[8]) {
   if (vec && c >= 0 && c + 8 <= d) {
@@ -147,10 +96,6 @@ struct Columns {
 // E elements in one access.
 template <int bytes>
 struct Word;
-template <>
-struct Word<2> { using type = uint16_t; };
-template <>
-struct Word<4> { using type = uint32_t; };
 template <>
 struct Word<8> { using type = uint2; };
 template <>
@@ -247,10 +192,9 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-template <int kLanes = 32>
 __device__ __forceinline__ float lanes_max(float x) {
 #pragma unroll
-  for (int i = kLanes / 2; i; i >>= 1) x = max_nan(x, __shfl_xor_sync(~0u, x, i));
+  for (int i = 16; i; i >>= 1) x = max_nan(x, __shfl_xor_sync(~0u, x, i));
   return x;
 }
 
@@ -285,10 +229,9 @@ inline RowThreads row_threads(int64_t d, int most) {
 }
 inline bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline int size_of(int32_t dtype) { return dtype == P24_BF16 ? 2 : dtype == P24_F32 ? 4 : 1; }
-// Whether every row's pieces at phase 0 are on 16-byte boundaries (8 for 8-bit elements).
+// Whether every row of bf16 or fp32 starts on a 16-byte boundary.
 inline bool rows_aligned(const void* p, int64_t ld, int32_t dtype) {
-  const unsigned unit = dtype == P24_E4M3 ? 8 : 16;
-  return !p || ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld * size_of(dtype))) & (unit - 1)) == 0;
+  return !p || ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld * size_of(dtype))) & 15u) == 0;
 }
 
 }  // namespace
