@@ -656,9 +656,9 @@ int p24_distill_topk_bwd(const p24_distill_args* a, void* stream);
  *   w    : [d], w_dtype, or NULL (all ones).
  *   y    : [T, d], y_dtype; it may be x or r itself, where h is elsewhere and they have one type.
  *          With P24_E4M3 codes of 8 bits (4 of exponent, 3 of fraction, largest 448), with
- *   scale: fp32 [T, ceil(d / group)], row stride lds: the group's largest magnitude / 448 (1 for a group of
- *          zeros, and no less than 2^-118); y = code * scale. A code is h rstd w / scale, in fp32 up to there,
- *          rounded to nearest even. The scale of a whole row comes from the largest |h w|, times rstd.
+ *   scale: fp32 [T, ceil(d / group)], row stride lds: the group's largest magnitude times fp32's 1 / 448 (1 for
+ *          a group of zeros, and no less than 2^-118); y = code * scale. A code is h rstd w / scale, in fp32 up to
+ *          there, rounded to nearest even. The scale of a whole row comes from the largest |h w|, times rstd.
  *          group is 32, 64, 128 or 256 columns, or 0 for whole rows.
  *   rstd : fp32 [T], or NULL. The backward reads it.
  * A row with a NaN is NaN; of a row with an infinity the infinity gives NaN and the rest 0. Squares

@@ -347,17 +347,15 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3) |
          static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3)) << 16;
 }
-// A scale from the largest magnitude: a 448th of it, rounded once (the product with 1/448 and one step of refinement
-// give that for each of the 2^23 fractions), and no less than 2^-118, below which its reciprocal leaves fp32's range.
-__device__ __forceinline__ float scale_of(float top) {
-  if (top == 0.f) return 1.f;
-  const float s = top * (1.f / 448.f);
-  return max_nan(s < __int_as_float(0x7f800000) ? fmaf(fmaf(s, -448.f, top), 1.f / 448.f, s) : s, 0x1p-118f);
-}
+// A scale from the largest magnitude: its product with fp32's 1/448, two units in the last place from the quotient at most
+// (any scale near it would do: codes are those of the quotients by the stored one), and no less than 2^-118, below which
+// its reciprocal leaves fp32's range.
+__device__ __forceinline__ float scale_of(float top) { return top == 0.f ? 1.f : max_nan(top * (1.f / 448.f), 0x1p-118f); }
 // What values are divided by, a scale. A quotient is the value times an approximate reciprocal, off by some units in the
 // last place, and a step of refinement: the remainder is exact or off by 2^-22 of such a unit, so what is rounded in the end
 // is within 2^-20 units of the true quotient, and exactly it where the quotient has few bits, as the midpoint of two codes
-// has. (The product alone is one of the neighbours of a midpoint as often as not.) Values come with their sign turned, which
+// has. (The product alone is one of the neighbours of a midpoint as often as not; with it 16384 x 4096 bf16 took 53 us with a
+// row's scale, like this 59.) Values come with their sign turned, which
 // keeps that of zeros. Beside a scale below 2^-90 the remainder would lie among the smallest numbers: both are taken times
 // 2^64. An infinite scale gives 0, and for infinite values NaN; so does a scale that is NaN.
 struct Divisor {
@@ -1032,9 +1030,9 @@ cudaError_t grid_of(K kern, const Shape& z, int64_t T, int64_t most, int64_t* gr
 //     fp32 in aligned rows 8 (8192 x 4096 to fp32 35 and 39, x 8192 fp32 86 and 93; x 6290 to fp32 89 and 61)
 //   with a residual: 8 (16384 x 4096 81 and 90, x 768 15.3 and 17.6; x 8192 166 and 176), unless they leave the SM a
 //     quarter empty (8192 x 5001 70 and 60, beside an fp32 stream 94 and 83)
-//   8-bit codes, half as many instructions again: 16 (16384 x 4096 without a residual 73 and 53, with one 87 and 82),
-//     with a residual where a row is more than 1024 columns (x 1024 25 and 24, x 768 18.7 and 21.7), or beside an
-//     fp32 stream in unaligned rows of more than 4096 (8192 x 6290 129 and 107, x 8192 115 and 129)
+//   8-bit codes, half as many instructions again: 16 (16384 x 4096 without a residual 78 and 59, with one 91 and 75),
+//     with a residual where a row is more than 1024 columns (x 1024 26 and 25, x 768 19.9 and 22.6), or beside an
+//     fp32 stream in unaligned rows of more than 4096 (8192 x 6290 135 and 115, x 8192 117 and 134)
 //   the gradient: 8 (16384 x 4096 64 and 67, x 1024 22 and 28), 16 without a skip connection's in rows of more than 4096
 //     bf16 (8192 x 6290 84 and 70; fp32 125 and 172)
 //   few rows: 8, for a row's time is a thread's
