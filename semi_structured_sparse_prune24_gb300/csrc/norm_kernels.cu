@@ -351,13 +351,13 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 // (any scale near it would do: codes are those of the quotients by the stored one), and no less than 2^-118, below which
 // its reciprocal leaves fp32's range.
 __device__ __forceinline__ float scale_of(float top) { return top == 0.f ? 1.f : max_nan(top * (1.f / 448.f), 0x1p-118f); }
-// What values are divided by, a scale. A quotient is the value times an approximate reciprocal, off by some units in the
-// last place, and a step of refinement: the remainder is exact or off by 2^-22 of such a unit, so what is rounded in the end
-// is within 2^-20 units of the true quotient, and exactly it where the quotient has few bits, as the midpoint of two codes
-// has. (The product alone is one of the neighbours of a midpoint as often as not; with it 16384 x 4096 bf16 took 53 us with a
-// row's scale, like this 59.) Values come with their sign turned, which
-// keeps that of zeros. Beside a scale below 2^-90 the remainder would lie among the smallest numbers: both are taken times
-// 2^64. An infinite scale gives 0, and for infinite values NaN; so does a scale that is NaN.
+// What values are divided by, a scale. A quotient is the value times an approximate reciprocal (2 units in the last place
+// off at most, the product then 5), and a step of refinement: the remainder is off by 2^-21 of such a unit and its product with
+// the reciprocal by 2^-20, so what is rounded in the end is within 2^-19 units of the true quotient. Where that is the
+// midpoint of two codes, a number of few bits, the rounding gives exactly it. (The product alone gives one of a midpoint's
+// neighbours as often as not; with it 16384 x 4096 bf16 took 53 us with a row's scale, like this 59.) Values come with their
+// sign turned, which keeps that of zeros. Beside a scale below 2^-90 the remainder would lie among the smallest numbers: both
+// are taken times 2^64. An infinite scale gives 0, and for infinite values NaN; so does a scale that is NaN.
 struct Divisor {
   float s, neg, up;  // the scale, which the remainder is found with; -1 / scale; 2^64 or 1
 };
